@@ -303,7 +303,8 @@ def _own_attend(s):
     from weight_activation_quantized_amd import mixllm as L
     if "ws" not in s:
         size = L.mixllm_kv4_attention_workspace_bytes(s["q"].shape[0], s["lens"].shape[0], s["q"].shape[1],
-                                                      s["cache"].shape[1], s["q"].shape[2], s["rows"], s["length"])
+                                                      s["cache"].shape[1], s["q"].shape[2], s["rows"], s["length"],
+                                                      s["window"])
         s["ws"] = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
     L.mixllm_kv4_attention(s["q"], s["cache"], s["table"], s["lens"], s["cu"], s["out"], s["page"], s["rows"],
                            s["length"], scale=s["scale"], window=s["window"], lse=s["lse"], workspace=s["ws"])
