@@ -56,6 +56,11 @@ typedef enum mixllm_status {
   MIXLLM_E_HIP = -7     /* the HIP runtime reported an error at launch */
 } mixllm_status;
 
+/* Element types of the calls that take more than fp16. */
+#define MIXLLM_FP16 0
+#define MIXLLM_BF16 1
+#define MIXLLM_FP32 2
+
 /* Host-side copy of the packed-blob header (the first 256 bytes of every blob). */
 typedef struct mixllm_blob_info {
   uint32_t magic, version;
@@ -250,6 +255,144 @@ int mixllm_gemm_w4w8a8_partials(const int8_t *aq_dev, const float *sa_dev, const
                                 const uint32_t *rowop_dev, int32_t M, int32_t N, int32_t K, int32_t n8,
                                 const mixllm_blob_info *blob_info, const void *blob_dev, size_t blob_bytes,
                                 int32_t n_begin, int32_t n_count, int32_t *p_dev, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * The norms around a block, fused with its gate, the residual sum and the quantization
+ * of the next layer's activations (device).
+ *
+ *   u  = x / rms(x) * post      (u = x when post is NULL)
+ *   h' = alpha * h + beta * gate * u   (gate 1 when NULL; h' = alpha * h when x is NULL)
+ *   y  = h' / rms(h') * pre,    rms(v) = sqrt(mean(v^2) + eps)
+ *
+ * All in fp32.  h' is rounded once to the residual's type, y (from the unrounded h') once
+ * to the type of x; the int8 outputs are mixllm_quant_act's for that y.
+ *
+ * x_dev:       [M][ldx] output of the block, or NULL (no block before: the first norm).
+ * post_dev, pre_dev: [N] norm weights; post NULL for no post norm; pre NULL for no second
+ *              norm (then no y and no int8 outputs).
+ * gate_dev:    [N] with ldgate = 0 (one gate per channel), [M][ldgate] (per token), or NULL.
+ * res_dev:     h, [M][ldr]; res_out_dev: h', [M][ldro], may be res_dev; NULL to skip.
+ * y_dev:       [M][ldy] or NULL.  aq, sa, asum, rowop: as mixllm_quant_act with K = N, aq
+ *              NULL for none; at least one of y and aq when pre is given.
+ * dtype:       MIXLLM_FP16 or MIXLLM_BF16: x, post, gate, pre, y.
+ * res_dtype:   dtype or MIXLLM_FP32: h and h'.
+ * N <= 65536; any N, stride and element-aligned pointer without the int8 outputs; 16-byte
+ * aligned rows (strides % 8 == 0) run faster.  With them N % 128 == 0, strides % 8 == 0
+ * and 16-byte aligned pointers.  eps >= 0.
+ * Errors: E_NULL, E_SHAPE, E_GROUP, E_HIP.
+ * ------------------------------------------------------------------------------------ */
+int mixllm_residual_norm(const void *x_dev, int64_t ldx, const void *post_dev, const void *gate_dev, int64_t ldgate,
+                         const void *res_dev, int64_t ldr, void *res_out_dev, int64_t ldro, const void *pre_dev,
+                         void *y_dev, int64_t ldy, int8_t *aq_dev, float *sa_dev, int32_t *asum_dev,
+                         uint32_t *rowop_dev, int32_t M, int32_t N, int32_t group, int32_t dtype, int32_t res_dtype,
+                         float eps, float alpha, float beta, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * The cache: keys and values of one attention layer in 4 bits, in pages.
+ *
+ * cache_dev holds `pages` pages of `page` tokens (a power of two, 16 to 1024), each page
+ * one block per key/value head, `dim` channels per head (64, 128 or 256).  64 channels of
+ * one token share an fp16 scale s and an fp16 minimum m; x is kept as m + s c, 0 <= c <= 15:
+ *   lo = min x, hi = max x;  m = fp16(lo);  s = fp16((hi - lo) / 15) (fp32 operations,
+ *   IEEE division; 2^-24 where that is 0 and hi > lo);
+ *   c = clamp(rne((x - m) / s), 0, 15) in fp32, 0 where s = 0.
+ * NaN counts as 0 and values beyond +-65504 as that, so what a cache holds is finite.
+ *
+ * A block of page p and head h starts at byte (p * heads + h) * page * dim * 9 / 8:
+ *   K codes (page * dim / 2 bytes): token t, quarter c (0..3), step s (0..dim/32-1): the
+ *     dword at t * dim/2 + c * dim/8 + 4 s holds channel 32 s + 8 c + j in nibble j;
+ *   V codes (page * dim / 2): token t, column n (0..15): the word of dim/32 bytes number
+ *     (t / 4 * 16 + n) * 4 + t % 4 holds channel 16 j + n in nibble j;
+ *   K params (page * dim / 16): per token dim/64 fp16 scales, then dim/64 fp16 minima;
+ *   V params (page * dim / 16): the same.
+ * A token's slot is page number * page + place in the page; a negative slot or one past the
+ * cache stands for no token.  Page tables are int32 [B][ldt], entry j of a request's row
+ * the page of its tokens j * page ..; entries past its length are not read, and tokens on
+ * a page number outside [0, pages) count as absent.  int32 arrays need 4-byte alignment.
+ * ------------------------------------------------------------------------------------ */
+
+/* Bytes of one page over all heads, or 0 if the parameters are invalid. */
+size_t mixllm_kv4_page_bytes(int32_t page, int32_t heads, int32_t dim);
+
+/*
+ * Plan of one step (device): page tables and slot maps from request lengths.
+ *
+ * fresh_dev:   [B] tokens to add to each request this step; negative: the request ended.
+ * lens_dev:    [B] tokens each request holds.
+ * table_dev:   [B][ldt] pages of each request (the first `width` of a row are used), in place.
+ * pool_dev:    [F] free pages, the first *count_dev of them valid, in place.
+ * lens_out_dev: [B] tokens held after the step (may be lens_dev): the sum, 0 for a request
+ *              that ended, unchanged for one that is refused.
+ * count_out_dev: [2] free pages after the step (may be count_dev, if that has 2 entries),
+ *              and the number of refused requests.
+ * cu_dev:      [B + 1] exclusive prefix sums of the tokens added (refused ones among them):
+ *              the rows of request b are cu[b] .. cu[b+1]-1.
+ * slots_dev, pos_dev: [tokens] slot and position of every row; -1 and 0 behind the last
+ *              row; slot -1 for rows of refused requests, and where the table or pool hold
+ *              a page outside [0, pages) (for all rows of the request, if its first is).
+ * Pages of ended requests are put on top of the free ones in the order of the requests
+ * (those past F are dropped; the rows keep their entries); new pages are then taken from
+ * the top in the order of the requests.  A request is refused if it would grow past
+ * width * page tokens, or if it needs pages and those needed up to and including it exceed
+ * the free ones.  Lengths outside [0, width * page] are taken as the nearest bound.
+ * One launch up to 4096 rows of `tokens`, two above.  Errors: E_NULL, E_SHAPE, E_HIP.
+ */
+int mixllm_kv_plan(const int32_t *fresh_dev, const int32_t *lens_dev, int32_t B, int32_t *table_dev, int64_t ldt,
+                   int32_t width, int32_t *pool_dev, int32_t F, const int32_t *count_dev, int32_t page, int32_t pages,
+                   int32_t *lens_out_dev, int32_t *count_out_dev, int32_t *cu_dev, int32_t *slots_dev,
+                   int32_t *pos_dev, int32_t tokens, void *stream);
+
+/*
+ * Quantizes the keys and values of T rows and writes them to their slots (device).
+ * k_dev, v_dev: [T][ldk], [T][ldv] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head h of a row at
+ *               h * dim; strides >= heads * dim and % 8 == 0, so slices of one GEMM output do.
+ * slots_dev:    [T]; rows without a slot are skipped, everything else in the cache is left
+ *               as it was.  Two rows with one slot leave that token unspecified (no other).
+ * Errors: E_NULL, E_SHAPE, E_SPACE (cache_bytes < pages * mixllm_kv4_page_bytes), E_HIP.
+ */
+int mixllm_kv4_append(const void *k_dev, int64_t ldk, const void *v_dev, int64_t ldv, int32_t dtype,
+                      const int32_t *slots_dev, int32_t T, void *cache_dev, size_t cache_bytes, int32_t pages,
+                      int32_t page, int32_t heads, int32_t dim, void *stream);
+
+/*
+ * The way back: the values m + s c of the tokens at T slots, rounded to dtype (device).
+ * Rows without a slot are left as they were.  Arguments and errors as mixllm_kv4_append.
+ */
+int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, int32_t page, int32_t heads,
+                    int32_t dim, const int32_t *slots_dev, int32_t T, void *k_dev, int64_t ldk, void *v_dev,
+                    int64_t ldv, int32_t dtype, void *stream);
+
+/*
+ * Attention over the cache (device).  Row i of request b, 0 <= i < n_b = cu[b+1] - cu[b],
+ * has the position p = lens[b] - n_b + i (lens counts the tokens of these rows: append them
+ * first) and sees the tokens max(0, p - window + 1) .. p (window 0: all up to p).  With
+ * query head x on key/value head x / (q_heads / kv_heads):
+ *   S_t = scale * q . k_t;  out = sum_t softmax(S)_t v_t;  lse = log sum_t exp S_t.
+ * A row that sees nothing has out 0 and lse -inf.  Softmax statistics and sums are fp32, the
+ * products fp16 x 4-bit codes; out is rounded once to dtype.  Any finite q is taken.
+ *
+ * q_dev, out_dev: [T][ldq], [T][ldo] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head x of a row
+ *               at x * dim; strides >= q_heads * dim and % 8 == 0.
+ * table_dev, lens_dev, cu_dev: as mixllm_kv_plan leaves them (its lens_out).
+ * max_rows, max_len: bounds the caller promises for n_b and lens[b]; rows and tokens beyond
+ *               them are ignored.  They size the launch: keep them near the truth.
+ * Rows outside cu[0] .. cu[B]-1 of out and lse are left as they were.
+ * lse_dev:      fp32 [T][q_heads] or NULL.
+ * workspace_dev: mixllm_kv4_attention_workspace_bytes(..) for the same arguments (0: NULL is
+ *               taken); calls that may run at the same time, replays of graphs among them,
+ *               need a workspace each.
+ * One launch where one workgroup per 16 rows is enough, else two (the second joins).
+ * Errors: E_NULL, E_SHAPE, E_SPACE, E_HIP.
+ */
+size_t mixllm_kv4_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                            int32_t max_rows, int32_t max_len, int32_t window);
+
+int mixllm_kv4_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t T, int32_t q_heads,
+                         const void *cache_dev, size_t cache_bytes, int32_t pages, int32_t page, int32_t kv_heads,
+                         int32_t dim, const int32_t *table_dev, int64_t ldt, int32_t width, const int32_t *lens_dev,
+                         const int32_t *cu_dev, int32_t B, int32_t max_rows, int32_t max_len, float scale,
+                         int32_t window, void *out_dev, int64_t ldo, float *lse_dev, void *workspace_dev,
+                         size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -31,7 +31,8 @@ LIB = os.path.join(HERE, "libmixllm.so")
 
 VARIANTS = {"fold_bias": ("MIXLLM_FOLD_BIAS=1",), "zero_pre": ("MIXLLM_ZERO_PRE=1",)}
 
-SOURCES = ["mixllm_pack.cpp", "mixllm_assign.cpp", "mixllm_quant_act.hip", "mixllm_gemm.hip"]
+SOURCES = ["mixllm_pack.cpp", "mixllm_assign.cpp", "mixllm_quant_act.hip", "mixllm_gemm.hip",
+           "mixllm_norm.hip", "mixllm_kv4.hip", "mixllm_kv4_attention.hip"]
 ARCH = os.environ.get("MIXLLM_ARCH", "gfx950")
 
 

@@ -61,7 +61,7 @@ class BlobInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
-_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "mixllm_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "mixllm_packed_bytes": ([_i32, _i32, _i32, _i32], _sz),
@@ -77,6 +77,17 @@ _SIGS = {
                             _vp], ctypes.c_int),
     "mixllm_gemm_w4w8a8_partials": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _sz, _i32, _i32,
                                      _vp, _vp], ctypes.c_int),
+    "mixllm_residual_norm": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
+                              _i32, _i32, _i32, _i32, _f32, _f32, _f32, _vp], ctypes.c_int),
+    "mixllm_kv4_page_bytes": ([_i32, _i32, _i32], _sz),
+    "mixllm_kv_plan": ([_vp, _vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
+                        _vp], ctypes.c_int),
+    "mixllm_kv4_append": ([_vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _sz, _i32, _i32, _i32, _i32, _vp],
+                          ctypes.c_int),
+    "mixllm_kv4_read": ([_vp, _sz, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp], ctypes.c_int),
+    "mixllm_kv4_attention_workspace_bytes": ([_i32] * 8, _sz),
+    "mixllm_kv4_attention": ([_vp, _i64, _i32, _i32, _i32, _vp, _sz, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _vp,
+                              _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
 }
 def _bind(lib):
     for name, (args, res) in _SIGS.items():
@@ -344,6 +355,213 @@ def mixllm_gemm_w4w8a8_partials(aq, sa, asum, rowop, m: int, n: int, k: int, n8:
     _check((lib or _lib).mixllm_gemm_w4w8a8_partials(_ptr(aq), _ptr(sa), _ptr(asum), _ptr(rowop), m, n, k, n8,
                                                      ctypes.byref(b.info), _ptr(b.dev), b.nbytes, n_begin,
                                                      n_count, _ptr(part), _stream(stream)))
+
+
+# ------------------------------------------------------------- between the packed layers
+
+FP16, BF16, FP32 = 0, 1, 2  # MIXLLM_FP16, MIXLLM_BF16, MIXLLM_FP32
+
+
+def _type16(t, name):
+    """The library's number of a 16-bit element type."""
+    if t.dtype is torch.float16:
+        return FP16
+    if t.dtype is torch.bfloat16:
+        return BF16
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+
+
+def _rows(t, name, dtype, shape):
+    """The row stride of a [M, N] (or [M, heads, dim]) CUDA tensor with contiguous rows."""
+    if not t.is_cuda or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if len(shape) == 2:
+        width = shape[1]
+        whole = st[1] == 1 or width == 1
+    else:
+        width = shape[1] * shape[2]
+        whole = st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
+    if not whole:
+        raise ValueError(f"{name} must have contiguous rows")
+    if shape[0] <= 1:
+        return (width + 7) // 8 * 8
+    if st[0] < width:
+        raise ValueError(f"the rows of {name} overlap")
+    return st[0]
+
+
+def _ints(t, name, numel):
+    """An int32 CUDA tensor, contiguous, of at least `numel` elements."""
+    if not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of at least {numel} elements")
+    return t
+
+
+def _launch(fn, tensors, stream, *args):
+    """Calls a device entry point with the stream last, on the device of its tensors."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"the tensors are on different devices: {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=None, asum=None, rowop=None,
+                         post_weight=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-5,
+                         stream=None):
+    """h' = alpha res + beta gate * norm(x; post_weight), y = norm(h'; pre_weight).  x: [M, N]
+    fp16 or bf16 (None: no block before); res, res_out: [M, N] of that type or fp32 (res_out
+    may be res); gate: [N], [M, N] or None; y: [M, N] in 16 bits; aq, sa, asum, rowop as
+    mixllm_quant_act's outputs for y."""
+    lead = x if x is not None else pre_weight
+    if lead is None:
+        raise ValueError("x or pre_weight is required")
+    dtype = _type16(lead, "x" if x is not None else "pre_weight")
+    shape = res.shape
+    if len(shape) != 2:
+        raise ValueError("res must be 2-D")
+    m, n = shape
+    t16 = lead.dtype
+    res_dtype = FP32 if res.dtype is torch.float32 else dtype
+    ldr = _rows(res, "res", torch.float32 if res_dtype == FP32 else t16, shape)
+    ldx = _rows(x, "x", t16, shape) if x is not None else 0
+    ldro = _rows(res_out, "res_out", res.dtype, shape) if res_out is not None else 0
+    ldy = _rows(y, "y", t16, shape) if y is not None else 0
+    ldgate = 0
+    if gate is not None:
+        if gate.dim() == 2:
+            ldgate = _rows(gate, "gate", t16, shape)
+        else:
+            _rows(gate.view(1, -1), "gate", t16, (1, n))
+    for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if w is not None and (not w.is_cuda or w.dtype is not t16 or w.shape != (n,) or w.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous [{n}] CUDA tensor of {t16}")
+    if aq is not None and m:
+        g = n // GROUP
+        _need(aq, "aq", torch.int8, (m, n))
+        _need(sa, "sa", torch.float32, (g, m))
+        if asum is not None:
+            _need(asum, "asum", torch.int32, (g, m))
+        if rowop is not None:
+            _need(rowop, "rowop", torch.int32, (g, m, 8))
+        if aq.shape != (m, n) or sa.shape != (g, m):
+            raise ValueError(f"aq and sa must be [{m}, {n}] and [{g}, {m}]")
+    _launch(_lib.mixllm_residual_norm, (res, x, res_out, pre_weight, post_weight, gate, y, aq, sa, asum, rowop), stream,
+            _at(x), ldx, _at(post_weight), _at(gate), ldgate, _at(res), ldr, _at(res_out), ldro, _at(pre_weight),
+            _at(y), ldy, _at(aq), _at(sa), _at(asum), _at(rowop), m, n, GROUP, dtype, res_dtype, eps, alpha, beta)
+
+
+def mixllm_kv4_page_bytes(page: int, heads: int, dim: int) -> int:
+    return int(_lib.mixllm_kv4_page_bytes(page, heads, dim))
+
+
+def kv4_cache(pages: int, page: int, heads: int, dim: int, device="cuda"):
+    """Storage of one layer's cache: uint8 [pages, heads, bytes of a (page, head) block]."""
+    size = mixllm_kv4_page_bytes(page, heads, dim)
+    if not size or pages <= 0:
+        raise ValueError("pages and heads must be positive, page a power of two of 16 .. 1024, dim 64, 128 or 256")
+    return torch.empty((pages, heads, size // heads), dtype=torch.uint8, device=device)
+
+
+def _cache(cache, page, dim):
+    """(bytes, pages, heads) of a cache tensor for pages of `page` tokens and heads of `dim` channels."""
+    if not cache.is_cuda or cache.dtype is not torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
+    pages, heads, block = cache.shape
+    if block * 8 != page * dim * 9:
+        raise ValueError(f"cache has blocks of {block} bytes, page {page} and dim {dim} need {page * dim * 9 / 8:g}")
+    return pages * heads * block, pages, heads
+
+
+def mixllm_kv_plan(fresh, lens, table, pool, count, page: int, pages: int, lens_out, count_out, cu, slots, pos,
+                   stream=None):
+    """The page tables and slot maps of a step from request lengths, on the GPU: fresh, lens,
+    lens_out: int32 [B]; table: int32 [B, width] (rows may be strided); pool: int32 [F]; count:
+    int32 [1 or more]; count_out: int32 [2]; cu: int32 [B + 1]; slots, pos: int32 [tokens]."""
+    b = fresh.shape[0]
+    if table.dim() != 2 or table.shape[0] != b or not table.is_cuda or table.dtype is not torch.int32 or (
+            table.numel() and table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be an int32 CUDA tensor [{b}, width] with contiguous rows")
+    width = table.shape[1]
+    for t, name, size in ((fresh, "fresh", b), (lens, "lens", b), (count, "count", 1), (lens_out, "lens_out", b),
+                          (count_out, "count_out", 2), (cu, "cu", b + 1), (pool, "pool", 0),
+                          (pos, "pos", slots.shape[0]), (slots, "slots", 0)):
+        _ints(t, name, size)
+    if b > 1 and table.stride(0) < width:
+        raise ValueError("the rows of table overlap")
+    _launch(_lib.mixllm_kv_plan, (fresh, lens, table, pool, count, lens_out, count_out, cu, slots, pos), stream,
+            fresh.data_ptr(), lens.data_ptr(), b, table.data_ptr(), table.stride(0) if b > 1 else width, width,
+            pool.data_ptr(), pool.numel(), count.data_ptr(), page, pages, lens_out.data_ptr(), count_out.data_ptr(),
+            cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), slots.shape[0])
+
+
+def mixllm_kv4_append(k, v, slots, cache, page: int, stream=None):
+    """Writes k and v ([T, heads, dim] fp16 or bf16, rows may be strided) into the cache at
+    slots (int32 [T], negative: skip the row)."""
+    t, _, dim = k.shape
+    size, pages, heads = _cache(cache, page, dim)
+    dtype, shape = _type16(k, "k"), (t, heads, dim)
+    ldk, ldv = _rows(k, "k", k.dtype, shape), _rows(v, "v", k.dtype, shape)
+    _ints(slots, "slots", t)
+    _launch(_lib.mixllm_kv4_append, (cache, k, v, slots), stream, k.data_ptr(), ldk, v.data_ptr(), ldv, dtype,
+            slots.data_ptr(), t, cache.data_ptr(), size, pages, page, heads, dim)
+
+
+def mixllm_kv4_read(cache, slots, k, v, page: int, stream=None):
+    """The values of the tokens at slots (int32 [T]) into k and v ([T, heads, dim] fp16 or
+    bf16); rows with a negative slot are left as they were."""
+    t, _, dim = k.shape
+    size, pages, heads = _cache(cache, page, dim)
+    dtype, shape = _type16(k, "k"), (t, heads, dim)
+    ldk, ldv = _rows(k, "k", k.dtype, shape), _rows(v, "v", k.dtype, shape)
+    _ints(slots, "slots", t)
+    _launch(_lib.mixllm_kv4_read, (cache, k, v, slots), stream, cache.data_ptr(), size, pages, page, heads, dim,
+            slots.data_ptr(), t, k.data_ptr(), ldk, v.data_ptr(), ldv, dtype)
+
+
+def mixllm_kv4_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
+                                         max_len: int, window: int = 0) -> int:
+    return int(_lib.mixllm_kv4_attention_workspace_bytes(t, b, q_heads, kv_heads, dim, max_rows, max_len, window))
+
+
+def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: int, max_len: int, scale=None,
+                         window: int = 0, lse=None, workspace=None, stream=None):
+    """Attention of the rows q ([T, q_heads, dim] fp16 or bf16) of B requests over the cache:
+    table: int32 [B, width]; lens: int32 [B] tokens cached (these rows' among them); cu: int32
+    [B + 1] first row of each request; out: as q; lse: fp32 [T, q_heads] or None; scale: 1 /
+    sqrt(dim) by default; workspace: a uint8 tensor of mixllm_kv4_attention_workspace_bytes(T,
+    B, ..) for the same arguments (None where that is 0)."""
+    t, hq, dim = q.shape
+    size, pages, heads = _cache(cache, page, dim)
+    dtype = _type16(q, "q")
+    ldq, ldo = _rows(q, "q", q.dtype, q.shape), _rows(out, "out", q.dtype, q.shape)
+    b = lens.shape[0]
+    if table.dim() != 2 or table.shape[0] < b or not table.is_cuda or table.dtype is not torch.int32 or (
+            table.numel() and table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be an int32 CUDA tensor [{b}, width] with contiguous rows")
+    _ints(lens, "lens", b)
+    _ints(cu, "cu", b + 1)
+    width = table.shape[1]
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (t, hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous fp32 tensor [{t}, {hq}]")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _launch(_lib.mixllm_kv4_attention, (q, cache, table, lens, cu, out, lse, workspace), stream, q.data_ptr(), ldq,
+            dtype, t, hq, cache.data_ptr(), size, pages, page, heads, dim, table.data_ptr(),
+            table.stride(0) if table.shape[0] > 1 else width, width, lens.data_ptr(), cu.data_ptr(), b, max_rows,
+            max_len, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo, _at(lse), _at(workspace), ws)
 
 
 def rowop_buffer(m: int, k: int, device="cuda"):
