@@ -361,7 +361,7 @@ def test_pages_that_do_not_exist_hide_their_tokens(L, length):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("vscale,qscale", [(1e-4, 1.0), (3000.0, 1.0), (1.0, 3e4), (1.0, 1e-6), ("rising", 1.0),
-                                           ("falling", 1.0), ("zeros", 0.0)])
+                                           ("falling", 1.0), ("zeros", 0.0), ("groups", 1.0)])
 def test_extreme_values(L, dtype, vscale, qscale):
     """Values tiny, huge or of changing size along the context, queries at the ends of the
     type, a maximum that keeps rising: the probabilities' fp16 operands must not lose it."""
@@ -376,6 +376,9 @@ def test_extreme_values(L, dtype, vscale, qscale):
         v *= (2.0 ** (-np.arange(n) / 60 + 8))[:, None, None]
     elif vscale == "zeros":
         v *= 0
+    elif vscale == "groups":     # the second group of channels far larger than the first
+        v[:, :, 64:] *= 2000.0
+        k[:, :, 64:] *= 0.01
     else:
         v *= vscale
     k, v = rounded(k.astype(np.float32), dtype), rounded(v.astype(np.float32), dtype)

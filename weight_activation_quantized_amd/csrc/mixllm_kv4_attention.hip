@@ -44,8 +44,8 @@ typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 32;         // tokens of one step of a wave
-constexpr int kRows = 16;         // query rows of a tile (token, head of the group)
+constexpr int kRun = 16;          // tokens of a run: a page holds it whole
+constexpr int kCols = 16;         // columns of a matrix operand
 constexpr float kLow = -1e38f;    // a running maximum before any score
 constexpr float kLazy = 6.0f;     // the maximum moves once a score is this far above it (log2)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -60,19 +60,20 @@ struct Args {
   int64_t ldq, ldo, ldt;
   float scale;
   int32_t T, hq, hkv, group, pages, page_log2, width, B, max_rows, max_len, window;
-  int32_t tiles, rows_tile;  // row tiles of a request and head, rows of a tile
+  int32_t tiles, tile_rows;  // row tiles of a request and head, rows of a full tile
   int32_t splits, chunk;     // workgroups along the tokens, tokens of each
-  int32_t bf16;
 };
 
-__device__ __forceinline__ float up(uint32_t bits, bool bf16) {
-  return bf16 ? __uint_as_float(bits << 16)
+template <bool BF16>
+__device__ __forceinline__ float up(uint32_t bits) {
+  return BF16 ? __uint_as_float(bits << 16)
               : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
 }
 
-__device__ __forceinline__ uint32_t down(float v, bool bf16) {
-  return bf16 ? (uint32_t)__builtin_bit_cast(uint16_t, static_cast<__bf16>(v))
-              : (uint32_t)__builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+template <bool BF16>
+__device__ __forceinline__ uint32_t down(float v) {
+  if (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
 // Maximum and sum over the four lanes n, n + 16, n + 32, n + 48 of a query row.
@@ -109,28 +110,51 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int nib) {
   return (nib >= 2 ? w >> 8 : w) & (nib & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef __attribute__((address_space(3))) void *LdsPtr;
+constexpr int kRsrcFlags = 0x00020000;  // raw buffer, 32-bit data format
+
+// Waits until at most N vector-memory operations of this wave are outstanding (vmcnt low
+// bits [3:0], high bits [15:14]; the other counts do not wait).
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-  if (N == 1) {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
-  } else if (N == 2) {
-    const uint2v v = *reinterpret_cast<const uint2v *>(p);
-    w[0] = v.x, w[N - 1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4v v = *reinterpret_cast<const uint4v *>(p + 16 * i);
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-    }
-  }
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// What a lane holds of 32 tokens: its part of the codes, and one token's parameters of
-// keys (lanes 0..31) or values (lanes 32..63).
-template <int D>
-struct Step {
-  uint32_t k[2][D / 32], v[2][D / 32], par[D / 64];
-  bool ok[2];  // wave-uniform: the 16 tokens are in the cache
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }  // lgkmcnt(0)
+
+// A number as a type: stages are named at compile time, so that the compiler sees that the
+// reads of one stage do not touch the copies into another and adds no wait of its own.
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
+// How many query rows a tile has and what follows from it.  16 rows fill the operands'
+// columns.  Where a request and head has fewer (a decode step has q_heads / kv_heads), a tile
+// has 16 / V rows, V = 2 or 4, and column n stands for row n % (16 / V) over the runs x of
+// tokens with x % V = n / (16 / V): the V columns of a row keep statistics and sums of their
+// own, like workgroups that split the tokens, and are joined at the end.  The operands are
+// zero where a column and a run do not belong together, so the products cost what they cost
+// for 16 rows, but the scores, exponentials and parameters are 4 per lane for V runs and not
+// for each: of about 290 vector operations for 32 tokens at D = 128 they are two thirds.
+template <int D, int V>
+struct Shape {
+  static constexpr int kRows = kCols / V;
+  static constexpr int kRuns = V == 1 || D == 256 ? 2 : 4;  // runs of a step
+  static constexpr int kSets = kRuns / V;         // scores of a lane and step, in fours
+  static constexpr int kTokens = kRuns * kRun;
+  // The wave's ring in LDS: a stage is one step; of each run the key codes, the value codes
+  // and the parameters of keys then values, copied from memory without passing registers
+  // (one instruction moves kSize bytes per lane to consecutive places).  One stage is in
+  // flight while one is used.
+  static constexpr int kSize = D == 64 ? 4 : 16;           // bytes per lane and instruction of codes
+  static constexpr int kCodes = 8 * D / (64 * kSize);      // instructions per run: key or value codes
+  static constexpr int kPars = D == 256 ? 2 : 1;           // and parameters, 4 bytes per lane
+  static constexpr int kBytes = 16 * D + 256 * kPars;      // bytes of a run
+  static constexpr int kStage = kRuns * kBytes;
+  static constexpr int kLoads = kRuns * (2 * kCodes + kPars);  // instructions of a stage
 };
 
 // The request, rows and tokens of a workgroup.
@@ -141,7 +165,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int32_t rt) {
   Tile t;
-  t.b = b, t.h = h, t.row0 = rt * kRows;
+  t.b = b, t.h = h, t.row0 = rt * a.tile_rows;
   t.q0 = a.cu[b];
   int32_t end = a.cu[b + 1];
   end = end < a.T ? end : a.T;
@@ -153,7 +177,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int
   t.len = len < 0 ? 0 : len < most ? len : most;
   const int64_t all = (int64_t)t.nq * a.group;
   const int64_t left = all - t.row0;
-  t.rows = left <= 0 ? 0 : left < kRows ? (int32_t)left : kRows;
+  t.rows = left <= 0 ? 0 : left < a.tile_rows ? (int32_t)left : a.tile_rows;
   if (t.rows > 0) {
     const int32_t first = t.len - t.nq + t.row0 / a.group, last = t.len - t.nq + (t.row0 + t.rows - 1) / a.group;
     t.hi = last + 1 > 0 ? last + 1 : 0;
@@ -165,21 +189,23 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int
   return t;
 }
 
-// The chunks of a tile start at its first token, rounded down to whole steps.
-__device__ __forceinline__ int32_t base_of(const Tile &t) { return t.lo & ~(kStep - 1); }
+// The chunks of a tile start at its first token, rounded down to whole runs.
+__device__ __forceinline__ int32_t base_of(const Tile &t) { return t.lo & ~(kRun - 1); }
 __device__ __forceinline__ int32_t chunks_of(const Args &a, const Tile &t) {
   return (t.hi - base_of(t) + a.chunk - 1) / a.chunk;
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args a) {
+template <int D, int V, bool BF16>
+__global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
+  using S = Shape<D, V>;
   constexpr int G = D / 64, W = D / 32, J = D / 16;
-  constexpr int kStride = D + 4;  // floats of a row of partial outputs in LDS
-  __shared__ __attribute__((aligned(16))) uint32_t s_par[kWaves][64 * G];
-  __shared__ __attribute__((aligned(16))) float s_o[kWaves][kRows * kStride];
-  __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
+  constexpr int kStride = D + 4;  // floats of a column of partial outputs in LDS
+  constexpr int kRing = 2 * S::kStage, kPartial = kCols * kStride * 4;
+  // the rings and, after the loop, the waves' partial outputs
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kWaves * (kRing > kPartial ? kRing : kPartial)];
+  __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
 
-  const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
+  const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4, part = n / S::kRows;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int32_t id = blockIdx.x;
   const int32_t split = id % a.splits;
@@ -195,11 +221,12 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args a) {
   const int32_t from = begin > t.lo ? begin : t.lo;
   const int32_t to = t.hi - begin > a.chunk ? begin + a.chunk : t.hi;
 
-  // The query row of this lane, as operands and as sums per group.
-  const int32_t r = t.row0 + (n < t.rows ? n : t.rows - 1);
+  // The query row of this lane, as operands (zero outside the column's part) and as sums per
+  // group of channels.
+  const int32_t row = n % S::kRows, r = t.row0 + (row < t.rows ? row : t.rows - 1);
   const int32_t i = r / a.group, head = h * a.group + r % a.group;
   const uint16_t *qp = a.q + (int64_t)(t.q0 + i) * a.ldq + (int64_t)head * D + 8 * c;
-  half8 q[W];
+  half8 q[V][W];
   float row_scale, qsum[G];
   {
     uint4v raw[W];
@@ -209,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args a) {
       raw[s] = *reinterpret_cast<const uint4v *>(qp + 32 * s);
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        top = fmaxf(top, fmaxf(fabsf(up(raw[s][w] & 0xFFFFu, a.bf16)), fabsf(up(raw[s][w] >> 16, a.bf16))));
+        top = fmaxf(top, fmaxf(fabsf(up<BF16>(raw[s][w] & 0xFFFFu)), fabsf(up<BF16>(raw[s][w] >> 16))));
     }
     top = quarters_max(top);
     int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;  // top in [2^(e-1), 2^e)
@@ -223,237 +250,358 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args a) {
       float x[8];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        x[2 * w] = up(raw[s][w] & 0xFFFFu, a.bf16);
-        x[2 * w + 1] = up(raw[s][w] >> 16, a.bf16);
+        x[2 * w] = up<BF16>(raw[s][w] & 0xFFFFu);
+        x[2 * w + 1] = up<BF16>(raw[s][w] >> 16);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) qsum[s / 2] += x[j];
+      half8 v;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // nibbles p and p + 4
         const float f = p & 1 ? mul * 0.0625f : mul;
-        q[s][2 * p] = (_Float16)(x[p] * f);
-        q[s][2 * p + 1] = (_Float16)(x[p + 4] * f);
+        v[2 * p] = (_Float16)(x[p] * f);
+        v[2 * p + 1] = (_Float16)(x[p + 4] * f);
       }
+#pragma unroll
+      for (int y = 0; y < V; ++y) q[y][s] = V == 1 || part == y ? v : half8{};
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) qsum[g] = quarters_sum(qsum[g]) * factor;
   }
-  const int32_t pos = t.len - t.nq + i;                       // this lane's row sees tokens
+  const int32_t pos = t.len - t.nq + i;                                      // this lane's row sees
   const int32_t row_hi = pos + 1, row_lo = a.window ? pos - a.window + 1 : 0;  // [row_lo, row_hi)
   // [all_lo, all_hi): tokens that every row of the tile sees
   const int32_t all_hi = t.len - t.nq + t.row0 / a.group + 1;
   const int32_t all_lo = a.window ? t.len - t.nq + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
 
+  // The column's running sums are of weights w = 2^(score - ref): ref is the largest score
+  // seen, up to kLazy, less a power k (the same in the wave) that keeps w times a value's
+  // scale below 2^15 and far above fp16's subnormals.
   float4v o[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) o[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kLow, l = 0.0f, bias[G], vs = 1.0f;
+  // rest: the sum of the weights before their rounding to fp16 less the sum after it.  Times
+  // 8, the middle code, it goes back into the output: the rounding then acts on codes about
+  // zero, half as large as 0 .. 15 and as little one-sided as the values themselves.  Next to
+  // a bf16 output's own rounding neither shows.
+  constexpr bool kRest = !BF16;
+  float m = kLow, k = 0.0f, ref = kLow, limit = kLow, l = 0.0f, bias[G], rest[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) bias[g] = 0.0f;
-  uint32_t vbits = 0;  // value scales up to this fp16 pattern fit the power of two vs
+  for (int g = 0; g < G; ++g) bias[g] = rest[g] = 0.0f;
+  uint32_t vbits = 0;  // value scales up to this fp16 pattern fit k
 
   const int32_t P = 1 << a.page_log2;
   const int32_t block = mixllm::kv4_block_bytes(P, D);
   const int32_t *table = a.table + b * a.ldt;
-  const int32_t koff = n * (D / 2) + c * (D / 8), voff = P * (D / 2) + (c * 16 + n) * 4 * (D / 32);
-  const int32_t poff = P * D + (lane >> 5) * (P * (D / 16)) + (lane & 15) * (4 * G);
-  uint32_t *par = s_par[wave];
+  // Where this lane's part of a run is in a block, before the run's own offset.
+  const int32_t koff = n * (D / 2) + c * (D / 8), voff = P * (D / 2) + (c * 16 + n) * (D / 8);
+  const int32_t pword = lane & (32 * G - 1);  // dword of the run's parameters (D = 256: and the one 64 on)
+  const int32_t poff = P * D + pword / (16 * G) * (P * (D / 16)) + pword % (16 * G) * 4;
+  const int32_t poff2 = P * D + P * (D / 16) + pword % (16 * G) * 4;  // D = 256: the values' half
+  uint8_t *ring = smem + wave * kRing;
 
-  auto load = [&](Step<D> &st, int32_t t0) {
-    const uint8_t *base[2];
-    int32_t in[2];
+  // Copies run x of the step at t0 into a stage; pg: its page, negative for none (then any
+  // memory of the cache is copied, to keep the number of instructions).
+  auto issue = [&](auto stage, int x, int32_t t0, int32_t pg) {
+    uint8_t *to_k = ring + decltype(stage)::value * S::kStage + x * S::kBytes, *to_v = to_k + 8 * D, *to_p = to_v + 8 * D;
+    pg = pg < 0 ? 0 : pg;
+    const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(a.cache) + ((int64_t)pg * a.hkv + h) * block, (short)0, block, kRsrcFlags);
+    const int32_t in = (t0 + kRun * x) & (P - 1), at = in * (D / 2);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int32_t tx = t0 + 16 * x;
-      int32_t pg = tx < to ? table[tx >> a.page_log2] : -1;
-      st.ok[x] = (uint32_t)pg < (uint32_t)a.pages;
-      pg = st.ok[x] ? pg : 0;
-      in[x] = tx & (P - 1);
-      base[x] = a.cache + ((int64_t)pg * a.hkv + h) * block + in[x] * (D / 2);
-      load_words(base[x] + koff, st.k[x]);
-      load_words(base[x] + voff, st.v[x]);
+    for (int e = 0; e < S::kCodes; ++e) {
+      if constexpr (D == 64) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 256), 4, koff + 4 * e, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 256), 4, voff + 4 * e, at, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 1024), 16, koff + 16 * e, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 1024), 16, voff + 16 * e, at, 0, 0);
+      }
     }
-    // parameters of this lane's token, nothing for one that is not there
-    const int x = (lane >> 4) & 1;
-    const uint8_t *bp = x ? base[1] - in[1] * (D / 2) + in[1] * (4 * G) : base[0] - in[0] * (D / 2) + in[0] * (4 * G);
-    load_words(bp + poff, st.par);
-    const bool there = (x ? st.ok[1] : st.ok[0]) && t0 + (lane & 31) < to;
-#pragma unroll
-    for (int g = 0; g < G; ++g) st.par[g] = there ? st.par[g] : 0u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)to_p, 4, poff, in * (4 * G), 0, 0);
+    if constexpr (S::kPars == 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_p + 256), 4, poff2, in * (4 * G), 0, 0);
   };
+  // This lane's dwords of key or value codes of a run.
+  auto codes = [&](const uint8_t *src, uint32_t (&w)[W]) {
+    if constexpr (D == 64) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) w[e] = *reinterpret_cast<const uint32_t *>(src + e * 256 + lane * 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W / 4; ++e) {
+        const uint4v v = *reinterpret_cast<const uint4v *>(src + e * 1024 + lane * 16);
+        w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+      }
+    }
+  };
+  auto params = [&](const uint8_t *src, half2v (&p)[4][G]) {  // of the 4 tokens of this quarter
+    const uint4v *q4 = reinterpret_cast<const uint4v *>(src + c * (16 * G));
+#pragma unroll
+    for (int f = 0; f < G; ++f) {
+      const uint4v v = q4[f];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t word = v[e];  // a copy: a bit cast of a vector's element takes its first one
+        p[(4 * f + e) / G][(4 * f + e) % G] = __builtin_bit_cast(half2v, word);
+      }
+    }
+  };
+  auto at = [](const half2v (&p)[G], int e) { return (float)p[e / 2][e % 2]; };
 
-  auto compute = [&](const Step<D> &st, int32_t t0) {
-    // Every lane needs the parameters of the 8 tokens of its quarter: through LDS.
+  // here: bit x says that run x is in the cache.
+  auto compute = [&](auto stage, int32_t t0, uint32_t here) {
+    const uint8_t *src = ring + decltype(stage)::value * S::kStage;
+    float s[S::kSets][4];
 #pragma unroll
-    for (int g = 0; g < G; ++g) par[lane * G + g] = st.par[g];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    half2v kp[2][4][G], vp[2][4][G];  // [16 tokens][token][scales, then minima]
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          kp[x][u][g] = __builtin_bit_cast(half2v, par[(16 * x + 4 * c + u) * G + g]);
-          vp[x][u][g] = __builtin_bit_cast(half2v, par[(32 + 16 * x + 4 * c + u) * G + g]);
-        }
-    __builtin_amdgcn_wave_barrier();
-    auto at = [](const half2v (&p)[G], int e) { return (float)p[e / 2][e % 2]; };
-
-    float s[8];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int z = 0; z < S::kSets; ++z) {
       float4v acc[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        acc[g] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-        acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(st.k[x][2 * g]), q[2 * g], acc[g], 0, 0, 0);
-        acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(st.k[x][2 * g + 1]), q[2 * g + 1], acc[g], 0, 0, 0);
+      for (int g = 0; g < G; ++g) acc[g] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int y = 0; y < V; ++y) {
+        uint32_t w[W];
+        codes(src + (z * V + y) * S::kBytes, w);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w[2 * g]), q[y][2 * g], acc[g], 0, 0, 0);
+          acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w[2 * g + 1]), q[y][2 * g + 1], acc[g], 0, 0, 0);
+        }
       }
+      half2v kp[4][G];
+      params(src + (z * V + part) * S::kBytes + 16 * D, kp);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         float dot = 0.0f, add = 0.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          dot = fmaf(at(kp[x][u], g), acc[g][u], dot);
-          add = fmaf(at(kp[x][u], G + g), qsum[g], add);
+          dot = fmaf(at(kp[u], g), acc[g][u], dot);
+          add = fmaf(at(kp[u], G + g), qsum[g], add);
         }
-        s[4 * x + u] = fmaf(row_scale, dot, add);
+        s[z][u] = fmaf(row_scale, dot, add);
       }
     }
-    if (!(t0 >= all_lo && t0 >= from && t0 + kStep <= all_hi && t0 + kStep <= to && st.ok[0] && st.ok[1])) {
+    half2v vp[S::kSets][4][G];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int32_t tok = t0 + 16 * (e / 4) + 4 * c + e % 4;
-        const bool seen = tok < row_hi && tok >= row_lo && tok < to && tok >= from && st.ok[e / 4];
-        s[e] = seen ? s[e] : -INFINITY;
-      }
+    for (int z = 0; z < S::kSets; ++z) params(src + (z * V + part) * S::kBytes + 16 * D + 64 * G, vp[z]);
+    if (!(t0 >= all_lo && t0 >= from && t0 + S::kTokens <= all_hi && t0 + S::kTokens <= to &&
+          here == (1u << S::kRuns) - 1)) {
+#pragma unroll
+      for (int z = 0; z < S::kSets; ++z)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int32_t tok = t0 + kRun * (z * V + part) + 4 * c + u;
+          const bool there = tok < to && (here >> (z * V + part) & 1);
+          s[z][u] = there && tok < row_hi && tok >= row_lo && tok >= from ? s[z][u] : -INFINITY;
+          // what lies behind the last token may be NaN: no part of a sum, not even times zero
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t w = __builtin_bit_cast(uint32_t, vp[z][u][g]);
+            vp[z][u][g] = __builtin_bit_cast(half2v, there ? w : 0u);
+          }
+        }
     }
-    float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-    top = quarters_max(top);
+    float top = s[0][0];
     uint32_t big = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int z = 0; z < S::kSets; ++z)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t v = __builtin_bit_cast(uint16_t, vp[e / 4][e % 4][g / 2][g % 2]);
-        big = v > big ? v : big;
-      }
-    if (__any(top > m + kLazy || big > vbits)) {
-      float ratio = 1.0f;
-      if (__any(big > vbits)) {
-        big = quarters_max(big);
-        const uint32_t e = big >> 10 ? big >> 10 : 1;
-        vbits = e << 10 | 0x3FF;
-        const float to_scale = __uint_as_float((127 + 23 - e) << 23);  // a scale below 2^(e-14) times this is below 2^9
-        ratio = to_scale / vs;
-        vs = to_scale;
-      }
-      const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
-      m = next;
-      l *= f;
+      for (int u = 0; u < 4; ++u) {
+        top = fmaxf(top, s[z][u]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) bias[g] *= f;
-#pragma unroll
-      for (int j = 0; j < J; ++j) o[j] *= f * ratio;
-    }
-    half8 p[G];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float w = __builtin_amdgcn_exp2f(s[e] - m);
-      l += w;
-      const float wv = w * vs;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        bias[g] = fmaf(at(vp[e / 4][e % 4], G + g), w, bias[g]);
-        p[g][e] = (_Float16)(wv * at(vp[e / 4][e % 4], g));
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      uint32_t w[4];  // pairs of tokens, the 4 nibbles of group g's channels in each half
-#pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        if (D == 64) {
-          w[z] = st.v[z / 2][z % 2];
-        } else {
-          const int per = D / 128;  // dwords of one token
-          const int d0 = (z % 2) * 2 * per + g / 2;
-          w[z] = __builtin_amdgcn_perm(st.v[z / 2][d0 + per], st.v[z / 2][d0], g % 2 ? 0x07060302u : 0x05040100u);
+        for (int g = 0; g < G; ++g) {
+          const uint32_t pair = __builtin_bit_cast(uint32_t, vp[z][u][g / 2]);
+          const uint32_t v = g % 2 ? pair >> 16 : pair & 0xFFFFu;
+          big = v > big ? v : big;
         }
       }
+    if (__any(top > limit || big > vbits)) {
+      if (__any(big > vbits)) {
 #pragma unroll
-      for (int nib = 0; nib < 4; ++nib) {
-        const uint4v v = {nibble_pair(w[0], nib), nibble_pair(w[1], nib), nibble_pair(w[2], nib), nibble_pair(w[3], nib)};
-        o[4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, v), p[g], o[4 * g + nib], 0, 0, 0);
+        for (int d = S::kRows; d < kCols; d <<= 1) {
+          const uint32_t other = __shfl_xor(big, d);
+          big = other > big ? other : big;
+        }
+        big = quarters_max(big);
+        const int32_t e = big >> 10 ? big >> 10 : 1;
+        vbits = e << 10 | 0x3FF;
+        k = (float)(23 - e);  // a scale below 2^(e-14) times 2^k is below 2^9
+      }
+      m = fmaxf(m, quarters_max(top));
+      const float next = m - k, f = __builtin_amdgcn_exp2f(ref - next);
+      ref = next;
+      limit = m + kLazy;
+      l *= f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        bias[g] *= f;
+        rest[g] *= f;
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) o[j] *= f;
+    }
+    half2v p[S::kSets][G][2];
+#pragma unroll
+    for (int z = 0; z < S::kSets; ++z)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = __builtin_amdgcn_exp2f(s[z][u] - ref);
+        l += w;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          bias[g] = fmaf(at(vp[z][u], G + g), w, bias[g]);
+          const float ps = fmaf(at(vp[z][u], g), w, 0.0f);  // as a fused sum it takes the fp16 factor as it is
+          if (kRest) rest[g] += ps;
+          p[z][g][u / 2][u % 2] = (_Float16)ps;
+        }
+      }
+    if (kRest) {
+#pragma unroll
+      for (int z = 0; z < S::kSets; ++z)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            rest[g] = __builtin_amdgcn_fdot2(p[z][g][y], half2v{(_Float16)-1.0f, (_Float16)-1.0f}, rest[g], false);
+    }
+#pragma unroll
+    for (int y = 0; y < S::kRuns / 2; ++y) {  // two runs fill an operand
+      uint32_t v[2][W];
+      codes(src + 2 * y * S::kBytes + 8 * D, v[0]);
+      codes(src + (2 * y + 1) * S::kBytes + 8 * D, v[1]);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint4v pw;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (V == 1) {
+            pw[e] = __builtin_bit_cast(uint32_t, p[0][g][e]);
+            pw[2 + e] = __builtin_bit_cast(uint32_t, p[S::kSets - 1][g][e]);
+          } else {
+            const uint32_t w = __builtin_bit_cast(uint32_t, p[V == 2 ? y : 0][g][e]);
+            const int first = V == 2 ? 0 : 2 * y;  // the column part of this pair's first run
+            pw[e] = part == first ? w : 0u;
+            pw[2 + e] = part == first + 1 ? w : 0u;
+          }
+        }
+        uint32_t w[4];  // pairs of tokens, the 4 nibbles of group g's channels in each half
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          if (D == 64) {
+            w[z] = v[z / 2][z % 2];
+          } else {
+            constexpr int per = D < 128 ? 1 : D / 128;  // dwords of one token
+            const int d0 = (z % 2) * 2 * per + g / 2;
+            w[z] = __builtin_amdgcn_perm(v[z / 2][d0 + per], v[z / 2][d0], g % 2 ? 0x07060302u : 0x05040100u);
+          }
+        }
+#pragma unroll
+        for (int nib = 0; nib < 4; ++nib) {
+          const uint4v u = {nibble_pair(w[0], nib), nibble_pair(w[1], nib), nibble_pair(w[2], nib), nibble_pair(w[3], nib)};
+          o[4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, u), __builtin_bit_cast(half8, pw),
+                                                                  o[4 * g + nib], 0, 0, 0);
+        }
       }
     }
   };
 
-  {
-    int32_t t0 = (from & ~(kStep - 1)) + wave * kStep;
-    Step<D> st[2];
-    if (t0 < to) load(st[0], t0);
-    while (t0 < to) {
-      int32_t t1 = t0 + kWaves * kStep;
-      if (t1 < to) load(st[1], t1);
-      compute(st[0], t0);
-      if (t1 >= to) break;
-      t0 = t1 + kWaves * kStep;
-      if (t0 < to) load(st[0], t0);
-      compute(st[1], t1);
+  // This wave takes every fourth step, in batches whose pages one load fetches.
+  constexpr int32_t kStride4 = kWaves * S::kTokens, kBatch = 64 / S::kRuns;
+  for (int32_t tb = (from & ~(kRun - 1)) + wave * S::kTokens; tb < to; tb += kBatch * kStride4) {
+    int32_t pages = -1;
+    {
+      const int32_t tok = tb + lane / S::kRuns * kStride4 + lane % S::kRuns * kRun;
+      if (tok < to) pages = table[tok >> a.page_log2];
+      pages = (uint32_t)pages < (uint32_t)a.pages ? pages : -1;
     }
+    const int32_t left = (to - tb + kStride4 - 1) / kStride4, steps = left < kBatch ? left : kBatch;
+    const uint64_t there = __ballot(pages >= 0);
+    auto start = [&](auto stage, int32_t j) {
+#pragma unroll
+      for (int x = 0; x < S::kRuns; ++x)
+        issue(stage, x, tb + j * kStride4, __builtin_amdgcn_readlane(pages, S::kRuns * j + x));
+    };
+    auto step = [&](auto stage, int32_t j) {
+      if (j + 1 < steps) {
+        wait_lds();  // the stage that is filled now was read in the last step
+        start(Const<1 - decltype(stage)::value>(), j + 1);
+        wait_vm<S::kLoads>();
+      } else {
+        wait_vm<0>();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      compute(stage, tb + j * kStride4, (uint32_t)(there >> (S::kRuns * j)) & ((1u << S::kRuns) - 1));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    start(Const<0>(), 0);
+    for (int32_t j = 0;;) {
+      step(Const<0>(), j);
+      if (++j == steps) break;
+      step(Const<1>(), j);
+      if (++j == steps) break;
+    }
+    wait_lds();
   }
 
-  // The four waves' statistics and outputs, over the largest maximum.
+  // The columns' statistics and outputs; a row's are V columns of each wave.
   l = quarters_sum(l);
 #pragma unroll
-  for (int g = 0; g < G; ++g) bias[g] = quarters_sum(bias[g]);
+  for (int g = 0; g < G; ++g) bias[g] = quarters_sum(kRest ? fmaf(rest[g], 8.0f, bias[g]) : bias[g]);
   if (c == 0) {
-    s_m[wave][n] = m;
+    s_m[wave][n] = ref;
     s_l[wave][n] = l;
   }
-  __syncthreads();
-  const float best = fmaxf(fmaxf(s_m[0][n], s_m[1][n]), fmaxf(s_m[2][n], s_m[3][n]));
-  const float f = __builtin_amdgcn_exp2f(m - best);
+  __syncthreads();  // and every wave is done with its ring
+  float *s_o = reinterpret_cast<float *>(smem);
+  float best = ref;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+    for (int y = 0; y < V; ++y) best = fmaxf(best, s_m[w][row + y * S::kRows]);
+  const float f = __builtin_amdgcn_exp2f(ref - best);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const float fo = f * (j & 1 ? 0x1p20f : 0x1p24f) / vs, fb = f * bias[j / 4];
+    const float fo = f * (j & 1 ? 0x1p20f : 0x1p24f), fb = f * bias[j / 4];
     float4v v;
 #pragma unroll
     for (int u = 0; u < 4; ++u) v[u] = fmaf(o[j][u], fo, fb);
-    *reinterpret_cast<float4v *>(&s_o[wave][n * kStride + 16 * j + 4 * c]) = v;
+    *reinterpret_cast<float4v *>(s_o + (wave * kCols + n) * kStride + 16 * j + 4 * c) = v;
   }
   __syncthreads();
-  const int64_t part = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits + split;
+  const int64_t place = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits + split;
   for (int e = threadIdx.x; e < t.rows * (D / 8); e += kThreads) {
-    const int row = e / (D / 8), ch = e % (D / 8) * 8;
-    float top = s_m[0][row], sum = 0.0f;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_m[w][row]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum = fmaf(s_l[w][row], __builtin_amdgcn_exp2f(s_m[w][row] - top), sum);
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = 0.0f;
+    const int rr = e / (D / 8), ch = e % (D / 8) * 8;
+    float top = kLow * 2.0f, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] += s_o[w][row * kStride + ch + u];
-    if (a.splits > 1) {
-      float *dst = a.ws_o + (part * a.rows_tile + row) * D + ch;
-      *reinterpret_cast<float4v *>(dst) = float4v{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<float4v *>(dst + 4) = float4v{v[4], v[5], v[6], v[7]};
-      if (ch == 0) *reinterpret_cast<float2v *>(a.ws_ml + (part * a.rows_tile + row) * 2) = float2v{top, sum};
-    } else {
-      const int32_t rr = t.row0 + row, ii = t.q0 + rr / a.group, hh = h * a.group + rr % a.group;
-      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays NaN
-      uint32_t w[4];
+      for (int y = 0; y < V; ++y) top = fmaxf(top, s_m[w][rr + y * S::kRows]);
+    float4v v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = down(v[2 * u] * inv, a.bf16) | down(v[2 * u + 1] * inv, a.bf16) << 16;
-      *reinterpret_cast<uint4v *>(a.out + (int64_t)ii * a.ldo + (int64_t)hh * D + ch) = uint4v{w[0], w[1], w[2], w[3]};
+    for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+      for (int y = 0; y < V; ++y) {
+        const int col = rr + y * S::kRows;
+        sum = fmaf(s_l[w][col], __builtin_amdgcn_exp2f(s_m[w][col] - top), sum);
+        const float *src = s_o + (w * kCols + col) * kStride + ch;
+        v0 += *reinterpret_cast<const float4v *>(src);
+        v1 += *reinterpret_cast<const float4v *>(src + 4);
+      }
+    if (a.splits > 1) {
+      float *dst = a.ws_o + (place * a.tile_rows + rr) * D + ch;
+      *reinterpret_cast<float4v *>(dst) = v0;
+      *reinterpret_cast<float4v *>(dst + 4) = v1;
+      if (ch == 0) *reinterpret_cast<float2v *>(a.ws_ml + (place * a.tile_rows + rr) * 2) = float2v{top, sum};
+    } else {
+      const int32_t rg = t.row0 + rr, ii = t.q0 + rg / a.group, hh = h * a.group + rg % a.group;
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays NaN
+      uint4v w;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        w[u] = down<BF16>(v0[2 * u] * inv) | down<BF16>(v0[2 * u + 1] * inv) << 16;
+        w[2 + u] = down<BF16>(v1[2 * u] * inv) | down<BF16>(v1[2 * u + 1] * inv) << 16;
+      }
+      *reinterpret_cast<uint4v *>(a.out + (int64_t)ii * a.ldo + (int64_t)hh * D + ch) = w;
       if (ch == 0 && a.lse) a.lse[(int64_t)ii * a.hq + hh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
   }
@@ -461,7 +609,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args a) {
 
 // Joins the chunks of a row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  WAVES
 // waves share a row and head, wave w takes the chunks w, w + WAVES, ..
-template <int D, int WAVES>
+template <int D, int WAVES, bool BF16>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   constexpr int C = D / 64;  // channels of a lane
   __shared__ float s_m[kWaves], s_l[kWaves], s_o[kWaves][D];
@@ -474,21 +622,21 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   const int32_t head = (int32_t)(id % a.hq);
   id /= a.hq;
   const int32_t i = (int32_t)(id % a.max_rows), b = (int32_t)(id / a.max_rows);
-  const int32_t h = head / a.group, r = i * a.group + head % a.group, rt = r / kRows, row = r % kRows;
+  const int32_t h = head / a.group, r = i * a.group + head % a.group, rt = r / a.tile_rows, row = r % a.tile_rows;
   const Tile t = tile_of(a, b, h, rt);
   const bool there = live && i < t.nq;
   const int32_t nchunks = there ? chunks_of(a, t) : 0;
   const int64_t part0 = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits;
-  const float *ml = a.ws_ml + (part0 * a.rows_tile + row) * 2;
-  const float *po = a.ws_o + (part0 * a.rows_tile + row) * D + lane * C;
-  float m = kLow, l = 0.0f, o[C] = {};
+  const float *ml = a.ws_ml + (part0 * a.tile_rows + row) * 2;
+  const float *po = a.ws_o + (part0 * a.tile_rows + row) * D + lane * C;
+  float m = 2.0f * kLow, l = 0.0f, o[C] = {};
   for (int32_t s = wave % WAVES; s < nchunks; s += WAVES) {
-    const float ms = ml[(int64_t)s * a.rows_tile * 2], ls = ml[(int64_t)s * a.rows_tile * 2 + 1];
+    const float ms = ml[(int64_t)s * a.tile_rows * 2], ls = ml[(int64_t)s * a.tile_rows * 2 + 1];
     const float next = fmaxf(m, ms), f = __builtin_amdgcn_exp2f(m - next), fs = __builtin_amdgcn_exp2f(ms - next);
     m = next;
     l = fmaf(l, f, ls * fs);
 #pragma unroll
-    for (int e = 0; e < C; ++e) o[e] = fmaf(o[e], f, po[(int64_t)s * a.rows_tile * D + e] * fs);
+    for (int e = 0; e < C; ++e) o[e] = fmaf(o[e], f, po[(int64_t)s * a.tile_rows * D + e] * fs);
   }
   if (WAVES > 1) {
     if (lane == 0) {
@@ -519,33 +667,33 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
   uint16_t *dst = a.out + (int64_t)(t.q0 + i) * a.ldo + (int64_t)head * D + lane * C;
 #pragma unroll
-  for (int e = 0; e < C; ++e) dst[e] = (uint16_t)down(o[e] * inv, a.bf16);
+  for (int e = 0; e < C; ++e) dst[e] = (uint16_t)down<BF16>(o[e] * inv);
   if (lane == 0 && a.lse) a.lse[(int64_t)(t.q0 + i) * a.hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// How the work of a call is cut.  Rows: tiles of 16 (row, head) pairs of one key/value head.
-// Tokens: chunks of a multiple of 128 (one step of each wave) so that about kTarget
-// workgroups run; 256 CUs hold 4 of them each.
-constexpr int64_t kTarget = 2048;
+// How the work of a call is cut.  Rows: tiles of 4, 8 or 16 (row, head) pairs of one
+// key/value head.  Tokens: chunks of a multiple of 256 (one step of each wave) so that about
+// kTarget workgroups run; 256 CUs hold 2 of them each.
+constexpr int64_t kTarget = 1024;
 constexpr int32_t kMaxChunk = 2048;
 
 struct Cut {
-  int32_t tiles, rows_tile, splits, chunk;
+  int32_t tiles, tile_rows, splits, chunk;
 };
 
-Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t max_rows, int32_t max_len, int32_t window) {
+Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
   Cut k;
   const int64_t rows = (int64_t)max_rows * (hq / hkv);
-  k.tiles = (int32_t)((rows + kRows - 1) / kRows);
-  k.rows_tile = rows < kRows ? (int32_t)rows : kRows;
+  k.tile_rows = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 8 : 16;
+  k.tiles = (int32_t)((rows + k.tile_rows - 1) / k.tile_rows);
   int64_t span = max_len;
-  // a tile's rows are at most 16 positions, its first chunk starts at a whole step
-  if (window && (int64_t)window + kRows + kStep < span) span = (int64_t)window + kRows + kStep;
+  // a tile's rows are at most 16 positions, its first chunk starts at a whole run
+  if (window && (int64_t)window + 16 + kRun < span) span = (int64_t)window + 16 + kRun;
   const int64_t groups = (int64_t)B * hkv * k.tiles;
   int64_t chunk = (span * groups + kTarget - 1) / kTarget;
-  chunk = (chunk + 127) / 128 * 128;
-  chunk = chunk < 128 ? 128 : chunk > kMaxChunk ? kMaxChunk : chunk;
-  if (groups >= kTarget) chunk = span < 128 ? 128 : (span + 127) / 128 * 128;
+  chunk = (chunk + 255) / 256 * 256;
+  chunk = chunk < 256 ? 256 : chunk > kMaxChunk ? kMaxChunk : chunk;
+  if (groups >= kTarget) chunk = span < 256 ? 256 : (span + 255) / 256 * 256;
   k.chunk = (int32_t)chunk;
   k.splits = span <= chunk ? 1 : (int32_t)((span + chunk - 1) / chunk);
   return k;
@@ -560,13 +708,23 @@ bool shape_ok(int64_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_
   return (int64_t)max_rows * (hq / hkv) < (1 << 30) && max_len < (1 << 30) && window < (1 << 30) && hq < (1 << 20);
 }
 
-template <int D>
+template <int D, bool BF16>
 void launch(const Args &a, int64_t blocks, hipStream_t s) {
-  hipLaunchKernelGGL((kv4_attention_kernel<D>), dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+  const dim3 grid((unsigned)blocks), threads(kThreads);
+  if (D < 256 && a.tile_rows == 4)
+    hipLaunchKernelGGL((kv4_attention_kernel<D, D < 256 ? 4 : 2, BF16>), grid, threads, 0, s, a);
+  else if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attention_kernel<D, 2, BF16>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((kv4_attention_kernel<D, 1, BF16>), grid, threads, 0, s, a);
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
   const int64_t rows = (int64_t)a.B * a.max_rows * a.hq;
-  if (a.splits > 16) hipLaunchKernelGGL((kv4_join_kernel<D, 4>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((kv4_join_kernel<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a);
+  if (a.splits > 16) hipLaunchKernelGGL((kv4_join_kernel<D, 4, BF16>), dim3((unsigned)rows), threads, 0, s, a);
+  else hipLaunchKernelGGL((kv4_join_kernel<D, 1, BF16>), dim3((unsigned)((rows + 3) / 4)), threads, 0, s, a);
+}
+
+template <int D>
+void launch(const Args &a, int32_t dtype, int64_t blocks, hipStream_t s) {
+  if (dtype == MIXLLM_BF16) launch<D, true>(a, blocks, s);
+  else launch<D, false>(a, blocks, s);
 }
 
 }  // namespace
@@ -575,9 +733,9 @@ extern "C" size_t mixllm_kv4_attention_workspace_bytes(int32_t T, int32_t B, int
                                                        int32_t dim, int32_t max_rows, int32_t max_len,
                                                        int32_t window) {
   if (!shape_ok(T, B, q_heads, kv_heads, dim, max_rows, max_len, window) || T == 0 || B == 0 || max_rows == 0) return 0;
-  const Cut k = cut_of(B, q_heads, kv_heads, max_rows, max_len, window);
+  const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
   if (k.splits == 1) return 0;
-  return (size_t)B * k.tiles * kv_heads * k.splits * k.rows_tile * (dim + 2) * sizeof(float);
+  return (size_t)B * k.tiles * kv_heads * k.splits * k.tile_rows * (dim + 2) * sizeof(float);
 }
 
 extern "C" int mixllm_kv4_attention(const void *q, int64_t ldq, int32_t dtype, int32_t T, int32_t q_heads,
@@ -599,22 +757,22 @@ extern "C" int mixllm_kv4_attention(const void *q, int64_t ldq, int32_t dtype, i
       !mixllm::is_aligned4(lens) || !mixllm::is_aligned4(cu) || !mixllm::is_aligned4(lse) ||
       !mixllm::is_aligned16(workspace))
     return MIXLLM_E_SHAPE;
-  const Cut k = cut_of(B, q_heads, kv_heads, max_rows, max_len, window);
+  const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
   const int64_t parts = (int64_t)B * k.tiles * kv_heads * k.splits;
   if (parts > 0x7FFFFFFF || (int64_t)B * k.tiles > 0x7FFFFFFF || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
     return MIXLLM_E_SHAPE;
   float *ws = static_cast<float *>(workspace);
   if (k.splits > 1) {
-    if (workspace_bytes < (size_t)parts * k.rows_tile * (dim + 2) * sizeof(float)) return MIXLLM_E_SPACE;
+    if (workspace_bytes < (size_t)parts * k.tile_rows * (dim + 2) * sizeof(float)) return MIXLLM_E_SPACE;
     if (!ws) return MIXLLM_E_NULL;
   }
   const Args a = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(cache), table, lens, cu,
-                  static_cast<uint16_t *>(out), lse, ws, ws ? ws + parts * k.rows_tile * dim : nullptr,
+                  static_cast<uint16_t *>(out), lse, ws, ws ? ws + parts * k.tile_rows * dim : nullptr,
                   ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
                   mixllm::log2_of(page), width, B, max_rows,
-                  max_len, window, k.tiles, k.rows_tile, k.splits, k.chunk, dtype == MIXLLM_BF16};
-  if (dim == 64) launch<64>(a, parts, (hipStream_t)stream);
-  else if (dim == 128) launch<128>(a, parts, (hipStream_t)stream);
-  else launch<256>(a, parts, (hipStream_t)stream);
+                  max_len, window, k.tiles, k.tile_rows, k.splits, k.chunk};
+  if (dim == 64) launch<64>(a, dtype, parts, (hipStream_t)stream);
+  else if (dim == 128) launch<128>(a, dtype, parts, (hipStream_t)stream);
+  else launch<256>(a, dtype, parts, (hipStream_t)stream);
   return mixllm::launch_status();
 }
