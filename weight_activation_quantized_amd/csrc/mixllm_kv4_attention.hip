@@ -46,6 +46,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRun = 16;          // tokens of a run: a page holds it whole
 constexpr int kCols = 16;         // columns of a matrix operand
+constexpr int32_t kMinChunk = 256;  // tokens: one step of each wave
 constexpr float kLow = -1e38f;    // a running maximum before any score
 constexpr float kLazy = 6.0f;     // the maximum moves once a score is this far above it (log2)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -61,7 +62,7 @@ struct Args {
   float scale;
   int32_t T, hq, hkv, group, pages, page_log2, width, B, max_rows, max_len, window;
   int32_t tiles, tile_rows;  // row tiles of a request and head, rows of a full tile
-  int32_t splits, chunk;     // workgroups along the tokens, tokens of each
+  int32_t splits;            // workgroups along the tokens of a tile
 };
 
 template <bool BF16>
@@ -191,8 +192,13 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int
 
 // The chunks of a tile start at its first token, rounded down to whole runs.
 __device__ __forceinline__ int32_t base_of(const Tile &t) { return t.lo & ~(kRun - 1); }
-__device__ __forceinline__ int32_t chunks_of(const Args &a, const Tile &t) {
-  return (t.hi - base_of(t) + a.chunk - 1) / a.chunk;
+// Each of the `splits` workgroups takes an equal chunk, a multiple of 64 tokens, 256 or more.
+__device__ __forceinline__ int32_t chunk_of(const Args &a, const Tile &t) {
+  const int32_t each = (int32_t)(((uint32_t)(t.hi - base_of(t)) + a.splits - 1) / (uint32_t)a.splits);
+  return each <= kMinChunk ? kMinChunk : (each + 63) & ~63;
+}
+__device__ __forceinline__ int32_t chunks_of(const Tile &t, int32_t chunk) {
+  return (int32_t)(((uint32_t)(t.hi - base_of(t)) + chunk - 1) / (uint32_t)chunk);
 }
 
 template <int D, int V, bool BF16>
@@ -215,11 +221,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   const int32_t rt = id % a.tiles, b = id / a.tiles;
   const Tile t = tile_of(a, b, h, rt);
   if (t.rows <= 0) return;
-  const int32_t nchunks = chunks_of(a, t);
+  const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
   if (split >= nchunks && !(split == 0 && a.splits == 1)) return;
-  const int32_t begin = base_of(t) + split * a.chunk;
+  const int32_t begin = base_of(t) + split * chunk;
   const int32_t from = begin > t.lo ? begin : t.lo;
-  const int32_t to = t.hi - begin > a.chunk ? begin + a.chunk : t.hi;
+  const int32_t to = t.hi - begin > chunk ? begin + chunk : t.hi;
 
   // The query row of this lane, as operands (zero outside the column's part) and as sums per
   // group of channels.
@@ -625,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   const int32_t h = head / a.group, r = i * a.group + head % a.group, rt = r / a.tile_rows, row = r % a.tile_rows;
   const Tile t = tile_of(a, b, h, rt);
   const bool there = live && i < t.nq;
-  const int32_t nchunks = there ? chunks_of(a, t) : 0;
+  const int32_t nchunks = there ? chunks_of(t, chunk_of(a, t)) : 0;
   const int64_t part0 = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits;
   const float *ml = a.ws_ml + (part0 * a.tile_rows + row) * 2;
   const float *po = a.ws_o + (part0 * a.tile_rows + row) * D + lane * C;
@@ -672,13 +678,12 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
 }
 
 // How the work of a call is cut.  Rows: tiles of 4, 8 or 16 (row, head) pairs of one
-// key/value head.  Tokens: chunks of a multiple of 256 (one step of each wave) so that about
-// kTarget workgroups run; 256 CUs hold 2 of them each.
-constexpr int64_t kTarget = 1024;
-constexpr int32_t kMaxChunk = 2048;
+// key/value head.  Tokens: so many equal chunks of each tile that about kTarget workgroups
+// run at the longest length; 256 CUs hold 2 of them each.
+constexpr int64_t kTarget = 512;
 
 struct Cut {
-  int32_t tiles, tile_rows, splits, chunk;
+  int32_t tiles, tile_rows, splits;
 };
 
 Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
@@ -690,12 +695,8 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
   // a tile's rows are at most 16 positions, its first chunk starts at a whole run
   if (window && (int64_t)window + 16 + kRun < span) span = (int64_t)window + 16 + kRun;
   const int64_t groups = (int64_t)B * hkv * k.tiles;
-  int64_t chunk = (span * groups + kTarget - 1) / kTarget;
-  chunk = (chunk + 255) / 256 * 256;
-  chunk = chunk < 256 ? 256 : chunk > kMaxChunk ? kMaxChunk : chunk;
-  if (groups >= kTarget) chunk = span < 256 ? 256 : (span + 255) / 256 * 256;
-  k.chunk = (int32_t)chunk;
-  k.splits = span <= chunk ? 1 : (int32_t)((span + chunk - 1) / chunk);
+  const int64_t most = (span + kMinChunk - 1) / kMinChunk, want = (kTarget + groups - 1) / groups;
+  k.splits = (int32_t)(most < 1 || want <= 1 ? 1 : want < most ? want : most);
   return k;
 }
 
@@ -770,7 +771,7 @@ extern "C" int mixllm_kv4_attention(const void *q, int64_t ldq, int32_t dtype, i
                   static_cast<uint16_t *>(out), lse, ws, ws ? ws + parts * k.tile_rows * dim : nullptr,
                   ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
                   mixllm::log2_of(page), width, B, max_rows,
-                  max_len, window, k.tiles, k.tile_rows, k.splits, k.chunk};
+                  max_len, window, k.tiles, k.tile_rows, k.splits};
   if (dim == 64) launch<64>(a, dtype, parts, (hipStream_t)stream);
   else if (dim == 128) launch<128>(a, dtype, parts, (hipStream_t)stream);
   else launch<256>(a, dtype, parts, (hipStream_t)stream);
