@@ -213,12 +213,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4, part = n / S::kRows;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int32_t id = blockIdx.x;
-  const int32_t split = id % a.splits;
-  id /= a.splits;
-  const int32_t h = id % a.hkv;
-  id /= a.hkv;
-  const int32_t rt = id % a.tiles, b = id / a.tiles;
+  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, rt = blockIdx.y, b = blockIdx.z;
   const Tile t = tile_of(a, b, h, rt);
   if (t.rows <= 0) return;
   const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
@@ -232,14 +227,70 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   const int32_t row = n % S::kRows, r = t.row0 + (row < t.rows ? row : t.rows - 1);
   const int32_t i = r / a.group, head = h * a.group + r % a.group;
   const uint16_t *qp = a.q + (int64_t)(t.q0 + i) * a.ldq + (int64_t)head * D + 8 * c;
+  uint4v raw[W];
+#pragma unroll
+  for (int s = 0; s < W; ++s) raw[s] = *reinterpret_cast<const uint4v *>(qp + 32 * s);
+
+  const int32_t P = 1 << a.page_log2;
+  const int32_t block = mixllm::kv4_block_bytes(P, D);
+  const int32_t *table = a.table + b * a.ldt;
+  // Where this lane's part of a run is in a block, before the run's own offset.
+  const int32_t koff = n * (D / 2) + c * (D / 8), voff = P * (D / 2) + (c * 16 + n) * (D / 8);
+  const int32_t pword = lane & (32 * G - 1);  // dword of the run's parameters (D = 256: and the one 64 on)
+  const int32_t poff = P * D + pword / (16 * G) * (P * (D / 16)) + pword % (16 * G) * 4;
+  const int32_t poff2 = P * D + P * (D / 16) + pword % (16 * G) * 4;  // D = 256: the values' half
+  uint8_t *ring = smem + wave * kRing;
+
+  // Copies run x of the step at t0 into a stage; pg: its page, negative for none (then any
+  // memory of the cache is copied, to keep the number of instructions).
+  auto issue = [&](auto stage, int x, int32_t t0, int32_t pg) {
+    uint8_t *to_k = ring + decltype(stage)::value * S::kStage + x * S::kBytes, *to_v = to_k + 8 * D, *to_p = to_v + 8 * D;
+    pg = pg < 0 ? 0 : pg;
+    const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(a.cache) + ((int64_t)pg * a.hkv + h) * block, (short)0, block, kRsrcFlags);
+    const int32_t in = (t0 + kRun * x) & (P - 1), at = in * (D / 2);
+#pragma unroll
+    for (int e = 0; e < S::kCodes; ++e) {
+      if constexpr (D == 64) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 256), 4, koff + 4 * e, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 256), 4, voff + 4 * e, at, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 1024), 16, koff + 16 * e, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 1024), 16, voff + 16 * e, at, 0, 0);
+      }
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)to_p, 4, poff, in * (4 * G), 0, 0);
+    if constexpr (S::kPars == 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_p + 256), 4, poff2, in * (4 * G), 0, 0);
+  };
+  // This wave takes every fourth step, in batches whose pages one load fetches: lane
+  // kRuns * j + x has the page of run x of the batch's step j, negative for none.  The first
+  // batch's loads start before the query is looked at.
+  constexpr int32_t kStride4 = kWaves * S::kTokens, kBatch = 64 / S::kRuns;
+  int32_t tb = (from & ~(kRun - 1)) + wave * S::kTokens, steps = 0, pages = -1;
+  uint64_t there = 0;
+  auto start = [&](auto stage, int32_t j) {
+#pragma unroll
+    for (int x = 0; x < S::kRuns; ++x)
+      issue(stage, x, tb + j * kStride4, __builtin_amdgcn_readlane(pages, S::kRuns * j + x));
+  };
+  auto fetch = [&]() {  // for the batch at tb < to
+    const int32_t tok = tb + lane / S::kRuns * kStride4 + lane % S::kRuns * kRun;
+    pages = tok < to ? table[tok >> a.page_log2] : -1;
+    pages = (uint32_t)pages < (uint32_t)a.pages ? pages : -1;
+    there = __ballot(pages >= 0);
+    const int32_t left = (to - tb + kStride4 - 1) / kStride4;
+    steps = left < kBatch ? left : kBatch;
+    start(Const<0>(), 0);
+  };
+  if (tb < to) fetch();
+
   half8 q[V][W];
   float row_scale, qsum[G];
   {
-    uint4v raw[W];
     float top = 0.0f;
 #pragma unroll
     for (int s = 0; s < W; ++s) {
-      raw[s] = *reinterpret_cast<const uint4v *>(qp + 32 * s);
 #pragma unroll
       for (int w = 0; w < 4; ++w)
         top = fmaxf(top, fmaxf(fabsf(up<BF16>(raw[s][w] & 0xFFFFu)), fabsf(up<BF16>(raw[s][w] >> 16))));
@@ -296,38 +347,6 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   for (int g = 0; g < G; ++g) bias[g] = rest[g] = 0.0f;
   uint32_t vbits = 0;  // value scales up to this fp16 pattern fit k
 
-  const int32_t P = 1 << a.page_log2;
-  const int32_t block = mixllm::kv4_block_bytes(P, D);
-  const int32_t *table = a.table + b * a.ldt;
-  // Where this lane's part of a run is in a block, before the run's own offset.
-  const int32_t koff = n * (D / 2) + c * (D / 8), voff = P * (D / 2) + (c * 16 + n) * (D / 8);
-  const int32_t pword = lane & (32 * G - 1);  // dword of the run's parameters (D = 256: and the one 64 on)
-  const int32_t poff = P * D + pword / (16 * G) * (P * (D / 16)) + pword % (16 * G) * 4;
-  const int32_t poff2 = P * D + P * (D / 16) + pword % (16 * G) * 4;  // D = 256: the values' half
-  uint8_t *ring = smem + wave * kRing;
-
-  // Copies run x of the step at t0 into a stage; pg: its page, negative for none (then any
-  // memory of the cache is copied, to keep the number of instructions).
-  auto issue = [&](auto stage, int x, int32_t t0, int32_t pg) {
-    uint8_t *to_k = ring + decltype(stage)::value * S::kStage + x * S::kBytes, *to_v = to_k + 8 * D, *to_p = to_v + 8 * D;
-    pg = pg < 0 ? 0 : pg;
-    const Rsrc rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t *>(a.cache) + ((int64_t)pg * a.hkv + h) * block, (short)0, block, kRsrcFlags);
-    const int32_t in = (t0 + kRun * x) & (P - 1), at = in * (D / 2);
-#pragma unroll
-    for (int e = 0; e < S::kCodes; ++e) {
-      if constexpr (D == 64) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 256), 4, koff + 4 * e, at, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 256), 4, voff + 4 * e, at, 0, 0);
-      } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_k + e * 1024), 16, koff + 16 * e, at, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_v + e * 1024), 16, voff + 16 * e, at, 0, 0);
-      }
-    }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)to_p, 4, poff, in * (4 * G), 0, 0);
-    if constexpr (S::kPars == 2)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LdsPtr)(to_p + 256), 4, poff2, in * (4 * G), 0, 0);
-  };
   // This lane's dwords of key or value codes of a run.
   auto codes = [&](const uint8_t *src, uint32_t (&w)[W]) {
     if constexpr (D == 64) {
@@ -511,22 +530,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     }
   };
 
-  // This wave takes every fourth step, in batches whose pages one load fetches.
-  constexpr int32_t kStride4 = kWaves * S::kTokens, kBatch = 64 / S::kRuns;
-  for (int32_t tb = (from & ~(kRun - 1)) + wave * S::kTokens; tb < to; tb += kBatch * kStride4) {
-    int32_t pages = -1;
-    {
-      const int32_t tok = tb + lane / S::kRuns * kStride4 + lane % S::kRuns * kRun;
-      if (tok < to) pages = table[tok >> a.page_log2];
-      pages = (uint32_t)pages < (uint32_t)a.pages ? pages : -1;
-    }
-    const int32_t left = (to - tb + kStride4 - 1) / kStride4, steps = left < kBatch ? left : kBatch;
-    const uint64_t there = __ballot(pages >= 0);
-    auto start = [&](auto stage, int32_t j) {
-#pragma unroll
-      for (int x = 0; x < S::kRuns; ++x)
-        issue(stage, x, tb + j * kStride4, __builtin_amdgcn_readlane(pages, S::kRuns * j + x));
-    };
+  while (tb < to) {
     auto step = [&](auto stage, int32_t j) {
       if (j + 1 < steps) {
         wait_lds();  // the stage that is filled now was read in the last step
@@ -539,7 +543,6 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       compute(stage, tb + j * kStride4, (uint32_t)(there >> (S::kRuns * j)) & ((1u << S::kRuns) - 1));
       __builtin_amdgcn_sched_barrier(0);
     };
-    start(Const<0>(), 0);
     for (int32_t j = 0;;) {
       step(Const<0>(), j);
       if (++j == steps) break;
@@ -547,6 +550,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       if (++j == steps) break;
     }
     wait_lds();
+    tb += kBatch * kStride4;
+    if (tb < to) fetch();
   }
 
   // The columns' statistics and outputs; a row's are V columns of each wave.
@@ -636,13 +641,33 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   const float *ml = a.ws_ml + (part0 * a.tile_rows + row) * 2;
   const float *po = a.ws_o + (part0 * a.tile_rows + row) * D + lane * C;
   float m = 2.0f * kLow, l = 0.0f, o[C] = {};
-  for (int32_t s = wave % WAVES; s < nchunks; s += WAVES) {
-    const float ms = ml[(int64_t)s * a.tile_rows * 2], ls = ml[(int64_t)s * a.tile_rows * 2 + 1];
-    const float next = fmaxf(m, ms), f = __builtin_amdgcn_exp2f(m - next), fs = __builtin_amdgcn_exp2f(ms - next);
-    m = next;
-    l = fmaf(l, f, ls * fs);
+  const int32_t mine = (nchunks - wave % WAVES + WAVES - 1) / WAVES;  // chunks of this wave
+  for (int32_t j0 = 0; j0 < mine; j0 += 64) {
+    // 64 chunks' statistics at once, one per lane; then their outputs, whose loads do not wait
+    // for one another
+    const int32_t many = mine - j0 < 64 ? mine - j0 : 64;
+    float2v st = {2.0f * kLow, 0.0f};
+    if (lane < many)
+      st = *reinterpret_cast<const float2v *>(ml + (int64_t)(wave % WAVES + (j0 + lane) * WAVES) * a.tile_rows * 2);
+    float top = st.x;
 #pragma unroll
-    for (int e = 0; e < C; ++e) o[e] = fmaf(o[e], f, po[(int64_t)s * a.tile_rows * D + e] * fs);
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float next = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - next);
+    const float weight = __builtin_amdgcn_exp2f(st.x - next);
+    m = next;
+    float sum = st.y * weight;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    l = fmaf(l, f, sum);
+#pragma unroll
+    for (int e = 0; e < C; ++e) o[e] *= f;
+#pragma unroll 8
+    for (int32_t j = 0; j < many; ++j) {
+      const float *src = po + (int64_t)(wave % WAVES + (j0 + j) * WAVES) * a.tile_rows * D;
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
+#pragma unroll
+      for (int e = 0; e < C; ++e) o[e] = fmaf(src[e], w, o[e]);
+    }
   }
   if (WAVES > 1) {
     if (lane == 0) {
@@ -710,8 +735,8 @@ bool shape_ok(int64_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_
 }
 
 template <int D, bool BF16>
-void launch(const Args &a, int64_t blocks, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), threads(kThreads);
+void launch(const Args &a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
   if (D < 256 && a.tile_rows == 4)
     hipLaunchKernelGGL((kv4_attention_kernel<D, D < 256 ? 4 : 2, BF16>), grid, threads, 0, s, a);
   else if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attention_kernel<D, 2, BF16>), grid, threads, 0, s, a);
@@ -723,9 +748,9 @@ void launch(const Args &a, int64_t blocks, hipStream_t s) {
 }
 
 template <int D>
-void launch(const Args &a, int32_t dtype, int64_t blocks, hipStream_t s) {
-  if (dtype == MIXLLM_BF16) launch<D, true>(a, blocks, s);
-  else launch<D, false>(a, blocks, s);
+void launch(const Args &a, int32_t dtype, hipStream_t s) {
+  if (dtype == MIXLLM_BF16) launch<D, true>(a, s);
+  else launch<D, false>(a, s);
 }
 
 }  // namespace
@@ -760,7 +785,7 @@ extern "C" int mixllm_kv4_attention(const void *q, int64_t ldq, int32_t dtype, i
     return MIXLLM_E_SHAPE;
   const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
   const int64_t parts = (int64_t)B * k.tiles * kv_heads * k.splits;
-  if (parts > 0x7FFFFFFF || (int64_t)B * k.tiles > 0x7FFFFFFF || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
+  if (parts > 0x7FFFFFFF || B > 65535 || k.tiles > 65535 || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
     return MIXLLM_E_SHAPE;
   float *ws = static_cast<float *>(workspace);
   if (k.splits > 1) {
@@ -772,8 +797,8 @@ extern "C" int mixllm_kv4_attention(const void *q, int64_t ldq, int32_t dtype, i
                   ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
                   mixllm::log2_of(page), width, B, max_rows,
                   max_len, window, k.tiles, k.tile_rows, k.splits};
-  if (dim == 64) launch<64>(a, dtype, parts, (hipStream_t)stream);
-  else if (dim == 128) launch<128>(a, dtype, parts, (hipStream_t)stream);
-  else launch<256>(a, dtype, parts, (hipStream_t)stream);
+  if (dim == 64) launch<64>(a, dtype, (hipStream_t)stream);
+  else if (dim == 128) launch<128>(a, dtype, (hipStream_t)stream);
+  else launch<256>(a, dtype, (hipStream_t)stream);
   return mixllm::launch_status();
 }
