@@ -360,61 +360,92 @@ def mixllm_gemm_w4w8a8_partials(aq, sa, asum, rowop, m: int, n: int, k: int, n8:
 # ------------------------------------------------------------- between the packed layers
 
 FP16, BF16, FP32 = 0, 1, 2  # MIXLLM_FP16, MIXLLM_BF16, MIXLLM_FP32
+_f16, _bf16, _i32t, _u8t = ((torch.float16, torch.bfloat16, torch.int32, torch.uint8) if torch is not None
+                            else (None,) * 4)
+
+# These calls run once or more per layer and token: a call that needs no error costs one
+# comparison chain per tensor (about 0.3 us), the library call 1.2 us and the launch 3 us;
+# torch.cuda.current_stream() alone would add 2.7 us to that.
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None)
 
 
-def _type16(t, name):
+def _dtype16(t, name):
     """The library's number of a 16-bit element type."""
-    if t.dtype is torch.float16:
+    d = t.dtype
+    if d is _f16:
         return FP16
-    if t.dtype is torch.bfloat16:
+    if d is _bf16:
         return BF16
-    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {d}")
 
 
-def _rows(t, name, dtype, shape):
-    """The row stride of a [M, N] (or [M, heads, dim]) CUDA tensor with contiguous rows."""
-    if not t.is_cuda or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    if len(shape) == 2:
-        width = shape[1]
-        whole = st[1] == 1 or width == 1
+def _gpu(t, name):
+    """The index of the GPU a tensor is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _ld(t, name, dtype, dev, shape, width):
+    """The row stride of a tensor of this type, place and shape whose rows are contiguous."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        if t.is_contiguous():
+            return width
+        st, rows = t.stride(), shape[0]
+        whole = True
+        step = 1
+        for size, stride in zip(reversed(shape[1:]), reversed(st[1:])):
+            whole = whole and (size == 1 or stride == step)
+            step *= size
+        if whole and rows <= 1:
+            return width
+        if whole and st[0] >= width:
+            return st[0]
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, has strides {st}")
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, is {t.dtype} of shape "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _flat(t, name, dtype, dev, numel):
+    """The address of a contiguous tensor of at least `numel` elements."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {numel} elements on cuda:{dev}, is "
+                     f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
+
+
+def _table(t, b, dev):
+    """(address, row stride, width) of a page table of at least b rows."""
+    if t.dtype is _i32t and t.dim() == 2 and t.get_device() == dev:
+        rows, width = t.shape
+        if rows >= b:
+            if t.is_contiguous():
+                return t.data_ptr(), width, width
+            ld, one = t.stride()
+            if (width <= 1 or one == 1) and (rows <= 1 or ld >= width):
+                return t.data_ptr(), ld if rows > 1 else width, width
+    raise ValueError(f"table must be an int32 tensor [{b} or more, width] with contiguous rows on cuda:{dev}, is "
+                     f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
+
+
+def _on(dev, stream, fn, *args):
+    """Calls a device entry point with the stream last, on the tensors' device: by default its
+    current stream."""
+    if stream is not None:
+        stream = stream if isinstance(stream, int) else stream.cuda_stream
+    elif _raw_stream is not None:
+        stream = _raw_stream(dev)
     else:
-        width = shape[1] * shape[2]
-        whole = st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
-    if not whole:
-        raise ValueError(f"{name} must have contiguous rows")
-    if shape[0] <= 1:
-        return (width + 7) // 8 * 8
-    if st[0] < width:
-        raise ValueError(f"the rows of {name} overlap")
-    return st[0]
-
-
-def _ints(t, name, numel):
-    """An int32 CUDA tensor, contiguous, of at least `numel` elements."""
-    if not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < numel:
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of at least {numel} elements")
-    return t
-
-
-def _launch(fn, tensors, stream, *args):
-    """Calls a device entry point with the stream last, on the device of its tensors."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"the tensors are on different devices: {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if (_device() if _device is not None else torch.cuda.current_device()) == dev:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+            status = fn(*args, stream)
+    if status:
+        raise MixLLMError(status)
 
 
 def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=None, asum=None, rowop=None,
@@ -427,39 +458,41 @@ def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=N
     lead = x if x is not None else pre_weight
     if lead is None:
         raise ValueError("x or pre_weight is required")
-    dtype = _type16(lead, "x" if x is not None else "pre_weight")
+    dtype, t16 = _dtype16(lead, "x or pre_weight"), lead.dtype
+    dev = _gpu(res, "res")
     shape = res.shape
     if len(shape) != 2:
         raise ValueError("res must be 2-D")
     m, n = shape
-    t16 = lead.dtype
-    res_dtype = FP32 if res.dtype is torch.float32 else dtype
-    ldr = _rows(res, "res", torch.float32 if res_dtype == FP32 else t16, shape)
-    ldx = _rows(x, "x", t16, shape) if x is not None else 0
-    ldro = _rows(res_out, "res_out", res.dtype, shape) if res_out is not None else 0
-    ldy = _rows(y, "y", t16, shape) if y is not None else 0
-    ldgate = 0
+    tres, res_dtype = (t16, dtype) if res.dtype is t16 else (torch.float32, FP32)
+    ldr = _ld(res, "res", tres, dev, shape, n)
+    ldx = ldro = ldy = ldgate = 0
+    px = pro = py = pgate = ppost = ppre = paq = psa = psum = pro4 = None
+    if x is not None:
+        ldx, px = _ld(x, "x", t16, dev, shape, n), x.data_ptr()
+    if res_out is not None:
+        ldro, pro = _ld(res_out, "res_out", tres, dev, shape, n), res_out.data_ptr()
+    if y is not None:
+        ldy, py = _ld(y, "y", t16, dev, shape, n), y.data_ptr()
+    if post_weight is not None:
+        ppost = _flat(post_weight, "post_weight", t16, dev, n)
+    if pre_weight is not None:
+        ppre = _flat(pre_weight, "pre_weight", t16, dev, n)
     if gate is not None:
         if gate.dim() == 2:
-            ldgate = _rows(gate, "gate", t16, shape)
+            ldgate, pgate = _ld(gate, "gate", t16, dev, shape, n), gate.data_ptr()
         else:
-            _rows(gate.view(1, -1), "gate", t16, (1, n))
-    for w, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        if w is not None and (not w.is_cuda or w.dtype is not t16 or w.shape != (n,) or w.stride(0) != 1):
-            raise ValueError(f"{name} must be a contiguous [{n}] CUDA tensor of {t16}")
-    if aq is not None and m:
+            pgate = _flat(gate, "gate", t16, dev, n)
+    if aq is not None:
         g = n // GROUP
-        _need(aq, "aq", torch.int8, (m, n))
-        _need(sa, "sa", torch.float32, (g, m))
-        if asum is not None:
-            _need(asum, "asum", torch.int32, (g, m))
-        if rowop is not None:
-            _need(rowop, "rowop", torch.int32, (g, m, 8))
-        if aq.shape != (m, n) or sa.shape != (g, m):
+        paq = _flat(aq, "aq", torch.int8, dev, m * n)
+        if sa is None or aq.shape != shape or sa.shape != (g, m):
             raise ValueError(f"aq and sa must be [{m}, {n}] and [{g}, {m}]")
-    _launch(_lib.mixllm_residual_norm, (res, x, res_out, pre_weight, post_weight, gate, y, aq, sa, asum, rowop), stream,
-            _at(x), ldx, _at(post_weight), _at(gate), ldgate, _at(res), ldr, _at(res_out), ldro, _at(pre_weight),
-            _at(y), ldy, _at(aq), _at(sa), _at(asum), _at(rowop), m, n, GROUP, dtype, res_dtype, eps, alpha, beta)
+        psa = _flat(sa, "sa", torch.float32, dev, g * m)
+        psum = _flat(asum, "asum", _i32t, dev, g * m) if asum is not None else None
+        pro4 = _flat(rowop, "rowop", _i32t, dev, g * m * 8) if rowop is not None else None
+    _on(dev, stream, _lib.mixllm_residual_norm, px, ldx, ppost, pgate, ldgate, res.data_ptr(), ldr, pro, ldro, ppre, py,
+        ldy, paq, psa, psum, pro4, m, n, GROUP, dtype, res_dtype, eps, alpha, beta)
 
 
 def mixllm_kv4_page_bytes(page: int, heads: int, dim: int) -> int:
@@ -475,13 +508,14 @@ def kv4_cache(pages: int, page: int, heads: int, dim: int, device="cuda"):
 
 
 def _cache(cache, page, dim):
-    """(bytes, pages, heads) of a cache tensor for pages of `page` tokens and heads of `dim` channels."""
-    if not cache.is_cuda or cache.dtype is not torch.uint8 or cache.dim() != 3 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 CUDA tensor [pages, heads, block bytes]")
-    pages, heads, block = cache.shape
-    if block * 8 != page * dim * 9:
-        raise ValueError(f"cache has blocks of {block} bytes, page {page} and dim {dim} need {page * dim * 9 / 8:g}")
-    return pages * heads * block, pages, heads
+    """(device, address, bytes, pages, heads) of a cache for pages of `page` tokens and heads of
+    `dim` channels."""
+    if cache.dtype is _u8t and cache.dim() == 3 and cache.is_contiguous():
+        pages, heads, block = cache.shape
+        if block * 8 == page * dim * 9:
+            return _gpu(cache, "cache"), cache.data_ptr(), pages * heads * block, pages, heads
+    raise ValueError(f"cache must be a contiguous uint8 tensor [pages, heads, {page * dim * 9 / 8:g}] for page {page} and "
+                     f"dim {dim}, is {cache.dtype} of shape {tuple(cache.shape)}")
 
 
 def mixllm_kv_plan(fresh, lens, table, pool, count, page: int, pages: int, lens_out, count_out, cu, slots, pos,
@@ -489,45 +523,39 @@ def mixllm_kv_plan(fresh, lens, table, pool, count, page: int, pages: int, lens_
     """The page tables and slot maps of a step from request lengths, on the GPU: fresh, lens,
     lens_out: int32 [B]; table: int32 [B, width] (rows may be strided); pool: int32 [F]; count:
     int32 [1 or more]; count_out: int32 [2]; cu: int32 [B + 1]; slots, pos: int32 [tokens]."""
-    b = fresh.shape[0]
-    if table.dim() != 2 or table.shape[0] != b or not table.is_cuda or table.dtype is not torch.int32 or (
-            table.numel() and table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be an int32 CUDA tensor [{b}, width] with contiguous rows")
-    width = table.shape[1]
-    for t, name, size in ((fresh, "fresh", b), (lens, "lens", b), (count, "count", 1), (lens_out, "lens_out", b),
-                          (count_out, "count_out", 2), (cu, "cu", b + 1), (pool, "pool", 0),
-                          (pos, "pos", slots.shape[0]), (slots, "slots", 0)):
-        _ints(t, name, size)
-    if b > 1 and table.stride(0) < width:
-        raise ValueError("the rows of table overlap")
-    _launch(_lib.mixllm_kv_plan, (fresh, lens, table, pool, count, lens_out, count_out, cu, slots, pos), stream,
-            fresh.data_ptr(), lens.data_ptr(), b, table.data_ptr(), table.stride(0) if b > 1 else width, width,
-            pool.data_ptr(), pool.numel(), count.data_ptr(), page, pages, lens_out.data_ptr(), count_out.data_ptr(),
-            cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), slots.shape[0])
+    b, tokens = fresh.numel(), slots.numel()
+    dev = _gpu(fresh, "fresh")
+    ptable, ldt, width = _table(table, b, dev)
+    _on(dev, stream, _lib.mixllm_kv_plan, _flat(fresh, "fresh", _i32t, dev, 0), _flat(lens, "lens", _i32t, dev, b), b,
+        ptable, ldt, width, _flat(pool, "pool", _i32t, dev, 0), pool.numel(), _flat(count, "count", _i32t, dev, 1), page,
+        pages, _flat(lens_out, "lens_out", _i32t, dev, b), _flat(count_out, "count_out", _i32t, dev, 2),
+        _flat(cu, "cu", _i32t, dev, b + 1), _flat(slots, "slots", _i32t, dev, 0), _flat(pos, "pos", _i32t, dev, tokens),
+        tokens)
 
 
 def mixllm_kv4_append(k, v, slots, cache, page: int, stream=None):
     """Writes k and v ([T, heads, dim] fp16 or bf16, rows may be strided) into the cache at
     slots (int32 [T], negative: skip the row)."""
-    t, _, dim = k.shape
-    size, pages, heads = _cache(cache, page, dim)
-    dtype, shape = _type16(k, "k"), (t, heads, dim)
-    ldk, ldv = _rows(k, "k", k.dtype, shape), _rows(v, "v", k.dtype, shape)
-    _ints(slots, "slots", t)
-    _launch(_lib.mixllm_kv4_append, (cache, k, v, slots), stream, k.data_ptr(), ldk, v.data_ptr(), ldv, dtype,
-            slots.data_ptr(), t, cache.data_ptr(), size, pages, page, heads, dim)
+    t, _, dim = shape = k.shape
+    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dtype, t16, width = _dtype16(k, "k"), k.dtype, heads * dim
+    if shape[1] != heads:
+        raise ValueError(f"k has {shape[1]} heads, the cache {heads}")
+    _on(dev, stream, _lib.mixllm_kv4_append, k.data_ptr(), _ld(k, "k", t16, dev, shape, width), v.data_ptr(),
+        _ld(v, "v", t16, dev, shape, width), dtype, _flat(slots, "slots", _i32t, dev, t), t, pcache, size, pages, page,
+        heads, dim)
 
 
 def mixllm_kv4_read(cache, slots, k, v, page: int, stream=None):
     """The values of the tokens at slots (int32 [T]) into k and v ([T, heads, dim] fp16 or
     bf16); rows with a negative slot are left as they were."""
-    t, _, dim = k.shape
-    size, pages, heads = _cache(cache, page, dim)
-    dtype, shape = _type16(k, "k"), (t, heads, dim)
-    ldk, ldv = _rows(k, "k", k.dtype, shape), _rows(v, "v", k.dtype, shape)
-    _ints(slots, "slots", t)
-    _launch(_lib.mixllm_kv4_read, (cache, k, v, slots), stream, cache.data_ptr(), size, pages, page, heads, dim,
-            slots.data_ptr(), t, k.data_ptr(), ldk, v.data_ptr(), ldv, dtype)
+    t, _, dim = shape = k.shape
+    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dtype, t16, width = _dtype16(k, "k"), k.dtype, heads * dim
+    if shape[1] != heads:
+        raise ValueError(f"k has {shape[1]} heads, the cache {heads}")
+    _on(dev, stream, _lib.mixllm_kv4_read, pcache, size, pages, page, heads, dim, _flat(slots, "slots", _i32t, dev, t), t,
+        k.data_ptr(), _ld(k, "k", t16, dev, shape, width), v.data_ptr(), _ld(v, "v", t16, dev, shape, width), dtype)
 
 
 def mixllm_kv4_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
@@ -542,26 +570,24 @@ def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: in
     [B + 1] first row of each request; out: as q; lse: fp32 [T, q_heads] or None; scale: 1 /
     sqrt(dim) by default; workspace: a uint8 tensor of mixllm_kv4_attention_workspace_bytes(T,
     B, ..) for the same arguments (None where that is 0)."""
-    t, hq, dim = q.shape
-    size, pages, heads = _cache(cache, page, dim)
-    dtype = _type16(q, "q")
-    ldq, ldo = _rows(q, "q", q.dtype, q.shape), _rows(out, "out", q.dtype, q.shape)
-    b = lens.shape[0]
-    if table.dim() != 2 or table.shape[0] < b or not table.is_cuda or table.dtype is not torch.int32 or (
-            table.numel() and table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be an int32 CUDA tensor [{b}, width] with contiguous rows")
-    _ints(lens, "lens", b)
-    _ints(cu, "cu", b + 1)
-    width = table.shape[1]
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (t, hq) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous fp32 tensor [{t}, {hq}]")
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _launch(_lib.mixllm_kv4_attention, (q, cache, table, lens, cu, out, lse, workspace), stream, q.data_ptr(), ldq,
-            dtype, t, hq, cache.data_ptr(), size, pages, page, heads, dim, table.data_ptr(),
-            table.stride(0) if table.shape[0] > 1 else width, width, lens.data_ptr(), cu.data_ptr(), b, max_rows,
-            max_len, dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo, _at(lse), _at(workspace), ws)
+    t, hq, dim = shape = q.shape
+    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dtype, t16, width = _dtype16(q, "q"), q.dtype, hq * dim
+    b = lens.numel()
+    ptable, ldt, tw = _table(table, b, dev)
+    plse = pws = None
+    ws = 0
+    if lse is not None:
+        plse = _flat(lse, "lse", torch.float32, dev, t * hq)
+        if lse.shape != (t, hq):
+            raise ValueError(f"lse must be [{t}, {hq}], is {tuple(lse.shape)}")
+    if workspace is not None:
+        ws = workspace.numel()
+        pws = _flat(workspace, "workspace", _u8t, dev, 0)
+    _on(dev, stream, _lib.mixllm_kv4_attention, q.data_ptr(), _ld(q, "q", t16, dev, shape, width), dtype, t, hq, pcache,
+        size, pages, page, heads, dim, ptable, ldt, tw, _flat(lens, "lens", _i32t, dev, 0),
+        _flat(cu, "cu", _i32t, dev, b + 1), b, max_rows, max_len, dim ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), _ld(out, "out", t16, dev, shape, width), plse, pws, ws)
 
 
 def rowop_buffer(m: int, k: int, device="cuda"):
