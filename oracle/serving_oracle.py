@@ -26,7 +26,7 @@ def kv4_quant(x):
     x = np.clip(np.where(np.isnan(x), np.float32(0), x), np.float32(-65504), np.float32(65504))
     g = x.reshape(*x.shape[:-1], x.shape[-1] // 64, 64)
     lo, hi = g.min(-1), g.max(-1)
-    m = lo.astype(np.float16)
+    m = (lo + np.float32(0)).astype(np.float16)          # -0 becomes 0
     s = ((hi - lo) / np.float32(15)).astype(np.float16)
     s = np.where((s == 0) & (hi > lo), np.float16(2.0 ** -24), s)
     sf, mf = s.astype(np.float32)[..., None], m.astype(np.float32)[..., None]

@@ -15,9 +15,10 @@ namespace {
 //
 // Everything is a prefix sum over the requests (pages given back, pages needed, tokens
 // added) and then a scatter of independent items.  The traffic is a few bytes per request
-// and 8 bytes per token, so the time is latency: the sums run in one workgroup, whose
-// threads also move the pages (found by bisection in the prefix sums held in LDS, so one
-// long request's pages spread over all threads).
+// and 8 bytes per token, so the time is latency: the sums run in one workgroup, all of them
+// at once and across lanes without LDS, and its threads also move the pages.  256 requests of
+// one token: 5.1 us (the sums one after the other through LDS shuffles: 14.0 us; a launch
+// alone takes about 4).
 // ---------------------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
@@ -30,32 +31,68 @@ struct PlanArgs {
   int32_t B, width, F, page_log2, pages, tokens;
 };
 
-// Inclusive sum over a wave's lanes.
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(v, d);
-    if ((int)(threadIdx.x & 63) >= d) v += u;
-  }
+// Inclusive sum over the lanes of a wave: within rows of 16 lanes, then the rows' last
+// lanes into the rows behind them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t shifted(int32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int32_t row_scan(int32_t v) {
+  v += shifted<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  return v;
+}
+__device__ __forceinline__ int32_t wave_scan(int32_t v) {
+  v = row_scan(v);
+  v += shifted<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+  v += shifted<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
   return v;
 }
 
-// Exclusive sum over the workgroup; `total` gets the sum of all.  `tmp`: kPlanWaves words.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *tmp, int64_t *total) {
-  const int wave = threadIdx.x >> 6;
-  const int64_t inc = wave_scan(v);
-  __syncthreads();  // tmp may still be read from the last call
-  if ((threadIdx.x & 63) == 63) tmp[wave] = inc;
+// A request of this step.
+struct Request {
+  int32_t held, add, have, need;  // tokens, tokens to add, pages, more pages
+  bool ended, fits;
+};
+
+__device__ __forceinline__ Request request_of(const PlanArgs &a, int32_t b) {
+  const int32_t cap = a.width << a.page_log2, page = 1 << a.page_log2;  // fits: checked on the host
+  const int32_t f = b < a.B ? a.fresh[b] : 0, len = b < a.B ? a.lens[b] : 0;
+  Request r;
+  r.held = len < 0 ? 0 : len < cap ? len : cap;
+  r.add = f > 0 ? f : 0;
+  r.ended = f < 0;
+  r.fits = r.add <= cap - r.held;
+  r.have = (int32_t)(((uint32_t)r.held + page - 1) >> a.page_log2);
+  r.need = r.ended || !r.fits ? 0 : (int32_t)(((uint32_t)(r.held + r.add) + page - 1) >> a.page_log2) - r.have;
+  return r;
+}
+
+// Sums over the requests before this one and over all of the workgroup's: pages given back,
+// pages needed, and the tokens added in two halves (their sum may pass 32 bits).
+struct Sums {
+  int32_t back, need, low, high;
+  __device__ __forceinline__ int64_t add() const { return ((int64_t)high << 16) + low; }
+};
+
+// `tmp`: a word per wave and sum, last read before the caller's next barrier.
+__device__ __forceinline__ Sums block_scan(const Request &r, Sums *tmp, Sums *total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Sums own = {r.ended ? r.have : 0, r.need, r.add & 0xFFFF, r.add >> 16};
+  const Sums inc = {wave_scan(own.back), wave_scan(own.need), wave_scan(own.low), wave_scan(own.high)};
+  if (lane == 63) tmp[wave] = inc;
   __syncthreads();
-  int64_t base = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) {
-    const int64_t t = tmp[w];
-    if (w < wave) base += t;
-    sum += t;
-  }
-  *total = sum;
-  return base + inc - v;
+  // each row of 16 lanes sums the waves' totals
+  Sums w = tmp[lane & 15];
+  const Sums mine = w;
+  w = {row_scan(w.back), row_scan(w.need), row_scan(w.low), row_scan(w.high)};
+  auto at = [](int32_t v, int l) { return __builtin_amdgcn_readlane(v, l); };
+  *total = {at(w.back, 15), at(w.need, 15), at(w.low, 15), at(w.high, 15)};
+  const int u = __builtin_amdgcn_readfirstlane(wave);
+  return {at(w.back - mine.back, u) + inc.back - own.back, at(w.need - mine.need, u) + inc.need - own.need,
+          at(w.low - mine.low, u) + inc.low - own.low, at(w.high - mine.high, u) + inc.high - own.high};
 }
 
 // Last index i of [0, n) with first[i] <= k (first ascending, first[0] <= k).
@@ -68,8 +105,7 @@ __device__ __forceinline__ int find(const int32_t *first, int n, int32_t k) {
   return lo;
 }
 
-__device__ __forceinline__ int32_t slot_of(const PlanArgs &a, int b, int32_t p) {
-  const int32_t pg = a.table[b * a.ldt + (p >> a.page_log2)];
+__device__ __forceinline__ int32_t slot_on(const PlanArgs &a, int32_t pg, int32_t p) {
   return (uint32_t)pg < (uint32_t)a.pages ? (pg << a.page_log2) + (p & ((1 << a.page_log2) - 1)) : -1;
 }
 
@@ -77,7 +113,7 @@ __device__ __forceinline__ int32_t slot_of(const PlanArgs &a, int b, int32_t p) 
 // each request, which the sums' kernel wrote: the position of a token is that of its
 // request's first one plus its distance from it, and a request without a slot for its first
 // token has none for the others.
-__device__ __forceinline__ void plan_tokens(const PlanArgs &a, int32_t t0, int32_t step) {
+__device__ __forceinline__ void plan_tokens(const PlanArgs &a, const int32_t *cu, int32_t t0, int32_t step) {
   const int32_t total = a.cu[a.B];
   for (int64_t t = t0; t < a.tokens; t += step) {
     if (t >= total) {
@@ -85,105 +121,124 @@ __device__ __forceinline__ void plan_tokens(const PlanArgs &a, int32_t t0, int32
       a.pos[t] = 0;
       continue;
     }
-    const int b = find(a.cu, a.B, (int32_t)t);
-    const int32_t first = a.cu[b];
+    const int b = find(cu, a.B, (int32_t)t);
+    const int32_t first = cu[b];
     if (t == first) continue;
     const int32_t p = a.pos[first] + ((int32_t)t - first);
     a.pos[t] = p;
-    a.slots[t] = a.slots[first] < 0 ? -1 : slot_of(a, b, p);
+    a.slots[t] = a.slots[first] < 0 ? -1 : slot_on(a, a.table[b * a.ldt + (p >> a.page_log2)], p);
   }
 }
 
 template <bool TOKENS>
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
-  __shared__ int64_t tmp[kPlanWaves];
-  __shared__ int32_t first[kPlanThreads], from[kPlanThreads], many[kPlanThreads];
+  __shared__ Sums tmp[2][kPlanWaves];
+  __shared__ int32_t first[kPlanThreads], cu[kPlanThreads];
+  __shared__ int32_t s_taken, s_refused;
   const int tid = threadIdx.x;
-  const int32_t cap = a.width << a.page_log2, page = 1 << a.page_log2;  // fits: checked on the host
+  if (tid == 0) s_taken = s_refused = 0;  // read after the first barrier
   int32_t count = *a.count;
   count = count < 0 ? 0 : count > a.F ? a.F : count;
+  Request r = request_of(a, tid);
+  // the page that the request's next token goes to, if the request has it
+  int32_t tail = -1;
+  if (r.add > 0 && r.held < r.have << a.page_log2) tail = a.table[tid * a.ldt + r.have - 1];
 
   // Pages of requests that ended go on top of the free ones, in the order of the requests.
+  Sums sum;
+  Sums pre = block_scan(r, tmp[0], &sum);
+  const Sums sum0 = sum;
   int64_t given = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + tid, n = a.B - b0 < kPlanThreads ? a.B - b0 : kPlanThreads;
-    int32_t have = 0;
-    if (b < a.B && a.fresh[b] < 0) {
-      const int32_t held = a.lens[b] < 0 ? 0 : a.lens[b] < cap ? a.lens[b] : cap;
-      have = (int32_t)(((uint32_t)held + page - 1) >> a.page_log2);
-    }
-    int64_t sum;
-    first[tid] = (int32_t)block_scan(have, tmp, &sum);
+  for (int b0 = 0;;) {
+    const int n = a.B - b0 < kPlanThreads ? a.B - b0 : kPlanThreads;
+    const int32_t back = b0 ? block_scan(request_of(a, b0 + tid), tmp[1], &sum).back : pre.back;
+    first[tid] = back;
     __syncthreads();
-    for (int32_t k = tid; k < sum; k += kPlanThreads) {
+    for (int32_t k = tid; k < sum.back; k += kPlanThreads) {
       const int i = find(first, n, k);
       const int64_t at = count + given + k;
       if (at < a.F) a.pool[at] = a.table[(int64_t)(b0 + i) * a.ldt + (k - first[i])];
     }
-    given += sum;
-    __syncthreads();
+    given += sum.back;
+    __syncthreads();  // the pool is complete, and first free
+    if ((b0 += kPlanThreads) >= a.B) break;
   }
   const int32_t top = (int32_t)(count + given < a.F ? count + given : a.F);
 
   // New pages come from the top, request by request; from the first request on that the
   // pool cannot serve, none that needs a page gets one.
   int64_t needed = 0, rows = 0;
-  int32_t taken = 0, refused = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + tid, n = a.B - b0 < kPlanThreads ? a.B - b0 : kPlanThreads;
+  bool more = false;  // a request has more than one token
+  sum = sum0;
+  for (int b0 = 0;;) {
+    const int b = b0 + tid;
     const bool in = b < a.B;
-    const int32_t f = in ? a.fresh[b] : 0;
-    const int32_t len = in ? a.lens[b] : 0;
-    const int32_t held = len < 0 ? 0 : len < cap ? len : cap;
-    const int32_t add = f > 0 ? f : 0;
-    const bool ended = f < 0, fits = add <= cap - held;
-    const int32_t have = (int32_t)(((uint32_t)held + page - 1) >> a.page_log2);
-    const int32_t need = ended || !fits ? 0 : (int32_t)(((uint32_t)(held + add) + page - 1) >> a.page_log2) - have;
-    int64_t sum, sum_add;
-    const int64_t pre = needed + block_scan(need, tmp, &sum);
-    const int64_t row = rows + block_scan(add, tmp, &sum_add);
-    const bool ok = ended || (fits && (need == 0 || pre + need <= top));
-    first[tid] = (int32_t)(pre - needed);
-    from[tid] = have;
-    many[tid] = ok ? need : 0;
-    if (ok && need > 0) taken = (int32_t)(pre + need);
+    if (b0) {
+      r = request_of(a, b);
+      tail = r.add > 0 && r.held < r.have << a.page_log2 ? a.table[b * a.ldt + r.have - 1] : -1;
+      pre = block_scan(r, tmp[0], &sum);
+    }
+    const int64_t before = needed + pre.need, row = rows + pre.add();
+    const bool ok = r.ended || (r.fits && (r.need == 0 || before + r.need <= top));
     if (in) {
-      refused += !ok;
-      a.lens_out[b] = ended ? 0 : ok ? held + add : held;
-      a.cu[b] = (int32_t)(row < 0x7FFFFFFF ? row : 0x7FFFFFFF);
+      const int32_t at = (int32_t)(row < 0x7FFFFFFF ? row : 0x7FFFFFFF);
+      if (ok && r.need > 0) atomicMax(&s_taken, (int32_t)(before + r.need));
+      if (!ok) atomicAdd(&s_refused, 1);
+      a.lens_out[b] = r.ended ? 0 : ok ? r.held + r.add : r.held;
+      a.cu[b] = at;
+      if (TOKENS && b0 == 0) cu[tid] = at;
+      more = more || r.add > 1;
+      if (r.add > 0 && row < a.tokens) {
+        const bool fresh_page = r.held == r.have << a.page_log2;  // it starts a page
+        a.pos[row] = r.held;
+        a.slots[row] = !ok ? -1 : slot_on(a, fresh_page ? a.pool[top - 1 - before] : tail, r.held);
+      }
     }
+    // A wave hands out its 64 requests' pages: one page by the request's own thread, more by
+    // all lanes, request after request (a bisection in the prefix sums for every page of the
+    // workgroup took 4 us longer at 5100 pages).
+    const int32_t gets = ok ? r.need : 0;
+    if (gets == 1) a.table[b * a.ldt + r.have] = a.pool[top - 1 - before];
+    for (uint64_t left = __ballot(gets > 1); left; left &= left - 1) {
+      const int l = __builtin_ctzll(left);
+      const int32_t pages = __builtin_amdgcn_readlane(gets, l), have = __builtin_amdgcn_readlane(r.have, l);
+      const int32_t from = top - 1 - __builtin_amdgcn_readlane((int32_t)before, l);  // it gets pages: that fits
+      int32_t *row = a.table + (int64_t)(b0 + (tid & ~63) + l) * a.ldt + have;
+      for (int32_t j0 = tid & 63; j0 < pages; j0 += 256) {
+        int32_t pg[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j0 + 64 * u < pages) pg[u] = a.pool[from - j0 - 64 * u];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j0 + 64 * u < pages) row[j0 + 64 * u] = pg[u];
+      }
+    }
+    needed += sum.need;
+    rows += sum.add();
     __syncthreads();
-    for (int32_t k = tid; k < sum; k += kPlanThreads) {
-      const int i = find(first, n, k);
-      if (k - first[i] < many[i])
-        a.table[(int64_t)(b0 + i) * a.ldt + from[i] + (k - first[i])] = a.pool[top - 1 - needed - k];
-    }
-    needed += sum;
-    rows += sum_add;
-    __syncthreads();  // the pages above are in the table before the slots read it
-    if (in && add > 0 && row < a.tokens) {
-      a.pos[row] = held;
-      a.slots[row] = ok ? slot_of(a, b, held) : -1;
-    }
+    if ((b0 += kPlanThreads) >= a.B) break;
   }
-  if (tid == 0) a.cu[a.B] = (int32_t)(rows < 0x7FFFFFFF ? rows : 0x7FFFFFFF);
-  int64_t out;
-  block_scan(refused, tmp, &out);
-  // taken is the same prefix sum in every thread that has one: the largest is the last
-  __syncthreads();
-  if (tid == 0) first[0] = 0;
-  __syncthreads();
-  atomicMax(&first[0], taken);
-  __syncthreads();
+  const int32_t total = (int32_t)(rows < 0x7FFFFFFF ? rows : 0x7FFFFFFF);
   if (tid == 0) {
-    a.count_out[0] = top - first[0];
-    a.count_out[1] = (int32_t)out;
+    a.cu[a.B] = total;
+    a.count_out[0] = top - s_taken;
+    a.count_out[1] = s_refused;
   }
-  if (TOKENS) plan_tokens(a, tid, kPlanThreads);
+  if (TOKENS) {
+    if (__syncthreads_or(more)) {
+      plan_tokens(a, a.B <= kPlanThreads ? cu : a.cu, tid, kPlanThreads);
+    } else {  // every row is its request's first
+      for (int64_t t = total + tid; t < a.tokens; t += kPlanThreads) {
+        a.slots[t] = -1;
+        a.pos[t] = 0;
+      }
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void plan_tokens_kernel(PlanArgs a) {
-  plan_tokens(a, (int32_t)(blockIdx.x * 256 + threadIdx.x), (int32_t)(gridDim.x * 256));
+  plan_tokens(a, a.cu, (int32_t)(blockIdx.x * 256 + threadIdx.x), (int32_t)(gridDim.x * 256));
 }
 
 // Up to this many token rows the sums' workgroup writes them itself.
@@ -193,10 +248,12 @@ constexpr int32_t kPlanOneLaunch = 4096;
 // The write and the read back.
 //
 // A quarter wave (16 lanes) owns one head of one token; a wave owns one head of four
-// consecutive rows.  Keys: lane i holds channels i * D/16 .. (one wide load), the minimum
-// and maximum of a group of 64 go over 64 / (D/16) lanes.  Values: lane n holds channels
-// 16 j + n, so its word is complete and the four quarters' words of consecutive tokens are
-// neighbours in the cache.
+// consecutive rows.  Lane i loads channels i * D/16 .. at once, the minimum and maximum of a
+// group of 64 go over 64 / (D/16) lanes.  Keys are stored from there; the values' codes change
+// places through LDS so that lane n has channels 16 j + n: its word is then complete, and the
+// four quarters' words of consecutive tokens are neighbours in the cache.  Long prompts are
+// bound by the vector units: 8191 tokens of 8 heads of 128 take 18.5 us with divisions and
+// fp32 extremes, 15.3 as written (12 of it without any store); reading them back takes 8.8.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kDppXor1 = 0xB1;        // quad_perm [1, 0, 3, 2]
@@ -207,6 +264,11 @@ constexpr int kDppMirror = 0x140;
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
 }
 
 // Minimum and maximum over LANES (4, 8 or 16) neighbouring lanes of a quarter.
@@ -245,24 +307,89 @@ __device__ __forceinline__ float tame(float x) {
 }
 
 struct Group {
-  float s, m;
+  float s, m, r;  // r: about 1 / s, 0 where s is
   uint32_t s16, m16;
 };
 
-// Scale and minimum of a group, every step in fp32 with IEEE division, stored as fp16.
+// Scale and minimum of a group, every step in fp32 with IEEE division, stored as fp16.  The
+// division by 15 in three steps: q = x RN(1 / 15), then q plus the rounded remainder times
+// RN(1 / 15), which is the correctly rounded quotient (so for every fp32 mantissa, tried one by
+// one; quotients too small for that round to 0 in fp16).
 __device__ __forceinline__ Group group_of(float lo, float hi) {
   Group g;
-  g.m16 = from_f32<false>(lo);
-  g.s16 = from_f32<false>((hi - lo) / 15.0f);
+  g.m16 = from_f32<false>(lo + 0.0f);  // -0 becomes 0
+  const float x = hi - lo, q = x * (1.0f / 15.0f);
+  g.s16 = from_f32<false>(fmaf(fmaf(-15.0f, q, x), 1.0f / 15.0f, q));
   if (g.s16 == 0 && hi > lo) g.s16 = 1;  // 2^-24
   g.m = to_f32<false>(g.m16);
   g.s = to_f32<false>(g.s16);
+  g.r = g.s16 ? __builtin_amdgcn_rcpf(g.s) : 0.0f;
   return g;
 }
 
-__device__ __forceinline__ uint32_t code_of(float x, const Group &g) {
-  if (g.s16 == 0) return 0;
-  return (uint32_t)fminf(fmaxf(__builtin_rintf((x - g.m) / g.s), 0.0f), 15.0f);
+typedef int16_t short2v __attribute__((ext_vector_type(2)));
+
+// A lane's C 16-bit values, of a group that LANES neighbouring lanes hold: the values as fp32
+// and the group's parameters.  The extremes are found on the 16-bit patterns, two at a time,
+// made to order as integers (the bits below a set sign flipped); across lanes the maximum and
+// the complement of the minimum move as one word.  Where the extremes are not finite (or
+// beyond fp16) the group's values are tamed first.
+template <int C, int LANES, bool BF16>
+__device__ __forceinline__ Group measure(const uint32_t (&raw)[C / 2], float (&x)[C]) {
+  short2v hi = {-32768, -32768}, lo = {32767, 32767};
+#pragma unroll
+  for (int j = 0; j < C / 2; ++j) {
+    const short2v w = __builtin_bit_cast(short2v, raw[j]);
+    const short2v key = w ^ ((w >> 15) & short2v{32767, 32767});
+    hi = __builtin_elementwise_max(hi, key);
+    lo = __builtin_elementwise_min(lo, key);
+    x[2 * j] = to_f32<BF16>(raw[j] & 0xFFFFu);
+    x[2 * j + 1] = to_f32<BF16>(raw[j] >> 16);
+  }
+  const int16_t top = hi.x > hi.y ? hi.x : hi.y, low = lo.x < lo.y ? lo.x : lo.y;
+  short2v both = {top, (int16_t)~low};
+  auto merge = [&](uint32_t other) { both = __builtin_elementwise_max(both, __builtin_bit_cast(short2v, other)); };
+  merge(moved<kDppXor1>(__builtin_bit_cast(uint32_t, both)));
+  merge(moved<kDppXor2>(__builtin_bit_cast(uint32_t, both)));
+  if (LANES >= 8) merge(moved<kDppHalfMirror>(__builtin_bit_cast(uint32_t, both)));
+  if (LANES >= 16) merge(moved<kDppMirror>(__builtin_bit_cast(uint32_t, both)));
+  const int16_t last = BF16 ? 0x477F : 0x7BFF;  // the largest pattern up to 65504
+  if (both.x > last || both.y > last) {
+    float l = INFINITY, h = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      x[j] = tame(x[j]);
+      l = fminf(l, x[j]);
+      h = fmaxf(h, x[j]);
+    }
+    lanes_minmax<LANES>(l, h);
+    return group_of(l, h);
+  }
+  const short2v ends = {both.x, (int16_t)~both.y};
+  const uint32_t w = __builtin_bit_cast(uint32_t, ends ^ ((ends >> 15) & short2v{32767, 32767}));
+  return group_of(to_f32<BF16>(w >> 16), to_f32<BF16>(w & 0xFFFFu));
+}
+
+// rne((x - m) / s) without a division: the quotient is below 32 (15, more where s is a
+// subnormal that was rounded down), so the product with v_rcp_f32's value (within 1 ulp) is
+// within 32 (2^-23 + 2^-24) of it, and its rounded value within another 32 2^-24: both round to
+// the same integer unless the product lies within 2^-16 of a half-integer, where the IEEE
+// division decides, for the lane's whole set.
+template <int C>
+__device__ __forceinline__ void codes_of(const float *x, const Group &g, uint32_t *c) {
+  float v[C], off = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const float t = (x[j] - g.m) * g.r;
+    v[j] = __builtin_rintf(t);
+    off = fmaxf(off, fabsf(t - v[j]));
+  }
+  if (off > 0.5f - 0x1p-16f) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = __builtin_rintf((x[j] - g.m) / g.s);
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) c[j] = (uint32_t)__builtin_amdgcn_fmed3f(v[j], 0.0f, 15.0f);
 }
 
 struct TokenArgs {
@@ -292,33 +419,60 @@ __device__ __forceinline__ int key_byte(int i) {
   return (i & 1) * 2 * (D / 8) + (i >> 1) * 4;  // D = 256: this dword and the one D/8 bytes on
 }
 
+// C 16-bit values from one 16-byte (C = 4: 8-byte) aligned place to another.
+template <int C>
+__device__ __forceinline__ void copy16(uint16_t *to, const uint16_t *from) {
+  if (C == 4) *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(from);
+  if (C >= 8) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+  if (C == 16) *reinterpret_cast<uint4 *>(to + 8) = *reinterpret_cast<const uint4 *>(from + 8);
+}
+
+// Between what the lanes of a quarter write to LDS and what others of them read: a wave's
+// LDS operations are done in order, so only the compiler has to be held.
+__device__ __forceinline__ void in_quarter() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void kv4_append_kernel(TokenArgs a) {
   constexpr int C = D / 16, G = D / 64;
-  const int i = threadIdx.x & 15;
-  const int32_t row = blockIdx.x * 16 + (threadIdx.x >> 4), head = blockIdx.y;
+  // a quarter's codes of values on the way from the lanes that hold a group to those that hold
+  // a column
+  __shared__ __attribute__((aligned(16))) uint8_t turn[16][D];
+  const int i = threadIdx.x & 15, quarter = threadIdx.x >> 4;
+  const int32_t group = blockIdx.x / a.heads, head = blockIdx.x - group * a.heads, row = group * 16 + quarter;
+  if (row >= a.T) return;  // whole quarters leave: the lane moves and LDS below stay inside a quarter
+  alignas(16) uint32_t raw[C / 2], raw_v[C / 2];
+  // loaded beside the slot, not after it
+  copy16<C>(reinterpret_cast<uint16_t *>(raw), a.k + (int64_t)row * a.ldk + head * D + i * C);
+  copy16<C>(reinterpret_cast<uint16_t *>(raw_v), a.v + (int64_t)row * a.ldv + head * D + i * C);
   int32_t tok = 0;
   uint8_t *blk = block_of<D>(a, row, head, tok);
-  if (!blk) return;  // whole quarters leave: the lane moves below stay inside a quarter
+  if (!blk) return;
+  constexpr int L = 64 / C;  // lanes of a group
   float x[C];
   uint32_t c[C];
+  // Lane 0 writes all groups' parameters: group e's are in lanes e L .., row_ror 16 - e L brings
+  // them to lane 0.
+  auto store = [&](uint8_t *to, uint32_t s16, uint32_t m16) {
+    const uint32_t own = s16 | m16 << 16;
+    uint32_t all[4] = {own, 0, 0, 0};
+    if (G == 2) all[1] = moved<0x128>(own);
+    if (G == 4) all[1] = moved<0x12C>(own), all[2] = moved<0x128>(own), all[3] = moved<0x124>(own);
+    auto lows = [](uint32_t u, uint32_t v) { return __builtin_amdgcn_perm(v, u, 0x05040100u); };
+    auto highs = [](uint32_t u, uint32_t v) { return __builtin_amdgcn_perm(v, u, 0x07060302u); };
+    if (i != 0) return;
+    if (G == 1) *reinterpret_cast<uint32_t *>(to) = own;
+    if (G == 2) *reinterpret_cast<uint2 *>(to) = make_uint2(lows(all[0], all[1]), highs(all[0], all[1]));
+    if (G == 4)
+      *reinterpret_cast<uint4 *>(to) = make_uint4(lows(all[0], all[1]), lows(all[2], all[3]), highs(all[0], all[1]),
+                                                  highs(all[2], all[3]));
+  };
   {  // keys
-    const uint16_t *src = a.k + (int64_t)row * a.ldk + head * D + i * C;
-    alignas(16) uint16_t raw[C];
-    if (C == 4) *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(src);
-    if (C >= 8) *reinterpret_cast<uint4 *>(raw) = *reinterpret_cast<const uint4 *>(src);
-    if (C == 16) *reinterpret_cast<uint4 *>(raw + 8) = *reinterpret_cast<const uint4 *>(src + 8);
-    float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      x[j] = tame(to_f32<BF16>(raw[j]));
-      lo = fminf(lo, x[j]);
-      hi = fmaxf(hi, x[j]);
-    }
-    lanes_minmax<64 / C>(lo, hi);
-    const Group g = group_of(lo, hi);
-#pragma unroll
-    for (int j = 0; j < C; ++j) c[j] = code_of(x[j], g);
+    const Group g = measure<C, L, BF16>(raw, x);
+    codes_of<C>(x, g, c);
     uint8_t *dst = blk + tok * (D / 2) + key_byte<D>(i);
 #pragma unroll
     for (int w = 0; w < (C + 7) / 8; ++w) {
@@ -328,31 +482,18 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(TokenArgs a) {
       if (C == 4) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word;
       else *reinterpret_cast<uint32_t *>(dst + w * (D / 8)) = word;
     }
-    if (i % (64 / C) == 0) {
-      uint16_t *par = reinterpret_cast<uint16_t *>(blk + a.page * D + tok * (4 * G));
-      par[i / (64 / C)] = (uint16_t)g.s16;
-      par[G + i / (64 / C)] = (uint16_t)g.m16;
-    }
+    store(blk + a.page * D + tok * (4 * G), g.s16, g.m16);
   }
-  {  // values
-    const uint16_t *src = a.v + (int64_t)row * a.ldv + head * D + i;
+  {  // values: codes by this lane's channels, then to the columns
+    const Group g = measure<C, L, BF16>(raw_v, x);
+    codes_of<C>(x, g, c);
 #pragma unroll
-    for (int j = 0; j < C; ++j) x[j] = tame(to_f32<BF16>(src[16 * j]));
+    for (int j = 0; j < C; ++j) turn[quarter][i * C + j] = (uint8_t)c[j];
+    store(blk + a.page * D + a.page * (D / 16) + tok * (4 * G), g.s16, g.m16);
+    in_quarter();
     uint32_t word[(C + 7) / 8] = {};
-    uint16_t *par = reinterpret_cast<uint16_t *>(blk + a.page * D + a.page * (D / 16) + tok * (4 * G));
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float lo = fminf(fminf(x[4 * g], x[4 * g + 1]), fminf(x[4 * g + 2], x[4 * g + 3]));
-      float hi = fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), fmaxf(x[4 * g + 2], x[4 * g + 3]));
-      lanes_minmax<16>(lo, hi);
-      const Group p = group_of(lo, hi);
-#pragma unroll
-      for (int j = 4 * g; j < 4 * g + 4; ++j) word[j / 8] |= code_of(x[j], p) << (4 * (j % 8));
-      if (i == 0) {
-        par[g] = (uint16_t)p.s16;
-        par[G + g] = (uint16_t)p.m16;
-      }
-    }
+    for (int j = 0; j < C; ++j) word[j / 8] |= (uint32_t)turn[quarter][16 * j + i] << (4 * (j % 8));
     uint8_t *dst = blk + a.page * (D / 2) + ((tok / 4 * 16 + i) * 4 + tok % 4) * (D / 32);
     if (C == 4) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word[0];
     if (C == 8) *reinterpret_cast<uint32_t *>(dst) = word[0];
@@ -364,8 +505,9 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(TokenArgs a) {
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void kv4_read_kernel(TokenArgs a) {
   constexpr int C = D / 16, G = D / 64;
-  const int i = threadIdx.x & 15;
-  const int32_t row = blockIdx.x * 16 + (threadIdx.x >> 4), head = blockIdx.y;
+  __shared__ __attribute__((aligned(16))) uint16_t turn[16][D];
+  const int i = threadIdx.x & 15, quarter = threadIdx.x >> 4;
+  const int32_t group = blockIdx.x / a.heads, head = blockIdx.x - group * a.heads, row = group * 16 + quarter;
   int32_t tok = 0;
   const uint8_t *blk = block_of<D>(a, row, head, tok);
   if (!blk) return;
@@ -382,20 +524,26 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(TokenArgs a) {
       for (int j = 0; j < (C < 8 ? C : 8); ++j)
         out[8 * w + j] = (uint16_t)from_f32<BF16>(m + s * (float)((word >> (4 * j)) & 15));
     }
-    uint16_t *dst = a.k + (int64_t)row * a.ldk + head * D + i * C;
-    if (C == 4) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(out);
-    if (C >= 8) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(out);
-    if (C == 16) *reinterpret_cast<uint4 *>(dst + 8) = *reinterpret_cast<uint4 *>(out + 8);
+    copy16<C>(a.k + (int64_t)row * a.ldk + head * D + i * C, out);
   }
   {
     const uint16_t *par = reinterpret_cast<const uint16_t *>(blk + a.page * D + a.page * (D / 16) + tok * (4 * G));
     const uint8_t *src = blk + a.page * (D / 2) + ((tok / 4 * 16 + i) * 4 + tok % 4) * (D / 32);
-    uint16_t *dst = a.v + (int64_t)row * a.ldv + head * D + i;
+    uint32_t word[(C + 7) / 8];
+    if (C == 4) word[0] = *reinterpret_cast<const uint16_t *>(src);
+    if (C == 8) word[0] = *reinterpret_cast<const uint32_t *>(src);
+    if (C == 16) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(src);
+      word[0] = w.x, word[(C + 7) / 8 - 1] = w.y;
+    }
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      const uint32_t c = (src[j / 2] >> (4 * (j & 1))) & 15;
-      dst[16 * j] = (uint16_t)from_f32<BF16>(to_f32<false>(par[G + j / 4]) + to_f32<false>(par[j / 4]) * (float)c);
+      const uint32_t c = (word[j / 8] >> (4 * (j % 8))) & 15;
+      turn[quarter][16 * j + i] =
+          (uint16_t)from_f32<BF16>(to_f32<false>(par[G + j / 4]) + to_f32<false>(par[j / 4]) * (float)c);
     }
+    in_quarter();
+    copy16<C>(a.v + (int64_t)row * a.ldv + head * D + i * C, &turn[quarter][i * C]);
   }
 }
 
@@ -406,7 +554,7 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
   const int st = mixllm::kv4_check_cache(cache, cache_bytes, pages, page, heads, dim);
   if (st != MIXLLM_OK) return st;
   const int64_t width = (int64_t)heads * dim;
-  if (heads > 65535 || ldk < width || ldv < width || ldk % 8 != 0 || ldv % 8 != 0) return MIXLLM_E_SHAPE;
+  if (heads > 65535 || ((int64_t)T + 15) / 16 * heads > 0x7FFFFFFF || ldk < width || ldv < width || ldk % 8 != 0 || ldv % 8 != 0) return MIXLLM_E_SHAPE;
   if (!k || !v || !slots) return MIXLLM_E_NULL;
   if (!mixllm::is_aligned16(k) || !mixllm::is_aligned16(v) || !mixllm::is_aligned4(slots)) return MIXLLM_E_SHAPE;
   return MIXLLM_OK;
@@ -414,7 +562,7 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
 
 template <bool APPEND, int D>
 void launch_tokens(const TokenArgs &a, int32_t dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16), (unsigned)a.heads);
+  const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16 * a.heads));  // heads of the same rows together
   if (APPEND) {
     if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv4_append_kernel<D, true>), grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((kv4_append_kernel<D, false>), grid, dim3(256), 0, stream, a);

@@ -257,11 +257,16 @@ extern "C" int mixllm_residual_norm(const void *x, int64_t ldx, const void *post
                       static_cast<uint16_t *>(y), aq, sa, asum, reinterpret_cast<uint4 *>(rowop), ldx, ldgate, ldr,
                       ldro, ldy, M, N, eps, alpha, beta, wide};
   const hipStream_t s = (hipStream_t)stream;
+  // Threads and chunks of 8 per thread, measured on fp16 rows (us at M = 1 / 256 / 2048):
+  // N = 4096: 512 x 1 3.4 / 5.4 / 17.9, 256 x 2 3.7 / 5.8 / 16.4; 8192: 512 x 2 3.9 / 7.1 / 25.3,
+  // 256 x 4 4.6 / 7.6 / 25.8, 1024 x 1 4.0 / 7.2 / 28.0 (2047 rows with an fp32 residual, to int8:
+  // 46.9, 51.2, 52.9); 14336: 512 x 4 5.1 / 10.3 / 52.0, 1024 x 2 4.9 / 10.4 / 58.2.
   if (N <= 512) launch<64, 1>(a, dtype, res_dtype, s);
   else if (N <= 2048) launch<256, 1>(a, dtype, res_dtype, s);
+  else if (N <= 4096 && M <= 512) launch<512, 1>(a, dtype, res_dtype, s);
   else if (N <= 4096) launch<256, 2>(a, dtype, res_dtype, s);
-  else if (N <= 8192) launch<256, 4>(a, dtype, res_dtype, s);
-  else if (N <= 16384) launch<1024, 2>(a, dtype, res_dtype, s);
+  else if (N <= 8192) launch<512, 2>(a, dtype, res_dtype, s);
+  else if (N <= 16384) launch<512, 4>(a, dtype, res_dtype, s);
   else if (N <= 32768) launch<1024, 4>(a, dtype, res_dtype, s);
   else launch<1024, 8>(a, dtype, res_dtype, s);
   return mixllm::launch_status();
