@@ -628,8 +628,12 @@ class PackedLinear:
         m = a.shape[0]
         bufs = bufs or self.buffers(m)
         mixllm_quant_act(a, bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], stream)
-        mixllm_gemm_w4w8a8(bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], m, self.n, self.k, self.n8,
-                           self.blob, bufs["y"], bufs["ws"], stream)
+        return self.gemm(bufs, stream)
+
+    def gemm(self, bufs, stream=None):
+        """The product alone, of activations that are quantized in ``bufs`` already."""
+        mixllm_gemm_w4w8a8(bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], bufs["aq"].shape[0], self.n, self.k,
+                           self.n8, self.blob, bufs["y"], bufs["ws"], stream)
         return bufs["y"]
 
 
@@ -698,15 +702,17 @@ class MLPBlock:
                     h16=torch.empty((m, self.inter), dtype=torch.float16, device=dev))
 
     def forward(self, x, bufs, stream=None, keep_h=False):
-        m = x.shape[0]
+        bx = bufs["x"]
+        mixllm_quant_act(x, bx["aq"], bx["sa"], bx["asum"], bx["rowop"], stream)
+        return self.forward_quantized(bufs, stream, keep_h)
+
+    def forward_quantized(self, bufs, stream=None, keep_h=False):
+        """The block from a hidden state that is quantized in ``bufs["x"]`` already."""
         bx, bh = bufs["x"], bufs["h"]
-        self.gu.forward(x, bx, stream)
-        gu = bx["y"]
+        gu = self.gu.gemm(bx, stream)
         mixllm_silu_mul_quant(gu[:, :self.inter], gu[:, self.inter:], bh["aq"], bh["sa"], bh["asum"], bh["rowop"],
                               bufs["h16"] if keep_h else None, stream)
-        mixllm_gemm_w4w8a8(bh["aq"], bh["sa"], bh["asum"], bh["rowop"], m, self.down.n, self.down.k,
-                           self.down.n8, self.down.blob, bh["y"], bh["ws"], stream)
-        return bh["y"]
+        return self.down.gemm(bh, stream)
 
     def capture(self, x, bufs, keep_h=False):
         """A HIP graph of one forward pass on these buffers (torch.cuda.CUDAGraph)."""
@@ -720,3 +726,93 @@ class MLPBlock:
         with torch.cuda.graph(g, stream=s):
             self.forward(x, bufs, s, keep_h)
         return g
+
+
+class RequestPages:
+    """Which pages the requests of a batch hold: the page table, the free pages and the lengths
+    of up to ``requests`` requests over caches of ``pages`` pages (every layer's cache uses the
+    same).  ``plan(fresh)`` moves it on by one step on the GPU and returns the step's slots
+    and row bounds; it can be captured.  Argument marshalling only."""
+
+    def __init__(self, requests: int, pages: int, page: int, max_len: int, tokens: int, device="cuda"):
+        if pages <= 0 or max_len <= 0:
+            raise ValueError("pages and max_len must be positive")
+        self.page, self.pages = page, pages
+        new = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        self.table = new(requests, -(-max_len // page))
+        self.pool = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.count = torch.tensor([pages, 0], dtype=torch.int32, device=device)  # free pages, requests refused last
+        self.lens, self.cu = new(requests), new(requests + 1)
+        self.slots, self.pos = new(tokens), new(tokens)
+
+    def plan(self, fresh, stream=None):
+        """fresh: int32 [requests] tokens to add to each request; negative: it ended."""
+        mixllm_kv_plan(fresh, self.lens, self.table, self.pool, self.count, self.page, self.pages, self.lens, self.count,
+                       self.cu, self.slots, self.pos, stream)
+        return self
+
+
+class AttentionBlock:
+    """The attention half of a decoder layer on packed layers and a cache in 4 bits: the residual
+    sum and norm quantized for the q/k/v projections, one GEMM over q, k and v, the write into
+    the cache, attention, and the output projection.  Seven launches on one stream (eight where
+    attention splits the tokens).  Argument marshalling only."""
+
+    def __init__(self, w_q, w_k, w_v, w_o, idx8_q, idx8_k, idx8_v, idx8_o, norm, q_heads: int, kv_heads: int,
+                 pages: int, page: int, post_norm=None, eps: float = 1e-5, window: int = 0, device="cuda"):
+        self.qkv = QKVProjection(w_q, w_k, w_v, idx8_q, idx8_k, idx8_v, device)
+        self.o = PackedLinear(np.asarray(w_o, np.float16), idx8_o, device)
+        self.q_heads, self.kv_heads = q_heads, kv_heads
+        self.dim = np.asarray(w_k).shape[0] // kv_heads
+        if np.asarray(w_q).shape[0] != q_heads * self.dim or np.asarray(w_k).shape != np.asarray(w_v).shape or (
+                self.o.k != q_heads * self.dim):
+            raise ValueError("the projections' shapes do not fit the heads")
+        self.cache = kv4_cache(pages, page, kv_heads, self.dim, device)
+        self.norm, self.post_norm, self.eps, self.window, self.page, self.device = norm, post_norm, eps, window, page, device
+
+    def buffers(self, m: int, requests: int, max_rows: int, max_len: int):
+        size = mixllm_kv4_attention_workspace_bytes(m, requests, self.q_heads, self.kv_heads, self.dim, max_rows, max_len,
+                                                    self.window)
+        return dict(qkv=self.qkv.buffers(m), o=self.o.buffers(m), max_rows=max_rows, max_len=max_len,
+                    attn=torch.zeros((m, self.q_heads, self.dim), dtype=torch.float16, device=self.device),
+                    ws=torch.empty(size, dtype=torch.uint8, device=self.device) if size else None)
+
+    def forward(self, x, h, bufs, req, rotate=None, stream=None):
+        """h: [M, hidden] the residual stream, updated in place by the block output x of the
+        layer before (None for the first); req: RequestPages after its plan(); rotate: called
+        with the views q [M, heads, dim], k and the positions before the keys are written, for
+        an embedding of positions (in place).  Returns the output projection's [M, hidden]."""
+        b, bo = bufs["qkv"], bufs["o"]
+        m = h.shape[0]
+        mixllm_residual_norm(x, h, self.norm, h if x is not None else None, aq=b["aq"], sa=b["sa"], asum=b["asum"],
+                             rowop=b["rowop"], post_weight=self.post_norm if x is not None else None, eps=self.eps,
+                             stream=stream)
+        q, k, v = self.qkv.split(self.qkv.layer.gemm(b, stream))
+        q, k, v = q.unflatten(1, (self.q_heads, self.dim)), k.unflatten(1, (self.kv_heads, self.dim)), v.unflatten(
+            1, (self.kv_heads, self.dim))
+        if rotate is not None:
+            rotate(q, k, req.pos[:m])
+        mixllm_kv4_append(k, v, req.slots[:m], self.cache, self.page, stream)
+        mixllm_kv4_attention(q, self.cache, req.table, req.lens, req.cu, bufs["attn"], self.page, bufs["max_rows"],
+                             bufs["max_len"], window=self.window, workspace=bufs["ws"], stream=stream)
+        return self.o.forward(bufs["attn"].flatten(1), bo, stream)
+
+
+class DecoderLayer:
+    """A decoder layer: AttentionBlock, the norm between, MLPBlock.  The layer's output is left
+    to the next layer's first norm (or a last mixllm_residual_norm) to add.  Argument
+    marshalling only."""
+
+    def __init__(self, attention: AttentionBlock, mlp: MLPBlock, norm, post_norm=None):
+        self.attention, self.mlp, self.norm, self.post_norm = attention, mlp, norm, post_norm
+
+    def buffers(self, m: int, requests: int, max_rows: int, max_len: int):
+        return dict(attention=self.attention.buffers(m, requests, max_rows, max_len), mlp=self.mlp.buffers(m))
+
+    def forward(self, x, h, bufs, req, rotate=None, stream=None):
+        """As AttentionBlock.forward; returns the MLP block's [M, hidden]."""
+        a = self.attention.forward(x, h, bufs["attention"], req, rotate, stream)
+        b = bufs["mlp"]["x"]
+        mixllm_residual_norm(a, h, self.norm, h, aq=b["aq"], sa=b["sa"], asum=b["asum"], rowop=b["rowop"],
+                             post_weight=self.post_norm, eps=self.attention.eps, stream=stream)
+        return self.mlp.forward_quantized(bufs["mlp"], stream)
