@@ -201,19 +201,22 @@ __device__ __forceinline__ int32_t chunks_of(const Tile &t, int32_t chunk) {
   return (int32_t)(((uint32_t)(t.hi - base_of(t)) + chunk - 1) / (uint32_t)chunk);
 }
 
-template <int D, int V, bool BF16>
+template <int D, int V, int CT, bool BF16>
 __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
+  static_assert(CT == 1 || V == 1, "more than one column block only where rows fill them");
   using S = Shape<D, V>;
   constexpr int G = D / 64, W = D / 32, J = D / 16;
   constexpr int kStride = D + 4;  // floats of a column of partial outputs in LDS
-  constexpr int kRing = 2 * S::kStage, kPartial = kCols * kStride * 4;
+  constexpr int kAll = CT * kCols;  // columns of a wave
+  constexpr int kRing = 2 * S::kStage, kPartial = kAll * kStride * 4;
   // the rings and, after the loop, the waves' partial outputs
   __shared__ __attribute__((aligned(16))) uint8_t smem[kWaves * (kRing > kPartial ? kRing : kPartial)];
-  __shared__ float s_m[kWaves][kCols], s_l[kWaves][kCols];
+  __shared__ float s_m[kWaves][kAll], s_l[kWaves][kAll];
 
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4, part = n / S::kRows;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, rt = blockIdx.y, b = blockIdx.z;
+  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, b = blockIdx.z;
+  const int32_t rt = a.tiles - 1 - (int32_t)blockIdx.y;  // a request's last rows see most tokens: their tiles first
   const Tile t = tile_of(a, b, h, rt);
   if (t.rows <= 0) return;
   const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
@@ -224,12 +227,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 
   // The query row of this lane, as operands (zero outside the column's part) and as sums per
   // group of channels.
-  const int32_t row = n % S::kRows, r = t.row0 + (row < t.rows ? row : t.rows - 1);
-  const int32_t i = r / a.group, head = h * a.group + r % a.group;
-  const uint16_t *qp = a.q + (int64_t)(t.q0 + i) * a.ldq + (int64_t)head * D + 8 * c;
-  uint4v raw[W];
+  int32_t i[CT];  // the row's place in its request
+  uint4v raw[CT][W];
 #pragma unroll
-  for (int s = 0; s < W; ++s) raw[s] = *reinterpret_cast<const uint4v *>(qp + 32 * s);
+  for (int z = 0; z < CT; ++z) {
+    const int32_t row = kCols * z + n % S::kRows, r = t.row0 + (row < t.rows ? row : t.rows - 1);
+    i[z] = r / a.group;
+    const int32_t head = h * a.group + r % a.group;
+    const uint16_t *qp = a.q + (int64_t)(t.q0 + i[z]) * a.ldq + (int64_t)head * D + 8 * c;
+#pragma unroll
+    for (int s = 0; s < W; ++s) raw[z][s] = *reinterpret_cast<const uint4v *>(qp + 32 * s);
+  }
 
   const int32_t P = 1 << a.page_log2;
   const int32_t block = mixllm::kv4_block_bytes(P, D);
@@ -285,33 +293,34 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   };
   if (tb < to) fetch();
 
-  half8 q[V][W];
-  float row_scale, qsum[G];
-  {
+  half8 q[CT][V][W];
+  float row_scale[CT], qsum[CT][G];
+  int32_t row_hi[CT], row_lo[CT];  // the row sees tokens [row_lo, row_hi)
+#pragma unroll
+  for (int z = 0; z < CT; ++z) {
     float top = 0.0f;
 #pragma unroll
-    for (int s = 0; s < W; ++s) {
+    for (int s = 0; s < W; ++s)
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        top = fmaxf(top, fmaxf(fabsf(up<BF16>(raw[s][w] & 0xFFFFu)), fabsf(up<BF16>(raw[s][w] >> 16))));
-    }
+        top = fmaxf(top, fmaxf(fabsf(up<BF16>(raw[z][s][w] & 0xFFFFu)), fabsf(up<BF16>(raw[z][s][w] >> 16))));
     top = quarters_max(top);
     int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;  // top in [2^(e-1), 2^e)
     e = e < -100 ? -100 : e;
     const float mul = ldexpf(1.0f, 14 - e), factor = a.scale * kLog2e;
-    row_scale = factor * ldexpf(1.0f, e - 14 + 24);
+    row_scale[z] = factor * ldexpf(1.0f, e - 14 + 24);
 #pragma unroll
-    for (int g = 0; g < G; ++g) qsum[g] = 0.0f;
+    for (int g = 0; g < G; ++g) qsum[z][g] = 0.0f;
 #pragma unroll
     for (int s = 0; s < W; ++s) {
       float x[8];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        x[2 * w] = up<BF16>(raw[s][w] & 0xFFFFu);
-        x[2 * w + 1] = up<BF16>(raw[s][w] >> 16);
+        x[2 * w] = up<BF16>(raw[z][s][w] & 0xFFFFu);
+        x[2 * w + 1] = up<BF16>(raw[z][s][w] >> 16);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) qsum[s / 2] += x[j];
+      for (int j = 0; j < 8; ++j) qsum[z][s / 2] += x[j];
       half8 v;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // nibbles p and p + 4
@@ -320,13 +329,14 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
         v[2 * p + 1] = (_Float16)(x[p + 4] * f);
       }
 #pragma unroll
-      for (int y = 0; y < V; ++y) q[y][s] = V == 1 || part == y ? v : half8{};
+      for (int y = 0; y < V; ++y) q[z][y][s] = V == 1 || part == y ? v : half8{};
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g) qsum[g] = quarters_sum(qsum[g]) * factor;
+    for (int g = 0; g < G; ++g) qsum[z][g] = quarters_sum(qsum[z][g]) * factor;
+    const int32_t pos = t.len - t.nq + i[z];
+    row_hi[z] = pos + 1;
+    row_lo[z] = a.window ? pos - a.window + 1 : 0;
   }
-  const int32_t pos = t.len - t.nq + i;                                      // this lane's row sees
-  const int32_t row_hi = pos + 1, row_lo = a.window ? pos - a.window + 1 : 0;  // [row_lo, row_hi)
   // [all_lo, all_hi): tokens that every row of the tile sees
   const int32_t all_hi = t.len - t.nq + t.row0 / a.group + 1;
   const int32_t all_lo = a.window ? t.len - t.nq + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
@@ -334,17 +344,22 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   // The column's running sums are of weights w = 2^(score - ref): ref is the largest score
   // seen, up to kLazy, less a power k (the same in the wave) that keeps w times a value's
   // scale below 2^15 and far above fp16's subnormals.
-  float4v o[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) o[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+  float4v o[CT][J];
   // rest: the sum of the weights before their rounding to fp16 less the sum after it.  Times
   // 8, the middle code, it goes back into the output: the rounding then acts on codes about
   // zero, half as large as 0 .. 15 and as little one-sided as the values themselves.  Next to
   // a bf16 output's own rounding neither shows.
   constexpr bool kRest = !BF16;
-  float m = kLow, k = 0.0f, ref = kLow, limit = kLow, l = 0.0f, bias[G], rest[G];
+  float m[CT], ref[CT], limit[CT], l[CT], bias[CT][G], rest[CT][G], k = 0.0f;
 #pragma unroll
-  for (int g = 0; g < G; ++g) bias[g] = rest[g] = 0.0f;
+  for (int z = 0; z < CT; ++z) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) o[z][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    m[z] = ref[z] = limit[z] = kLow;
+    l[z] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) bias[z][g] = rest[z][g] = 0.0f;
+  }
   uint32_t vbits = 0;  // value scales up to this fp16 pattern fit k
 
   // This lane's dwords of key or value codes of a run.
@@ -375,36 +390,42 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   auto at = [](const half2v (&p)[G], int e) { return (float)p[e / 2][e % 2]; };
 
   // here: bit x says that run x is in the cache.
-  auto compute = [&](auto stage, int32_t t0, uint32_t here) {
+  auto compute = [&](auto stage, int32_t t0, uint32_t here) __attribute__((always_inline)) {
     const uint8_t *src = ring + decltype(stage)::value * S::kStage;
-    float s[S::kSets][4];
+    float s[CT][S::kSets][4];
 #pragma unroll
     for (int z = 0; z < S::kSets; ++z) {
-      float4v acc[G];
+      float4v acc[CT][G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int e = 0; e < CT; ++e)
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[e][g] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int y = 0; y < V; ++y) {
         uint32_t w[W];
         codes(src + (z * V + y) * S::kBytes, w);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w[2 * g]), q[y][2 * g], acc[g], 0, 0, 0);
-          acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w[2 * g + 1]), q[y][2 * g + 1], acc[g], 0, 0, 0);
+        for (int d = 0; d < W; ++d) {
+          const half8 v = codes8(w[d]);
+#pragma unroll
+          for (int e = 0; e < CT; ++e)
+            acc[e][d / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, q[e][y][d], acc[e][d / 2], 0, 0, 0);
         }
       }
       half2v kp[4][G];
       params(src + (z * V + part) * S::kBytes + 16 * D, kp);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float dot = 0.0f, add = 0.0f;
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          dot = fmaf(at(kp[u], g), acc[g][u], dot);
-          add = fmaf(at(kp[u], G + g), qsum[g], add);
+        for (int e = 0; e < CT; ++e) {
+          float dot = 0.0f, add = 0.0f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            dot = fmaf(at(kp[u], g), acc[e][g][u], dot);
+            add = fmaf(at(kp[u], G + g), qsum[e][g], add);
+          }
+          s[e][z][u] = fmaf(row_scale[e], dot, add);
         }
-        s[z][u] = fmaf(row_scale, dot, add);
-      }
     }
     half2v vp[S::kSets][4][G];
 #pragma unroll
@@ -417,7 +438,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
         for (int u = 0; u < 4; ++u) {
           const int32_t tok = t0 + kRun * (z * V + part) + 4 * c + u;
           const bool there = tok < to && (here >> (z * V + part) & 1);
-          s[z][u] = there && tok < row_hi && tok >= row_lo && tok >= from ? s[z][u] : -INFINITY;
+#pragma unroll
+          for (int e = 0; e < CT; ++e)
+            s[e][z][u] = there && tok < row_hi[e] && tok >= row_lo[e] && tok >= from ? s[e][z][u] : -INFINITY;
           // what lies behind the last token may be NaN: no part of a sum, not even times zero
 #pragma unroll
           for (int g = 0; g < G; ++g) {
@@ -426,13 +449,15 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
           }
         }
     }
-    float top = s[0][0];
+    float top[CT];
+    bool over = false;
     uint32_t big = 0;
 #pragma unroll
     for (int z = 0; z < S::kSets; ++z)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        top = fmaxf(top, s[z][u]);
+#pragma unroll
+        for (int e = 0; e < CT; ++e) top[e] = z + u == 0 ? s[e][0][0] : fmaxf(top[e], s[e][z][u]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const uint32_t pair = __builtin_bit_cast(uint32_t, vp[z][u][g / 2]);
@@ -440,7 +465,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
           big = v > big ? v : big;
         }
       }
-    if (__any(top > limit || big > vbits)) {
+#pragma unroll
+    for (int e = 0; e < CT; ++e) over = over || top[e] > limit[e];
+    if (__any(over || big > vbits)) {
       if (__any(big > vbits)) {
 #pragma unroll
         for (int d = S::kRows; d < kCols; d <<= 1) {
@@ -452,43 +479,47 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
         vbits = e << 10 | 0x3FF;
         k = (float)(23 - e);  // a scale below 2^(e-14) times 2^k is below 2^9
       }
-      m = fmaxf(m, quarters_max(top));
-      const float next = m - k, f = __builtin_amdgcn_exp2f(ref - next);
-      ref = next;
-      limit = m + kLazy;
-      l *= f;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        bias[g] *= f;
-        rest[g] *= f;
-      }
-#pragma unroll
-      for (int j = 0; j < J; ++j) o[j] *= f;
-    }
-    half2v p[S::kSets][G][2];
-#pragma unroll
-    for (int z = 0; z < S::kSets; ++z)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float w = __builtin_amdgcn_exp2f(s[z][u] - ref);
-        l += w;
+      for (int e = 0; e < CT; ++e) {
+        m[e] = fmaxf(m[e], quarters_max(top[e]));
+        const float next = m[e] - k, f = __builtin_amdgcn_exp2f(ref[e] - next);
+        ref[e] = next;
+        limit[e] = m[e] + kLazy;
+        l[e] *= f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          bias[g] = fmaf(at(vp[z][u], G + g), w, bias[g]);
-          const float ps = fmaf(at(vp[z][u], g), w, 0.0f);  // as a fused sum it takes the fp16 factor as it is
-          if (kRest) rest[g] += ps;
-          p[z][g][u / 2][u % 2] = (_Float16)ps;
+          bias[e][g] *= f;
+          rest[e][g] *= f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) o[e][j] *= f;
+      }
+    }
+    half2v p[CT][S::kSets][G][2];
+#pragma unroll
+    for (int e = 0; e < CT; ++e)
+#pragma unroll
+      for (int z = 0; z < S::kSets; ++z) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float w = __builtin_amdgcn_exp2f(s[e][z][u] - ref[e]);
+          l[e] += w;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            bias[e][g] = fmaf(at(vp[z][u], G + g), w, bias[e][g]);
+            const float ps = fmaf(at(vp[z][u], g), w, 0.0f);  // as a fused sum it takes the fp16 factor as it is
+            if (kRest) rest[e][g] += ps;
+            p[e][z][g][u / 2][u % 2] = (_Float16)ps;
+          }
+        }
+        if (kRest) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              rest[e][g] = __builtin_amdgcn_fdot2(p[e][z][g][y], half2v{(_Float16)-1.0f, (_Float16)-1.0f}, rest[e][g], false);
         }
       }
-    if (kRest) {
-#pragma unroll
-      for (int z = 0; z < S::kSets; ++z)
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            rest[g] = __builtin_amdgcn_fdot2(p[z][g][y], half2v{(_Float16)-1.0f, (_Float16)-1.0f}, rest[g], false);
-    }
 #pragma unroll
     for (int y = 0; y < S::kRuns / 2; ++y) {  // two runs fill an operand
       uint32_t v[2][W];
@@ -496,19 +527,21 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       codes(src + (2 * y + 1) * S::kBytes + 8 * D, v[1]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint4v pw;
+        uint4v pw[CT];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (V == 1) {
-            pw[e] = __builtin_bit_cast(uint32_t, p[0][g][e]);
-            pw[2 + e] = __builtin_bit_cast(uint32_t, p[S::kSets - 1][g][e]);
-          } else {
-            const uint32_t w = __builtin_bit_cast(uint32_t, p[V == 2 ? y : 0][g][e]);
-            const int first = V == 2 ? 0 : 2 * y;  // the column part of this pair's first run
-            pw[e] = part == first ? w : 0u;
-            pw[2 + e] = part == first + 1 ? w : 0u;
+        for (int e = 0; e < CT; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            if (V == 1) {
+              pw[e][f] = __builtin_bit_cast(uint32_t, p[e][0][g][f]);
+              pw[e][2 + f] = __builtin_bit_cast(uint32_t, p[e][S::kSets - 1][g][f]);
+            } else {
+              const uint32_t w = __builtin_bit_cast(uint32_t, p[e][V == 2 ? y : 0][g][f]);
+              const int first = V == 2 ? 0 : 2 * y;  // the column part of this pair's first run
+              pw[e][f] = part == first ? w : 0u;
+              pw[e][2 + f] = part == first + 1 ? w : 0u;
+            }
           }
-        }
         uint32_t w[4];  // pairs of tokens, the 4 nibbles of group g's channels in each half
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -523,15 +556,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 #pragma unroll
         for (int nib = 0; nib < 4; ++nib) {
           const uint4v u = {nibble_pair(w[0], nib), nibble_pair(w[1], nib), nibble_pair(w[2], nib), nibble_pair(w[3], nib)};
-          o[4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, u), __builtin_bit_cast(half8, pw),
-                                                                  o[4 * g + nib], 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < CT; ++e)
+            o[e][4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                __builtin_bit_cast(half8, u), __builtin_bit_cast(half8, pw[e]), o[e][4 * g + nib], 0, 0, 0);
         }
       }
     }
   };
 
   while (tb < to) {
-    auto step = [&](auto stage, int32_t j) {
+    auto step = [&](auto stage, int32_t j) __attribute__((always_inline)) {
       if (j + 1 < steps) {
         wait_lds();  // the stage that is filled now was read in the last step
         start(Const<1 - decltype(stage)::value>(), j + 1);
@@ -555,28 +590,34 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   }
 
   // The columns' statistics and outputs; a row's are V columns of each wave.
-  l = quarters_sum(l);
 #pragma unroll
-  for (int g = 0; g < G; ++g) bias[g] = quarters_sum(kRest ? fmaf(rest[g], 8.0f, bias[g]) : bias[g]);
-  if (c == 0) {
-    s_m[wave][n] = ref;
-    s_l[wave][n] = l;
+  for (int z = 0; z < CT; ++z) {
+    l[z] = quarters_sum(l[z]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) bias[z][g] = quarters_sum(kRest ? fmaf(rest[z][g], 8.0f, bias[z][g]) : bias[z][g]);
+    if (c == 0) {
+      s_m[wave][kCols * z + n] = ref[z];
+      s_l[wave][kCols * z + n] = l[z];
+    }
   }
   __syncthreads();  // and every wave is done with its ring
   float *s_o = reinterpret_cast<float *>(smem);
-  float best = ref;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w)
+  for (int z = 0; z < CT; ++z) {
+    float best = ref[z];
 #pragma unroll
-    for (int y = 0; y < V; ++y) best = fmaxf(best, s_m[w][row + y * S::kRows]);
-  const float f = __builtin_amdgcn_exp2f(ref - best);
+    for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const float fo = f * (j & 1 ? 0x1p20f : 0x1p24f), fb = f * bias[j / 4];
-    float4v v;
+      for (int y = 0; y < V; ++y) best = fmaxf(best, s_m[w][kCols * z + n % S::kRows + y * S::kRows]);
+    const float f = __builtin_amdgcn_exp2f(ref[z] - best);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = fmaf(o[j][u], fo, fb);
-    *reinterpret_cast<float4v *>(s_o + (wave * kCols + n) * kStride + 16 * j + 4 * c) = v;
+    for (int j = 0; j < J; ++j) {
+      const float fo = f * (j & 1 ? 0x1p20f : 0x1p24f), fb = f * bias[z][j / 4];
+      float4v v;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = fmaf(o[z][j][u], fo, fb);
+      *reinterpret_cast<float4v *>(s_o + (wave * kAll + kCols * z + n) * kStride + 16 * j + 4 * c) = v;
+    }
   }
   __syncthreads();
   const int64_t place = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits + split;
@@ -594,7 +635,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       for (int y = 0; y < V; ++y) {
         const int col = rr + y * S::kRows;
         sum = fmaf(s_l[w][col], __builtin_amdgcn_exp2f(s_m[w][col] - top), sum);
-        const float *src = s_o + (w * kCols + col) * kStride + ch;
+        const float *src = s_o + (w * kAll + col) * kStride + ch;
         v0 += *reinterpret_cast<const float4v *>(src);
         v1 += *reinterpret_cast<const float4v *>(src + 4);
       }
@@ -702,7 +743,7 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
   if (lane == 0 && a.lse) a.lse[(int64_t)(t.q0 + i) * a.hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// How the work of a call is cut.  Rows: tiles of 4, 8 or 16 (row, head) pairs of one
+// How the work of a call is cut.  Rows: tiles of 4, 8, 16 or 32 (row, head) pairs of one
 // key/value head.  Tokens: so many equal chunks of each tile that about kTarget workgroups
 // run at the longest length; 256 CUs hold 2 of them each.
 constexpr int64_t kTarget = 512;
@@ -714,11 +755,11 @@ struct Cut {
 Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
   Cut k;
   const int64_t rows = (int64_t)max_rows * (hq / hkv);
-  k.tile_rows = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 8 : 16;
+  k.tile_rows = rows <= 4 && dim < 256 ? 4 : rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32;
   k.tiles = (int32_t)((rows + k.tile_rows - 1) / k.tile_rows);
   int64_t span = max_len;
-  // a tile's rows are at most 16 positions, its first chunk starts at a whole run
-  if (window && (int64_t)window + 16 + kRun < span) span = (int64_t)window + 16 + kRun;
+  // a tile's rows are at most tile_rows positions, its first chunk starts at a whole run
+  if (window && (int64_t)window + k.tile_rows + kRun < span) span = (int64_t)window + k.tile_rows + kRun;
   const int64_t groups = (int64_t)B * hkv * k.tiles;
   const int64_t most = (span + kMinChunk - 1) / kMinChunk, want = (kTarget + groups - 1) / groups;
   k.splits = (int32_t)(most < 1 || want <= 1 ? 1 : want < most ? want : most);
@@ -737,10 +778,13 @@ bool shape_ok(int64_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_
 template <int D, bool BF16>
 void launch(const Args &a, hipStream_t s) {
   const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
-  if (D < 256 && a.tile_rows == 4)
-    hipLaunchKernelGGL((kv4_attention_kernel<D, D < 256 ? 4 : 2, BF16>), grid, threads, 0, s, a);
-  else if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attention_kernel<D, 2, BF16>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((kv4_attention_kernel<D, 1, BF16>), grid, threads, 0, s, a);
+  constexpr bool kWide = D < 256;  // 256 channels: the registers of 4-row and 32-row tiles are not there
+  if (kWide && a.tile_rows == 32)
+    hipLaunchKernelGGL((kv4_attention_kernel<D, 1, kWide ? 2 : 1, BF16>), grid, threads, 0, s, a);
+  else if (kWide && a.tile_rows == 4)
+    hipLaunchKernelGGL((kv4_attention_kernel<D, kWide ? 4 : 2, 1, BF16>), grid, threads, 0, s, a);
+  else if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attention_kernel<D, 2, 1, BF16>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((kv4_attention_kernel<D, 1, 1, BF16>), grid, threads, 0, s, a);
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
   const int64_t rows = (int64_t)a.B * a.max_rows * a.hq;
   if (a.splits > 16) hipLaunchKernelGGL((kv4_join_kernel<D, 4, BF16>), dim3((unsigned)rows), threads, 0, s, a);
