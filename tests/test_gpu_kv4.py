@@ -168,7 +168,8 @@ def test_plan(L, name, in_place):
         assert np.array_equal(got[k].cpu().numpy(), v), k
 
 
-@pytest.mark.parametrize("b,prompt,free", [(1023, 1, 2000), (1024, 1, 40), (1025, 40, 3000), (2500, 7, 9000)])
+@pytest.mark.parametrize("b,prompt,free", [(1023, 1, 2000), (1024, 1, 40), (1025, 40, 3000), (2500, 7, 9000), (2100, 2, 4000),
+                                           (1024, 300, 9000)])
 def test_plan_of_many_requests(L, b, prompt, free):
     """More requests than the sums' workgroup has threads, with ends, prompts and refusals."""
     U.say("plan many", b, prompt, free)
@@ -394,6 +395,71 @@ def test_extreme_values(L, dtype, vscale, qscale):
     scale = 0.09 / max(qscale, 1.0)
     out, lse = attend(L, q, cache, table, [n], [1], 16, dtype, scale)
     compare(out, lse, q, [parts], [n], [1], dtype, scale)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 2.0])
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_any_finite_scale(L, scale, rows):
+    """A negative scale turns the order of the scores, zero makes them equal; 2.0 makes them peaked."""
+    lens = [300]
+    dev, table, kv = build(lens, 2, 128, 16, torch.float16, 29)
+    q = rounded(np.random.default_rng(3).normal(size=(rows, 8, 128)).astype(np.float32), torch.float16)
+    U.say("attention scale", scale, rows)
+    out, lse = attend(L, q, dev, table, lens, [rows], 16, torch.float16, scale)
+    compare(out, lse, q, kv, lens, [rows], torch.float16, scale, picks=lambda n: {0, n // 2, n - 1})
+
+
+def test_rows_past_the_promise_are_left(L):
+    """More rows than max_rows: the first ones are computed at their own positions, the others of
+    out and lse stay."""
+    dev, table, kv = build([100], 2, 128, 16, torch.float16, 29)
+    q = rounded(np.random.default_rng(3).normal(size=(9, 8, 128)).astype(np.float32), torch.float16)
+    full, lf = attend(L, q, dev, table, [100], [9], 16, torch.float16, 0.1)
+    for mr in (1, 2, 5):
+        U.say("attention rows cut", mr)
+        out, lse = attend(L, q, dev, table, [100], [9], 16, torch.float16, 0.1, 0, mr)
+        # another number of rows is another cut of the work: equal up to its rounding
+        compare(out[:mr], lse[:mr], q[:mr], [[x[:100 - 9 + mr] for x in kv[0]]], [100 - 9 + mr], [mr], torch.float16, 0.1)
+        assert torch.all(out[mr:] == 9.0) and torch.all(lse[mr:] == 9.0)
+    compare(full, lf, q, kv, [100], [9], torch.float16, 0.1)
+
+
+def test_calls_side_by_side(L):
+    """Attention and appends on two streams at once, each with its own workspace and cache: the
+    results of running them one after the other."""
+    lens = [6000, 900, 3000]
+    sides = []
+    for i in range(2):
+        dev, table, _ = build(lens, 4, 128, 64, torch.bfloat16, 51 + i)
+        q = cuda(rounded(np.random.default_rng(i).normal(size=(3, 16, 128)).astype(np.float32), torch.bfloat16), torch.bfloat16)
+        size = L.mixllm_kv4_attention_workspace_bytes(3, 3, 16, 4, 128, 1, 6000)
+        assert size
+        sides.append(dict(q=q, dev=dev, table=cuda(table), out=torch.empty_like(q),
+                          ws=torch.empty(size, dtype=torch.uint8, device="cuda"), stream=torch.cuda.Stream()))
+    ln, cu = i32(lens), i32([0, 1, 2, 3])
+    k = torch.randn(3, 4, 128, device="cuda").bfloat16()
+
+    def run(s, stream):
+        slots = s["table"][:, 0] * 64
+        L.mixllm_kv4_append(k, k, slots, s["dev"], 64, stream=stream)
+        L.mixllm_kv4_attention(s["q"], s["dev"], s["table"], ln, cu, s["out"], 64, 1, 6000, workspace=s["ws"], stream=stream)
+
+    want = []
+    for s in sides:
+        run(s, None)
+        want.append(s["out"].clone())
+    torch.cuda.synchronize()
+    U.say("attention side by side")
+    for rep in range(20):
+        for s in sides:
+            s["out"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for s in sides:
+            with torch.cuda.stream(s["stream"]):
+                run(s, s["stream"] if rep % 2 else s["stream"].cuda_stream)
+        torch.cuda.synchronize()
+        for s, w in zip(sides, want):
+            assert torch.equal(s["out"], w), rep
 
 
 def test_a_row_that_is_not_finite_stays_alone(L):

@@ -125,8 +125,10 @@ __device__ __forceinline__ void wait_vm() {
 
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }  // lgkmcnt(0)
 
-// A number as a type: stages are named at compile time, so that the compiler sees that the
-// reads of one stage do not touch the copies into another and adds no wait of its own.
+// A number as a type: stages are named at compile time, or the compiler takes every read of a
+// stage for one of the copies in flight and waits for them all.  With both in one array it
+// still does so in every second step; an array per stage takes that wait out too and measures
+// 1 to 2% slower (128 decodes of 8192 tokens 189.5 us for 188.0), so it stays.
 template <int N>
 struct Const {
   static constexpr int value = N;
@@ -160,7 +162,7 @@ struct Shape {
 
 // The request, rows and tokens of a workgroup.
 struct Tile {
-  int32_t b, h, row0, rows, nq, len, q0;  // rows: query rows of this tile
+  int32_t b, h, row0, rows, nq, len, q0;  // rows: query rows of this tile; nq: of the request
   int32_t lo, hi;                         // tokens that any of its rows sees
 };
 
@@ -169,14 +171,14 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int
   t.b = b, t.h = h, t.row0 = rt * a.tile_rows;
   t.q0 = a.cu[b];
   int32_t end = a.cu[b + 1];
-  end = end < a.T ? end : a.T;
+  end = end < 0 ? 0 : end < a.T ? end : a.T;
   t.q0 = t.q0 < 0 ? 0 : t.q0;
   t.nq = end - t.q0;
-  t.nq = t.nq < a.max_rows ? t.nq : a.max_rows;
+  const int32_t take = t.nq < a.max_rows ? t.nq : a.max_rows;
   const int64_t cap = (int64_t)a.width << a.page_log2;
   const int32_t most = cap < a.max_len ? (int32_t)cap : a.max_len, len = a.lens[b];
   t.len = len < 0 ? 0 : len < most ? len : most;
-  const int64_t all = (int64_t)t.nq * a.group;
+  const int64_t all = (int64_t)take * a.group;
   const int64_t left = all - t.row0;
   t.rows = left <= 0 ? 0 : left < a.tile_rows ? (int32_t)left : a.tile_rows;
   if (t.rows > 0) {
@@ -430,6 +432,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     half2v vp[S::kSets][4][G];
 #pragma unroll
     for (int z = 0; z < S::kSets; ++z) params(src + (z * V + part) * S::kBytes + 16 * D + 64 * G, vp[z]);
+    uint32_t vc[S::kRuns][W];  // read here, beside the scores, and not when they are needed
+#pragma unroll
+    for (int x = 0; x < S::kRuns; ++x) codes(src + x * S::kBytes + 8 * D, vc[x]);
     if (!(t0 >= all_lo && t0 >= from && t0 + S::kTokens <= all_hi && t0 + S::kTokens <= to &&
           here == (1u << S::kRuns) - 1)) {
 #pragma unroll
@@ -522,9 +527,6 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       }
 #pragma unroll
     for (int y = 0; y < S::kRuns / 2; ++y) {  // two runs fill an operand
-      uint32_t v[2][W];
-      codes(src + 2 * y * S::kBytes + 8 * D, v[0]);
-      codes(src + (2 * y + 1) * S::kBytes + 8 * D, v[1]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint4v pw[CT];
@@ -546,11 +548,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           if (D == 64) {
-            w[z] = v[z / 2][z % 2];
+            w[z] = vc[2 * y + z / 2][z % 2];
           } else {
             constexpr int per = D < 128 ? 1 : D / 128;  // dwords of one token
             const int d0 = (z % 2) * 2 * per + g / 2;
-            w[z] = __builtin_amdgcn_perm(v[z / 2][d0 + per], v[z / 2][d0], g % 2 ? 0x07060302u : 0x05040100u);
+            w[z] = __builtin_amdgcn_perm(vc[2 * y + z / 2][d0 + per], vc[2 * y + z / 2][d0], g % 2 ? 0x07060302u : 0x05040100u);
           }
         }
 #pragma unroll
@@ -660,14 +662,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 }
 
 // Joins the chunks of a row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  WAVES
-// waves share a row and head, wave w takes the chunks w, w + WAVES, ..
+// waves share a row and head, wave w takes the chunks w, w + WAVES, ..; a workgroup has 4 waves
+// or as many as share.  Up to 16 chunks a wave does alone (4 us, of which a launch is most);
+// 64 chunks take 5.7 us with 16 waves, 8.0 with 4.
 template <int D, int WAVES, bool BF16>
-__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args a) {
+__global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void kv4_join_kernel(Args a) {
   constexpr int C = D / 64;  // channels of a lane
-  __shared__ float s_m[kWaves], s_l[kWaves], s_o[kWaves][D];
+  constexpr int kAll = WAVES > kWaves ? WAVES : kWaves;
+  __shared__ float s_m[kAll], s_l[kAll], s_o[kAll][D];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t id = (int64_t)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
+  int64_t id = (int64_t)blockIdx.x * (kAll / WAVES) + wave / WAVES;
   const int64_t all = (int64_t)a.B * a.max_rows * a.hq;
   const bool live = id < all;
   id = live ? id : all - 1;
@@ -768,7 +773,7 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
 
 bool shape_ok(int64_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len,
               int32_t window) {
-  if (T < 0 || B < 0 || hkv <= 0 || hq <= 0 || hq % hkv != 0 || !mixllm::kv4_dim_ok(dim) || max_rows < 0 ||
+  if (T < 0 || T >= (1 << 30) || B < 0 || hkv <= 0 || hq <= 0 || hq % hkv != 0 || !mixllm::kv4_dim_ok(dim) || max_rows < 0 ||
       max_len < 0 || window < 0)
     return false;
   // 32-bit row and token arithmetic: rows of a request and head, positions plus a window
@@ -787,7 +792,7 @@ void launch(const Args &a, hipStream_t s) {
   else hipLaunchKernelGGL((kv4_attention_kernel<D, 1, 1, BF16>), grid, threads, 0, s, a);
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
   const int64_t rows = (int64_t)a.B * a.max_rows * a.hq;
-  if (a.splits > 16) hipLaunchKernelGGL((kv4_join_kernel<D, 4, BF16>), dim3((unsigned)rows), threads, 0, s, a);
+  if (a.splits > 16) hipLaunchKernelGGL((kv4_join_kernel<D, 16, BF16>), dim3((unsigned)rows), dim3(1024), 0, s, a);
   else hipLaunchKernelGGL((kv4_join_kernel<D, 1, BF16>), dim3((unsigned)((rows + 3) / 4)), threads, 0, s, a);
 }
 
