@@ -381,8 +381,10 @@ int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  * workspace_dev: mixllm_kv4_attention_workspace_bytes(..) for the same arguments (0: NULL is
  *               taken); calls that may run at the same time, replays of graphs among them,
  *               need a workspace each.
- * One launch where one workgroup per 16 rows is enough, else two (the second joins).
- * Errors: E_NULL, E_SHAPE, E_SPACE, E_HIP.
+ * One launch where the workspace is 0 bytes, else two (the second joins chunks of tokens).
+ * Limits (E_SHAPE past them): B and the row tiles of a request and key/value head, at most
+ * max_rows * q_heads / kv_heads / 4, 65535 each; T, max_len and window below 2^30;
+ * B * max_rows * q_heads below 2^31.  Errors: E_NULL, E_SHAPE, E_SPACE, E_HIP.
  */
 size_t mixllm_kv4_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t dim,
                                             int32_t max_rows, int32_t max_len, int32_t window);

@@ -26,6 +26,12 @@
 // largest value scale seen so that it stays clear of fp16's subnormals.  Statistics, sums
 // and outputs are fp32.
 //
+// What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of 8192 tokens,
+// 946 MB: 188 us, 5.03 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
+// the last workgroups where there is less (32 requests, 127 MB: 35 us, 21.7 at the copy's
+// rate); for prompts (2 x 1024 rows: 251 us, 435 TFLOP/s) the registers, which leave 2 waves
+// per SIMD to hide the making of operands and the softmax between the matrix instructions.
+//
 // A decode step is bound by reading the cache: D * 9 / 8 bytes per token and head.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -135,13 +141,15 @@ struct Const {
 };
 
 // How many query rows a tile has and what follows from it.  16 rows fill the operands'
-// columns.  Where a request and head has fewer (a decode step has q_heads / kv_heads), a tile
-// has 16 / V rows, V = 2 or 4, and column n stands for row n % (16 / V) over the runs x of
-// tokens with x % V = n / (16 / V): the V columns of a row keep statistics and sums of their
+// columns.  Where a request and head has 8 or 4 at most (a decode step has q_heads / kv_heads),
+// a tile has 16 / V rows, V = 2 or 4, and column n stands for row n % (16 / V) over the runs x
+// of tokens with x % V = n / (16 / V): the V columns of a row keep statistics and sums of their
 // own, like workgroups that split the tokens, and are joined at the end.  The operands are
 // zero where a column and a run do not belong together, so the products cost what they cost
-// for 16 rows, but the scores, exponentials and parameters are 4 per lane for V runs and not
-// for each: of about 290 vector operations for 32 tokens at D = 128 they are two thirds.
+// for 16 rows, but the scores, exponentials and parameters, most of the vector operations,
+// are 4 per lane for V runs and not for each.  With more than 16 rows a tile has 32, CT = 2
+// column blocks that share each operand made of codes (prompts of 2 x 1024 rows, 8 rows a
+// token: 251 us, 263 with 16).
 template <int D, int V>
 struct Shape {
   static constexpr int kRows = kCols / V;
@@ -749,8 +757,10 @@ __global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void kv4_jo
 }
 
 // How the work of a call is cut.  Rows: tiles of 4, 8, 16 or 32 (row, head) pairs of one
-// key/value head.  Tokens: so many equal chunks of each tile that about kTarget workgroups
-// run at the longest length; 256 CUs hold 2 of them each.
+// key/value head, the fewest that hold them or 32.  Tokens: so many equal chunks of each tile
+// that about kTarget workgroups run at the longest length; 256 CUs hold 2 of them each.  32
+// requests of up to 8192 tokens, 8 heads: 36.3 us with 512, 40.6 with 1024 (more to join),
+// 36.0 with 256, whose single workgroup a CU loses where there are fewer requests.
 constexpr int64_t kTarget = 512;
 
 struct Cut {
