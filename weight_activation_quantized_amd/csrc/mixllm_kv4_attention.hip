@@ -22,14 +22,14 @@
 //
 // The query is scaled by a power of two per row so that it fits fp16 (bf16 inputs lose
 // nothing but values 2^-38 below the row's largest); the probability times the value's
-// scale is rounded once to fp16 (relative 2^-11), scaled by a power of two that follows the
-// largest value scale seen so that it stays clear of fp16's subnormals.  Statistics, sums
-// and outputs are fp32.
+// scale is rounded to fp16 (relative 2^-11), scaled by a power of two that follows the
+// largest value scale seen so that it stays clear of fp16's subnormals, and for fp16 outputs
+// what that rounding leaves is a second operand.  Statistics, sums and outputs are fp32.
 //
 // What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of 8192 tokens,
 // 946 MB: 188 us, 5.03 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
 // the last workgroups where there is less (32 requests, 127 MB: 35 us, 21.7 at the copy's
-// rate); for prompts (2 x 1024 rows: 251 us, 435 TFLOP/s) the registers, which leave 2 waves
+// rate); for prompts (2 x 1024 rows: 266 us, 410 TFLOP/s) the registers, which leave 2 waves
 // per SIMD to hide the making of operands and the softmax between the matrix instructions.
 //
 // A decode step is bound by reading the cache: D * 9 / 8 bytes per token and head.
@@ -148,8 +148,8 @@ struct Const {
 // zero where a column and a run do not belong together, so the products cost what they cost
 // for 16 rows, but the scores, exponentials and parameters, most of the vector operations,
 // are 4 per lane for V runs and not for each.  With more than 16 rows a tile has 32, CT = 2
-// column blocks that share each operand made of codes (prompts of 2 x 1024 rows, 8 rows a
-// token: 251 us, 263 with 16).
+// column blocks that share each operand made of codes (prompts of 2 x 1024 rows: 4% less time
+// than with 16).
 template <int D, int V>
 struct Shape {
   static constexpr int kRows = kCols / V;
@@ -355,12 +355,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   // seen, up to kLazy, less a power k (the same in the wave) that keeps w times a value's
   // scale below 2^15 and far above fp16's subnormals.
   float4v o[CT][J];
-  // rest: the sum of the weights before their rounding to fp16 less the sum after it.  Times
-  // 8, the middle code, it goes back into the output: the rounding then acts on codes about
-  // zero, half as large as 0 .. 15 and as little one-sided as the values themselves.  Next to
-  // a bf16 output's own rounding neither shows.
-  constexpr bool kRest = !BF16;
-  float m[CT], ref[CT], limit[CT], l[CT], bias[CT][G], rest[CT][G], k = 0.0f;
+  // A weight times a value's scale is rounded to fp16 for the product.  Where the output is
+  // fp16 too that rounding would show beside the output's own (together 1.5 times its error),
+  // so what it leaves goes through the product as a second operand (prompts of 2 x 1024 rows
+  // 252 -> 266 us, decodes 0 to 1%).  A bf16 output's rounding is 8 times larger.
+  constexpr int kParts = BF16 ? 1 : 2;
+  float m[CT], ref[CT], limit[CT], l[CT], bias[CT][G], k = 0.0f;
 #pragma unroll
   for (int z = 0; z < CT; ++z) {
 #pragma unroll
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     m[z] = ref[z] = limit[z] = kLow;
     l[z] = 0.0f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) bias[z][g] = rest[z][g] = 0.0f;
+    for (int g = 0; g < G; ++g) bias[z][g] = 0.0f;
   }
   uint32_t vbits = 0;  // value scales up to this fp16 pattern fit k
 
@@ -500,19 +500,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
         limit[e] = m[e] + kLazy;
         l[e] *= f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          bias[e][g] *= f;
-          rest[e][g] *= f;
-        }
+        for (int g = 0; g < G; ++g) bias[e][g] *= f;
 #pragma unroll
         for (int j = 0; j < J; ++j) o[e][j] *= f;
       }
     }
-    half2v p[CT][S::kSets][G][2];
+    half2v p[kParts][CT][S::kSets][G][2];
 #pragma unroll
     for (int e = 0; e < CT; ++e)
 #pragma unroll
-      for (int z = 0; z < S::kSets; ++z) {
+      for (int z = 0; z < S::kSets; ++z)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float w = __builtin_amdgcn_exp2f(s[e][z][u] - ref[e]);
@@ -520,38 +517,33 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             bias[e][g] = fmaf(at(vp[z][u], G + g), w, bias[e][g]);
-            const float ps = fmaf(at(vp[z][u], g), w, 0.0f);  // as a fused sum it takes the fp16 factor as it is
-            if (kRest) rest[e][g] += ps;
-            p[e][z][g][u / 2][u % 2] = (_Float16)ps;
+            // as a fused sum it takes the fp16 factor as it is
+            const _Float16 ps = (_Float16)fmaf(at(vp[z][u], g), w, 0.0f);
+            p[0][e][z][g][u / 2][u % 2] = ps;
+            if (kParts == 2) p[kParts - 1][e][z][g][u / 2][u % 2] = (_Float16)fmaf(at(vp[z][u], g), w, -(float)ps);
           }
         }
-        if (kRest) {
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              rest[e][g] = __builtin_amdgcn_fdot2(p[e][z][g][y], half2v{(_Float16)-1.0f, (_Float16)-1.0f}, rest[e][g], false);
-        }
-      }
 #pragma unroll
     for (int y = 0; y < S::kRuns / 2; ++y) {  // two runs fill an operand
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint4v pw[CT];
+        uint4v pw[kParts][CT];
 #pragma unroll
-        for (int e = 0; e < CT; ++e)
+        for (int r = 0; r < kParts; ++r)
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            if (V == 1) {
-              pw[e][f] = __builtin_bit_cast(uint32_t, p[e][0][g][f]);
-              pw[e][2 + f] = __builtin_bit_cast(uint32_t, p[e][S::kSets - 1][g][f]);
-            } else {
-              const uint32_t w = __builtin_bit_cast(uint32_t, p[e][V == 2 ? y : 0][g][f]);
-              const int first = V == 2 ? 0 : 2 * y;  // the column part of this pair's first run
-              pw[e][f] = part == first ? w : 0u;
-              pw[e][2 + f] = part == first + 1 ? w : 0u;
+          for (int e = 0; e < CT; ++e)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              if (V == 1) {
+                pw[r][e][f] = __builtin_bit_cast(uint32_t, p[r][e][0][g][f]);
+                pw[r][e][2 + f] = __builtin_bit_cast(uint32_t, p[r][e][S::kSets - 1][g][f]);
+              } else {
+                const uint32_t w = __builtin_bit_cast(uint32_t, p[r][e][V == 2 ? y : 0][g][f]);
+                const int first = V == 2 ? 0 : 2 * y;  // the column part of this pair's first run
+                pw[r][e][f] = part == first ? w : 0u;
+                pw[r][e][2 + f] = part == first + 1 ? w : 0u;
+              }
             }
-          }
         uint32_t w[4];  // pairs of tokens, the 4 nibbles of group g's channels in each half
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
@@ -567,9 +559,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
         for (int nib = 0; nib < 4; ++nib) {
           const uint4v u = {nibble_pair(w[0], nib), nibble_pair(w[1], nib), nibble_pair(w[2], nib), nibble_pair(w[3], nib)};
 #pragma unroll
-          for (int e = 0; e < CT; ++e)
-            o[e][4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                __builtin_bit_cast(half8, u), __builtin_bit_cast(half8, pw[e]), o[e][4 * g + nib], 0, 0, 0);
+          for (int r = 0; r < kParts; ++r)
+#pragma unroll
+            for (int e = 0; e < CT; ++e)
+              o[e][4 * g + nib] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  __builtin_bit_cast(half8, u), __builtin_bit_cast(half8, pw[r][e]), o[e][4 * g + nib], 0, 0, 0);
         }
       }
     }
@@ -604,7 +598,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   for (int z = 0; z < CT; ++z) {
     l[z] = quarters_sum(l[z]);
 #pragma unroll
-    for (int g = 0; g < G; ++g) bias[z][g] = quarters_sum(kRest ? fmaf(rest[z][g], 8.0f, bias[z][g]) : bias[z][g]);
+    for (int g = 0; g < G; ++g) bias[z][g] = quarters_sum(bias[z][g]);
     if (c == 0) {
       s_m[wave][kCols * z + n] = ref[z];
       s_l[wave][kCols * z + n] = l[z];
