@@ -15,10 +15,15 @@
 // softmax statistics, the probabilities and the output's scale factors of a row stay in its
 // lanes, and only the row maximum crosses quarters.
 //
-// Codes become fp16 without arithmetic: a nibble masked in place is a subnormal fp16,
-// c 2^-24 (or 16 c 2^-24 where it sits 4 bits higher), which the matrix instruction takes
-// exactly; the power of two goes into the row's factor (keys: the query's odd nibbles are
-// pre-divided by 16).  5 integer operations make 8 operands.
+// Codes become fp16 without arithmetic: a nibble masked where it sits in a half is a subnormal
+// fp16, c 2^-24 times the power of two of its place, which goes into the row's factor.  The
+// matrix instruction takes subnormals, but lines its 32 products up by the exponent of the
+// normal range that a subnormal does not reach and cuts what lies more than about 24 bits
+// below: measured, products with c 2^-24 lose 2^-15 of the code beside the largest weight.
+// All are cut downwards, and scores and outputs are small differences of large sums, so codes
+// at bit 0 showed (60000 tokens: fp16 outputs 1.7 times the error of their rounding, lse
+// 1.5e-5 off).  So keys move to bit 4 (7 operations for 8 codes instead of 5) and values to
+// bits 2 and 6 (6 operations): 1.02 times and 1.8e-6, for 1 to 3% of the time.
 //
 // The query is scaled by a power of two per row so that it fits fp16 (bf16 inputs lose
 // nothing but values 2^-38 below the row's largest); the probability times the value's
@@ -27,9 +32,9 @@
 // what that rounding leaves is a second operand.  Statistics, sums and outputs are fp32.
 //
 // What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of 8192 tokens,
-// 946 MB: 188 us, 5.03 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
-// the last workgroups where there is less (32 requests, 127 MB: 35 us, 21.7 at the copy's
-// rate); for prompts (2 x 1024 rows: 266 us, 410 TFLOP/s) the registers, which leave 2 waves
+// 946 MB: 189 us, 5.01 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
+// the last workgroups where there is less (32 requests, 127 MB: 36 us, 21.7 at the copy's
+// rate); for prompts (2 x 1024 rows: 273 us, 400 TFLOP/s) the registers, which leave 2 waves
 // per SIMD to hide the making of operands and the softmax between the matrix instructions.
 //
 // A decode step is bound by reading the cache: D * 9 / 8 bytes per token and head.
@@ -105,17 +110,19 @@ __device__ __forceinline__ float quarters_sum(float v) {
   return __uint_as_float(a.x) + __uint_as_float(a.y);
 }
 
-// 8 codes of a dword as fp16 operands in the nibble order 0 4 1 5 2 6 3 7; nibbles 1, 3, 5
-// and 7 come out 16 times larger.
+// 8 codes of a dword as fp16 operands c 2^-20, in the nibble order 0 4 1 5 2 6 3 7.
+constexpr float kKeyUnit = 0x1p-20f;
 __device__ __forceinline__ half8 codes8(uint32_t w) {
-  const uint32_t v = w >> 8;
-  const uint4v r = {w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u};
+  constexpr uint32_t mask = 0x00F000F0u;
+  const uint4v r = {w << 4 & mask, w & mask, w >> 4 & mask, w >> 8 & mask};
   return __builtin_bit_cast(half8, r);
 }
 
+// Nibble `nib` of both halves: c 2^-22, or c 2^-18 for odd ones.
 __device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int nib) {
-  return (nib >= 2 ? w >> 8 : w) & (nib & 1 ? 0x00F000F0u : 0x000F000Fu);
+  return (nib >= 2 ? w >> 6 : w << 2) & (nib & 1 ? 0x03C003C0u : 0x003C003Cu);
 }
+constexpr float kEvenUnit = 0x1p-22f, kOddUnit = 0x1p-18f;
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void *LdsPtr;
@@ -318,7 +325,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;  // top in [2^(e-1), 2^e)
     e = e < -100 ? -100 : e;
     const float mul = ldexpf(1.0f, 14 - e), factor = a.scale * kLog2e;
-    row_scale[z] = factor * ldexpf(1.0f, e - 14 + 24);
+    row_scale[z] = factor * (1.0f / kKeyUnit) * ldexpf(1.0f, e - 14);
 #pragma unroll
     for (int g = 0; g < G; ++g) qsum[z][g] = 0.0f;
 #pragma unroll
@@ -334,9 +341,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
       half8 v;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // nibbles p and p + 4
-        const float f = p & 1 ? mul * 0.0625f : mul;
-        v[2 * p] = (_Float16)(x[p] * f);
-        v[2 * p + 1] = (_Float16)(x[p + 4] * f);
+        v[2 * p] = (_Float16)(x[p] * mul);
+        v[2 * p + 1] = (_Float16)(x[p + 4] * mul);
       }
 #pragma unroll
       for (int y = 0; y < V; ++y) q[z][y][s] = V == 1 || part == y ? v : half8{};
@@ -616,7 +622,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     const float f = __builtin_amdgcn_exp2f(ref[z] - best);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const float fo = f * (j & 1 ? 0x1p20f : 0x1p24f), fb = f * bias[z][j / 4];
+      const float fo = f * (j & 1 ? 1.0f / kOddUnit : 1.0f / kEvenUnit), fb = f * bias[z][j / 4];
       float4v v;
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[u] = fmaf(o[z][j][u], fo, fb);
