@@ -31,13 +31,11 @@
 // largest value scale seen so that it stays clear of fp16's subnormals, and for fp16 outputs
 // what that rounding leaves is a second operand.  Statistics, sums and outputs are fp32.
 //
-// What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of 8192 tokens,
+// What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of up to 8192 tokens,
 // 946 MB: 189 us, 5.01 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
 // the last workgroups where there is less (32 requests, 127 MB: 36 us, 21.7 at the copy's
 // rate); for prompts (2 x 1024 rows: 273 us, 400 TFLOP/s) the registers, which leave 2 waves
 // per SIMD to hide the making of operands and the softmax between the matrix instructions.
-//
-// A decode step is bound by reading the cache: D * 9 / 8 bytes per token and head.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -141,7 +139,7 @@ __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 
 // A number as a type: stages are named at compile time, or the compiler takes every read of a
 // stage for one of the copies in flight and waits for them all.  With both in one array it
 // still does so in every second step; an array per stage takes that wait out too and measures
-// 1 to 2% slower (128 decodes of 8192 tokens 189.5 us for 188.0), so it stays.
+// 1 to 2% slower (128 decodes of up to 8192 tokens 189.5 us for 188.0), so it stays.
 template <int N>
 struct Const {
   static constexpr int value = N;
@@ -759,7 +757,7 @@ __global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void kv4_jo
 // How the work of a call is cut.  Rows: tiles of 4, 8, 16 or 32 (row, head) pairs of one
 // key/value head, the fewest that hold them or 32.  Tokens: so many equal chunks of each tile
 // that about kTarget workgroups run at the longest length; 256 CUs hold 2 of them each.  32
-// requests of up to 8192 tokens, 8 heads: 36.3 us with 512, 40.6 with 1024 (more to join),
+// requests of up to 4001 tokens, 8 heads: 36.3 us with 512, 40.6 with 1024 (more to join),
 // 36.0 with 256, whose single workgroup a CU loses where there are fewer requests.
 constexpr int64_t kTarget = 512;
 
