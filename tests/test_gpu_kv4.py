@@ -397,6 +397,26 @@ def test_extreme_values(L, dtype, vscale, qscale):
     compare(out, lse, q, [parts], [n], [1], dtype, scale)
 
 
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (24, 3, 64), (16, 1, 256), (40, 1, 128)])
+def test_half_outputs_are_nearly_rounded(L, hq, hkv, dim):
+    """fp16 outputs have the error of their own rounding and little else: 1.1 times it, that is
+    0.45 of it added in squares, 0.45 * 2^-11 / sqrt(3) / 1.44 = 9e-5 of an output.  What is added:
+    the two operands of a weight hold it to 2^-22; a product of codes at bit 2 of a subnormal
+    operand is cut below 2^10 2^-24 2^-2 = 2^-16 of the largest w s beside it, by half of that
+    where it is cut at all, of 100 weights whose products with codes are 1 to 15: 100 2^-17 / 15 =
+    5e-5 of the largest weight's share at the most; scores are off by 2^-19 or less.  A weight
+    in one fp16 operand adds up to 2^-11 / sqrt(3) / 1.44 = 2e-4: up to 1.4 times."""
+    lens = [100] * 6
+    dev, table, kv = build(lens, hkv, dim, 16, torch.float16, 71)
+    q = rounded(np.random.default_rng(8).normal(size=(len(lens), hq, dim)).astype(np.float32), torch.float16)
+    U.say("attention half outputs", hq, hkv, dim)
+    out, _ = attend(L, q, dev, table, lens, [1] * len(lens), 16, torch.float16, dim ** -0.5)
+    out = out.float().cpu().numpy().astype(np.float64)
+    want = np.stack([S.attention(q[b:b + 1], kv[b][0], kv[b][2], 100, dim ** -0.5, 0, ())[0][0] for b in range(len(lens))])
+    own, rounding = np.square(out - want).mean(), np.square(want.astype(np.float16) - want).mean()
+    assert own <= 1.1 ** 2 * rounding, (own / rounding) ** 0.5
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 2.0])
 @pytest.mark.parametrize("rows", [1, 3, 40])
 def test_any_finite_scale(L, scale, rows):
