@@ -97,6 +97,12 @@ def test_attention_refusals(over, status):
     assert call(L.library_handle().mixllm_kv4_attention, ATT, **over) == status
 
 
+@pytest.mark.parametrize("over", [dict(t=1 << 30), dict(window=1 << 30), dict(b=65536), dict(max_rows=1 << 28),
+                                  dict(b=60000, max_rows=2000)])
+def test_attention_limits(over):
+    assert call(L.library_handle().mixllm_kv4_attention, ATT, **over) == SHAPE
+
+
 def test_sizes():
     assert L.mixllm_kv4_page_bytes(16, 8, 128) == 16 * 8 * 144
     assert L.mixllm_kv4_page_bytes(64, 1, 64) == 64 * 72
