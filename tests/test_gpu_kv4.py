@@ -8,6 +8,11 @@ the cache stands for (64 bits):
   relative error of a probability <= e := (2 D + 16) 2^-24 size + 2^-21 (exp2 and its argument);
 * a weight s P is rounded once to fp16: 2^-11 of s c P, with s c <= |v| + |m|; sums over the
   tokens in fp32 add 2^-24 per token and step of the tree, below 2^-13 in all here;
+* the matrix instruction cuts its products (of subnormal codes) at 2^10 2^-24 2^-p of a code
+  beside its largest factor, p the lowest bit the codes are at: keys (p = 4) 2^-18 / 15 of the
+  largest term, D times at most, which is less than the 3 (2 D + 16) 2^-24 that the bound below
+  takes of `size`; values (p = 2) 2^-16 s of the largest weight, 32 times, where its mass is s c +
+  |m| with |m| > 5 s here: below the 2^-13;
 * so |out - exact| <= (2^-11 + 2^-13 + 2 e) (mass of P (s c + |m|)), plus half a step of the
   output's type;
 * lse: e + 2^-20 (1 + |lse|).
