@@ -1,0 +1,60 @@
+"""The layers' own checks, on the host: a call that cannot be right is refused before anything
+is launched.  The library's calls are replaced by ones that note their names, so nothing here
+needs a GPU."""
+import numpy as np
+import pytest
+
+from weight_activation_quantized_amd import workloads as WL
+
+L = pytest.importorskip("weight_activation_quantized_amd.mixllm")
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names and arguments of the device calls made, which do nothing."""
+    made = []
+    for name in ("mixllm_quant_act", "mixllm_silu_mul_quant", "mixllm_gemm_w4w8a8", "mixllm_residual_norm", "mixllm_kv_plan",
+                 "mixllm_kv4_append", "mixllm_kv4_attention"):
+        monkeypatch.setattr(L, name, lambda *a, _name=name, **k: made.append((_name, a)))
+    return made
+
+
+def weights(n, k, seed):
+    return WL.make_weights(n, k, (seed,)), WL.make_idx8(n, 5, (seed,))
+
+
+def layers():
+    (wq, iq), (wk, ik), (wv, iv) = (weights(n, 256, i) for i, n in enumerate((128, 64, 64)))
+    (wg, ig), (wu, iu), (wd, idn) = weights(128, 256, 3), weights(128, 256, 4), weights(256, 128, 5)
+    return {"linear": L.PackedLinear(wq, iq, "cpu"), "qkv": L.QKVProjection(wq, wk, wv, iq, ik, iv, "cpu"),
+            "mlp": L.MLPBlock(wg, wu, wd, ig, iu, idn, "cpu")}
+
+
+@pytest.mark.parametrize("name", ["linear", "qkv", "mlp"])
+@pytest.mark.parametrize("rows", [3, 8])
+def test_buffers_of_another_number_of_rows(calls, name, rows):
+    """Quantization packs its scales by the input's rows, the GEMM reads them by the buffers'."""
+    layer = layers()[name]
+    a = torch.zeros((rows, 256), dtype=torch.float16)
+    with pytest.raises(ValueError, match="rows"):
+        layer.forward(a, layer.buffers(5))
+    assert not calls
+    layer.forward(a, layer.buffers(rows))
+    assert [a[4] for n, a in calls if n == "mixllm_gemm_w4w8a8"] == [rows] * (2 if name == "mlp" else 1)
+
+
+@pytest.mark.parametrize("name", ["linear", "qkv", "mlp"])
+def test_no_rows_are_no_rows_in_any_buffers(calls, name):
+    layer = layers()[name]
+    layer.forward(torch.zeros((0, 256), dtype=torch.float16), layer.buffers(5))
+    assert {a[4] for n, a in calls if n == "mixllm_gemm_w4w8a8"} == {0}
+
+
+def test_blocks_buffers_that_do_not_fit_each_other(calls):
+    mlp = layers()["mlp"]
+    bufs = dict(mlp.buffers(4), h=mlp.down.buffers(6))
+    for run in (lambda: mlp.forward(torch.zeros((4, 256), dtype=torch.float16), bufs), lambda: mlp.forward_quantized(bufs)):
+        with pytest.raises(ValueError, match="rows"):
+            run()
+        assert not calls

@@ -597,6 +597,13 @@ def rowop_buffer(m: int, k: int, device="cuda"):
 
 # ---------------------------------------------------------------------------- convenience
 
+def _same_rows(bufs, m):
+    """The quantized operands are packed by the number of rows: buffers for another number would
+    be written by one and read by the other.  No rows: nothing is read."""
+    if m and bufs["aq"].shape[0] != m:
+        raise ValueError(f"the buffers are for {bufs['aq'].shape[0]} rows, the input has {m} rows")
+
+
 class PackedLinear:
     """A packed layer resident on the GPU plus the buffers one forward pass needs.
 
@@ -627,13 +634,16 @@ class PackedLinear:
     def forward(self, a, bufs=None, stream=None):
         m = a.shape[0]
         bufs = bufs or self.buffers(m)
+        _same_rows(bufs, m)
         mixllm_quant_act(a, bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], stream)
-        return self.gemm(bufs, stream)
+        return self.gemm(bufs, stream, m)
 
-    def gemm(self, bufs, stream=None):
-        """The product alone, of activations that are quantized in ``bufs`` already."""
-        mixllm_gemm_w4w8a8(bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], bufs["aq"].shape[0], self.n, self.k,
-                           self.n8, self.blob, bufs["y"], bufs["ws"], stream)
+    def gemm(self, bufs, stream=None, rows=None):
+        """The product alone, of activations that are quantized in ``bufs`` already (as many
+        rows as the buffers have, unless ``rows`` is given)."""
+        m = bufs["aq"].shape[0] if rows is None else rows
+        mixllm_gemm_w4w8a8(bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], m, self.n, self.k, self.n8, self.blob,
+                           bufs["y"], bufs["ws"], stream)
         return bufs["y"]
 
 
@@ -702,17 +712,22 @@ class MLPBlock:
                     h16=torch.empty((m, self.inter), dtype=torch.float16, device=dev))
 
     def forward(self, x, bufs, stream=None, keep_h=False):
-        bx = bufs["x"]
+        bx, m = bufs["x"], x.shape[0]
+        for b in (bx, bufs["h"]):
+            _same_rows(b, m)
         mixllm_quant_act(x, bx["aq"], bx["sa"], bx["asum"], bx["rowop"], stream)
-        return self.forward_quantized(bufs, stream, keep_h)
+        return self.forward_quantized(bufs, stream, keep_h, m)
 
-    def forward_quantized(self, bufs, stream=None, keep_h=False):
-        """The block from a hidden state that is quantized in ``bufs["x"]`` already."""
+    def forward_quantized(self, bufs, stream=None, keep_h=False, rows=None):
+        """The block from a hidden state that is quantized in ``bufs["x"]`` already (as many
+        rows as the buffers have, unless ``rows`` is given)."""
         bx, bh = bufs["x"], bufs["h"]
-        gu = self.gu.gemm(bx, stream)
+        m = bx["aq"].shape[0] if rows is None else rows
+        _same_rows(bh, m)
+        gu = self.gu.gemm(bx, stream, m)
         mixllm_silu_mul_quant(gu[:, :self.inter], gu[:, self.inter:], bh["aq"], bh["sa"], bh["asum"], bh["rowop"],
                               bufs["h16"] if keep_h else None, stream)
-        return self.down.gemm(bh, stream)
+        return self.down.gemm(bh, stream, m)
 
     def capture(self, x, bufs, keep_h=False):
         """A HIP graph of one forward pass on these buffers (torch.cuda.CUDAGraph)."""
