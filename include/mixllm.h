@@ -373,7 +373,8 @@ int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  *
  * q_dev, out_dev: [T][ldq], [T][ldo] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head x of a row
  *               at x * dim; strides >= q_heads * dim and % 8 == 0.
- * table_dev, lens_dev, cu_dev: as mixllm_kv_plan leaves them (its lens_out).
+ * table_dev, lens_dev, cu_dev: as mixllm_kv_plan leaves them (its lens_out), of the same B.
+ *               Rows from T on are left out, and count in n_b.
  * max_rows, max_len: bounds the caller promises for n_b and lens[b]; rows and tokens beyond
  *               them are ignored.  They size the launch: keep them near the truth.
  * Rows outside cu[0] .. cu[B]-1 of out and lse are left as they were.

@@ -1,0 +1,66 @@
+"""Calls of the 4-bit cache's operators at the ends of what their documentation allows: row
+buffers shorter than the requests' rows, memory that no token was written to inside a page that
+is read, scores near the ends of fp32.  Tolerances as in test_gpu_kv4.py."""
+import numpy as np
+import pytest
+
+from oracle import serving_oracle as S
+from tests import gpu_util as U
+from tests import test_gpu_kv4 as K
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    from weight_activation_quantized_amd import mixllm
+    return mixllm
+
+
+def call(L, q, dev, table, lens, cu, page, max_rows, max_len, scale, window=0):
+    """Attention of the rows q [T], whatever cu says; out and lse as they are left."""
+    out = torch.full_like(q, 9.0)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    size = L.mixllm_kv4_attention_workspace_bytes(q.shape[0], len(lens), q.shape[1], dev.shape[1], q.shape[2], max_rows,
+                                                  max_len, window)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda") if size else None
+    L.mixllm_kv4_attention(q, dev, K.cuda(table), K.i32(lens), K.i32(cu), out, page, max_rows, max_len, scale=scale,
+                           window=window, lse=lse, workspace=ws)
+    return out, lse
+
+
+@pytest.mark.parametrize("before", [0, 2994])
+@pytest.mark.parametrize("window", [0, 5])
+@pytest.mark.parametrize("group", [1, 4])
+def test_rows_behind_the_buffer_do_not_move_the_others(L, before, window, group):
+    """10 rows, of which 8 fit: they have the positions of the first 8, and the two tokens that no
+    row wrote (their memory holds NaN) are not seen.  A request all behind the buffer is left out."""
+    U.say("attention rows behind the buffer", before, window, group)
+    n, dtype = before + 8, torch.float16
+    dev, table, kv = K.build([n, 20], 2, 128, 16, dtype, 61)
+    q = K.rounded(np.random.default_rng(4).normal(size=(8, 2 * group, 128)).astype(np.float32), dtype)
+    # the table's rows as they stand: two more tokens stay inside the request's last page
+    assert (n + 2 + 15) // 16 == (n + 15) // 16
+    out, lse = call(L, K.cuda(q, dtype), dev, table, [n + 2, 20], [0, 10, 13], 16, 10, n + 2, 0.1, window)
+    K.compare(out, lse, q, kv, [n], [8], dtype, 0.1, window)
+
+
+def test_row_bounds_far_behind_the_buffer(L):
+    """Row bounds that saturate, as a plan of too many tokens leaves them."""
+    U.say("attention saturated bounds")
+    dtype = torch.bfloat16
+    dev, table, kv = K.build([40, 30], 2, 64, 16, dtype, 62)
+    q = K.rounded(np.random.default_rng(4).normal(size=(3, 4, 64)).astype(np.float32), dtype)
+    for cu, window in (([0, 1, 2 ** 31 - 1], 0), ([0, 1, 2 ** 31 - 1], 2 ** 30 - 1)):
+        out, lse = call(L, K.cuda(q, dtype), dev, table, [40, 30], cu, 16, 2000, 40, 0.1, window)
+        K.compare(out[:1], lse[:1], q[:1], kv, [40], [1], dtype, 0.1, window)
+        # the second request's rows stand far before its first token: they see nothing
+        assert not out[1:].any() and torch.isneginf(lse[1:]).all()
+    for cu in ([0, 1, 1], [2 ** 31 - 1] * 3, [5, 9, 12]):
+        out, lse = call(L, K.cuda(q, dtype), dev, table, [40, 30], cu, 16, 2000, 40, 0.1)
+        K.compare(out[:cu[1] if cu[0] == 0 else 0], lse, q, kv, [40], [1 if cu[0] == 0 else 0], dtype, 0.1)
+        assert torch.all(out[1 if cu[0] == 0 else 0:] == 9.0)

@@ -173,29 +173,32 @@ struct Shape {
   static constexpr int kLoads = kRuns * (2 * kCodes + kPars);  // instructions of a stage
 };
 
-// The request, rows and tokens of a workgroup.
+// The request, rows and tokens of a workgroup.  Row i of the request has the position
+// pos0 + i; how many of its rows are computed does not move them.
 struct Tile {
-  int32_t b, h, row0, rows, nq, len, q0;  // rows: query rows of this tile; nq: of the request
+  int32_t b, h, row0, rows, n, q0, pos0;  // rows: query rows of this tile; n: of the request, computed ones
   int32_t lo, hi;                         // tokens that any of its rows sees
 };
 
 __device__ __forceinline__ Tile tile_of(const Args &a, int32_t b, int32_t h, int32_t rt) {
   Tile t;
   t.b = b, t.h = h, t.row0 = rt * a.tile_rows;
-  t.q0 = a.cu[b];
-  int32_t end = a.cu[b + 1];
-  end = end < 0 ? 0 : end < a.T ? end : a.T;
-  t.q0 = t.q0 < 0 ? 0 : t.q0;
-  t.nq = end - t.q0;
-  const int32_t take = t.nq < a.max_rows ? t.nq : a.max_rows;
+  const int32_t first_row = a.cu[b], end = a.cu[b + 1];
+  t.q0 = first_row > 0 ? first_row : 0;
+  const int32_t nq = end > t.q0 ? end - t.q0 : 0;  // rows behind T count: they are the request's last ones
+  const int32_t room = t.q0 < a.T ? a.T - t.q0 : 0;
+  t.n = nq < a.max_rows ? nq : a.max_rows;
+  t.n = t.n < room ? t.n : room;
   const int64_t cap = (int64_t)a.width << a.page_log2;
-  const int32_t most = cap < a.max_len ? (int32_t)cap : a.max_len, len = a.lens[b];
-  t.len = len < 0 ? 0 : len < most ? len : most;
-  const int64_t all = (int64_t)take * a.group;
+  const int32_t most = cap < a.max_len ? (int32_t)cap : a.max_len, held = a.lens[b];
+  const int32_t len = held < 0 ? 0 : held < most ? held : most;
+  // the host keeps max_rows below 2^30: from there down no row sees anything
+  t.pos0 = len - nq > -(1 << 30) ? len - nq : -(1 << 30);
+  const int64_t all = (int64_t)t.n * a.group;
   const int64_t left = all - t.row0;
   t.rows = left <= 0 ? 0 : left < a.tile_rows ? (int32_t)left : a.tile_rows;
   if (t.rows > 0) {
-    const int32_t first = t.len - t.nq + t.row0 / a.group, last = t.len - t.nq + (t.row0 + t.rows - 1) / a.group;
+    const int32_t first = t.pos0 + t.row0 / a.group, last = t.pos0 + (t.row0 + t.rows - 1) / a.group;
     t.hi = last + 1 > 0 ? last + 1 : 0;
     t.lo = a.window && first - a.window + 1 > 0 ? first - a.window + 1 : 0;
     t.lo = t.lo < t.hi ? t.lo : t.hi;
@@ -347,13 +350,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) qsum[z][g] = quarters_sum(qsum[z][g]) * factor;
-    const int32_t pos = t.len - t.nq + i[z];
+    const int32_t pos = t.pos0 + i[z];
     row_hi[z] = pos + 1;
     row_lo[z] = a.window ? pos - a.window + 1 : 0;
   }
   // [all_lo, all_hi): tokens that every row of the tile sees
-  const int32_t all_hi = t.len - t.nq + t.row0 / a.group + 1;
-  const int32_t all_lo = a.window ? t.len - t.nq + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
+  const int32_t all_hi = t.pos0 + t.row0 / a.group + 1;
+  const int32_t all_lo = a.window ? t.pos0 + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
 
   // The column's running sums are of weights w = 2^(score - ref): ref is the largest score
   // seen, up to kLazy, less a power k (the same in the wave) that keeps w times a value's
@@ -687,7 +690,7 @@ __global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void kv4_jo
   const int32_t i = (int32_t)(id % a.max_rows), b = (int32_t)(id / a.max_rows);
   const int32_t h = head / a.group, r = i * a.group + head % a.group, rt = r / a.tile_rows, row = r % a.tile_rows;
   const Tile t = tile_of(a, b, h, rt);
-  const bool there = live && i < t.nq;
+  const bool there = live && i < t.n;
   const int32_t nchunks = there ? chunks_of(t, chunk_of(a, t)) : 0;
   const int64_t part0 = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits;
   const float *ml = a.ws_ml + (part0 * a.tile_rows + row) * 2;
