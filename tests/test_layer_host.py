@@ -58,3 +58,15 @@ def test_blocks_buffers_that_do_not_fit_each_other(calls):
         with pytest.raises(ValueError, match="rows"):
             run()
         assert not calls
+
+
+def test_a_plan_needs_a_count_for_every_request(calls):
+    """The row bounds of the requests behind a shorter `fresh` would stay those of the step before,
+    and their rows overlap the new ones'."""
+    req = L.RequestPages(3, 8, 16, 64, 20, device="cpu")
+    for size in (2, 4, 0):
+        with pytest.raises(ValueError, match="fresh"):
+            req.plan(torch.zeros(size, dtype=torch.int32))
+    assert not calls
+    req.plan(torch.zeros(3, dtype=torch.int32))
+    assert len(calls) == 1

@@ -521,8 +521,9 @@ def _cache(cache, page, dim):
 def mixllm_kv_plan(fresh, lens, table, pool, count, page: int, pages: int, lens_out, count_out, cu, slots, pos,
                    stream=None):
     """The page tables and slot maps of a step from request lengths, on the GPU: fresh, lens,
-    lens_out: int32 [B]; table: int32 [B, width] (rows may be strided); pool: int32 [F]; count:
-    int32 [1 or more]; count_out: int32 [2]; cu: int32 [B + 1]; slots, pos: int32 [tokens]."""
+    lens_out: int32 [B] (B is fresh's size; give attention as many lengths); table: int32 [B,
+    width] (rows may be strided); pool: int32 [F]; count: int32 [1 or more]; count_out: int32 [2];
+    cu: int32 [B + 1]; slots, pos: int32 [tokens]."""
     b, tokens = fresh.numel(), slots.numel()
     dev = _gpu(fresh, "fresh")
     ptable, ldt, width = _table(table, b, dev)
@@ -762,6 +763,8 @@ class RequestPages:
 
     def plan(self, fresh, stream=None):
         """fresh: int32 [requests] tokens to add to each request; negative: it ended."""
+        if fresh.numel() != self.lens.numel():  # the row bounds of the others would stay the last step's
+            raise ValueError(f"fresh must have a count for each of the {self.lens.numel()} requests, has {fresh.numel()}")
         mixllm_kv_plan(fresh, self.lens, self.table, self.pool, self.count, self.page, self.pages, self.lens, self.count,
                        self.cu, self.slots, self.pos, stream)
         return self
