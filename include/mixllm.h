@@ -330,6 +330,9 @@ size_t mixllm_kv4_page_bytes(int32_t page, int32_t heads, int32_t dim);
  * slots_dev, pos_dev: [tokens] slot and position of every row; -1 and 0 behind the last
  *              row; slot -1 for rows of refused requests, and where the table or pool hold
  *              a page outside [0, pages) (for all rows of the request, if its first is).
+ *              Give `tokens` rows or more than the tokens added: lens_out counts those of rows
+ *              past `tokens` too, which have no slot, so nothing writes what it counts there
+ *              (mixllm_kv_plan_fit refuses such requests instead).
  * Pages of ended requests are put on top of the free ones in the order of the requests
  * (those past F are dropped; the rows keep their entries); new pages are then taken from
  * the top in the order of the requests.  A request is refused if it would grow past
@@ -341,6 +344,16 @@ int mixllm_kv_plan(const int32_t *fresh_dev, const int32_t *lens_dev, int32_t B,
                    int32_t width, int32_t *pool_dev, int32_t F, const int32_t *count_dev, int32_t page, int32_t pages,
                    int32_t *lens_out_dev, int32_t *count_out_dev, int32_t *cu_dev, int32_t *slots_dev,
                    int32_t *pos_dev, int32_t tokens, void *stream);
+
+/*
+ * The same, and a request that adds tokens is refused too if its rows would end behind `tokens`
+ * (rows of requests refused before it count, so all later ones that add tokens are): every
+ * token that lens_out counts has a row, or had one in an earlier step.
+ */
+int mixllm_kv_plan_fit(const int32_t *fresh_dev, const int32_t *lens_dev, int32_t B, int32_t *table_dev, int64_t ldt,
+                       int32_t width, int32_t *pool_dev, int32_t F, const int32_t *count_dev, int32_t page,
+                       int32_t pages, int32_t *lens_out_dev, int32_t *count_out_dev, int32_t *cu_dev,
+                       int32_t *slots_dev, int32_t *pos_dev, int32_t tokens, void *stream);
 
 /*
  * Quantizes the keys and values of T rows and writes them to their slots (device).

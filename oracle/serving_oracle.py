@@ -78,8 +78,9 @@ def kv4_write(cache, slots, k, v, page):
 
 # ------------------------------------------------------------------------------ the plan
 
-def kv_plan(fresh, lens, table, pool, count, page, pages, tokens):
-    """The plan of a step, request by request.  Returns a dict; inputs are not changed."""
+def kv_plan(fresh, lens, table, pool, count, page, pages, tokens, fit=False):
+    """The plan of a step, request by request; with ``fit`` a request whose rows do not fit is
+    refused.  Returns a dict; inputs are not changed."""
     table, pool = table.copy(), pool.copy()
     b_all, width = table.shape
     cap = width * page
@@ -94,18 +95,19 @@ def kv_plan(fresh, lens, table, pool, count, page, pages, tokens):
                 top += 1
     top = min(top, len(pool))
     lens_out, cu, slots, pos, ok = [], [0], [], [], []
-    needed = taken = 0
+    needed = taken = rows = 0
     for b in range(b_all):
         f = int(fresh[b])
         add = max(f, 0)
         cu.append(min(cu[-1] + add, 2 ** 31 - 1))   # saturates
+        rows += add
         if f < 0:
             lens_out.append(0)
             ok.append(True)
             continue
         fits = held[b] + add <= cap
         need = -(-(held[b] + add) // page) - have[b] if fits else 0
-        good = fits and (need == 0 or needed + need <= top)
+        good = fits and (need == 0 or needed + need <= top) and not (fit and add and rows > tokens)
         if good and need:
             for j in range(need):
                 table[b, have[b] + j] = pool[top - 1 - needed - j]

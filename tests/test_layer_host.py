@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 def calls(monkeypatch):
     """Names and arguments of the device calls made, which do nothing."""
     made = []
-    for name in ("mixllm_quant_act", "mixllm_silu_mul_quant", "mixllm_gemm_w4w8a8", "mixllm_residual_norm", "mixllm_kv_plan",
+    for name in ("mixllm_quant_act", "mixllm_silu_mul_quant", "mixllm_gemm_w4w8a8", "mixllm_residual_norm", "mixllm_kv_plan_fit",
                  "mixllm_kv4_append", "mixllm_kv4_attention"):
         monkeypatch.setattr(L, name, lambda *a, _name=name, **k: made.append((_name, a)))
     return made
@@ -69,4 +69,4 @@ def test_a_plan_needs_a_count_for_every_request(calls):
             req.plan(torch.zeros(size, dtype=torch.int32))
     assert not calls
     req.plan(torch.zeros(3, dtype=torch.int32))
-    assert len(calls) == 1
+    assert [n for n, _ in calls] == ["mixllm_kv_plan_fit"]

@@ -29,6 +29,7 @@ struct PlanArgs {
   int32_t *table, *pool, *lens_out, *count_out, *cu, *slots, *pos;
   int64_t ldt;
   int32_t B, width, F, page_log2, pages, tokens;
+  int64_t room;  // rows that requests may have: one whose rows end behind it is refused
 };
 
 // Inclusive sum over the lanes of a wave: within rows of 16 lanes, then the rows' last
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
       pre = block_scan(r, tmp[0], &sum);
     }
     const int64_t before = needed + pre.need, row = rows + pre.add();
-    const bool ok = r.ended || (r.fits && (r.need == 0 || before + r.need <= top));
+    const bool ok = r.ended || (r.fits && (r.need == 0 || before + r.need <= top) && (r.add == 0 || row + r.add <= a.room));
     if (in) {
       const int32_t at = (int32_t)(row < 0x7FFFFFFF ? row : 0x7FFFFFFF);
       if (ok && r.need > 0) atomicMax(&s_taken, (int32_t)(before + r.need));
@@ -587,10 +588,12 @@ extern "C" size_t mixllm_kv4_page_bytes(int32_t page, int32_t heads, int32_t dim
   return (size_t)heads * mixllm::kv4_block_bytes(page, dim);
 }
 
-extern "C" int mixllm_kv_plan(const int32_t *fresh, const int32_t *lens, int32_t B, int32_t *table, int64_t ldt,
-                              int32_t width, int32_t *pool, int32_t F, const int32_t *count, int32_t page,
-                              int32_t pages, int32_t *lens_out, int32_t *count_out, int32_t *cu, int32_t *slots,
-                              int32_t *pos, int32_t tokens, void *stream) {
+namespace {
+
+int run_plan(const int32_t *fresh, const int32_t *lens, int32_t B, int32_t *table, int64_t ldt, int32_t width,
+             int32_t *pool, int32_t F, const int32_t *count, int32_t page, int32_t pages, int32_t *lens_out,
+             int32_t *count_out, int32_t *cu, int32_t *slots, int32_t *pos, int32_t tokens, int64_t room,
+             void *stream) {
   if (B < 0 || tokens < 0 || F < 0 || width <= 0 || ldt < width || pages <= 0 || !mixllm::kv4_page_ok(page))
     return MIXLLM_E_SHAPE;
   if ((int64_t)pages * page > 0x7FFFFFFF || (int64_t)width * page > 0x7FFFFFFF ||
@@ -603,7 +606,7 @@ extern "C" int mixllm_kv_plan(const int32_t *fresh, const int32_t *lens, int32_t
   for (const void *p : all)
     if (!mixllm::is_aligned4(p)) return MIXLLM_E_SHAPE;
   const PlanArgs a = {fresh, lens, count, table, pool, lens_out, count_out, cu, slots, pos, ldt, B, width, F,
-                      mixllm::log2_of(page), pages, tokens};
+                      mixllm::log2_of(page), pages, tokens, room};
   if (tokens <= kPlanOneLaunch) {
     hipLaunchKernelGGL((plan_kernel<true>), dim3(1), dim3(kPlanThreads), 0, (hipStream_t)stream, a);
     return mixllm::launch_status();
@@ -615,6 +618,24 @@ extern "C" int mixllm_kv_plan(const int32_t *fresh, const int32_t *lens, int32_t
   hipLaunchKernelGGL(plan_tokens_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0,
                      (hipStream_t)stream, a);
   return mixllm::launch_status();
+}
+
+}  // namespace
+
+extern "C" int mixllm_kv_plan(const int32_t *fresh, const int32_t *lens, int32_t B, int32_t *table, int64_t ldt,
+                              int32_t width, int32_t *pool, int32_t F, const int32_t *count, int32_t page,
+                              int32_t pages, int32_t *lens_out, int32_t *count_out, int32_t *cu, int32_t *slots,
+                              int32_t *pos, int32_t tokens, void *stream) {
+  return run_plan(fresh, lens, B, table, ldt, width, pool, F, count, page, pages, lens_out, count_out, cu, slots, pos,
+                  tokens, INT64_MAX, stream);
+}
+
+extern "C" int mixllm_kv_plan_fit(const int32_t *fresh, const int32_t *lens, int32_t B, int32_t *table, int64_t ldt,
+                                  int32_t width, int32_t *pool, int32_t F, const int32_t *count, int32_t page,
+                                  int32_t pages, int32_t *lens_out, int32_t *count_out, int32_t *cu, int32_t *slots,
+                                  int32_t *pos, int32_t tokens, void *stream) {
+  return run_plan(fresh, lens, B, table, ldt, width, pool, F, count, page, pages, lens_out, count_out, cu, slots, pos,
+                  tokens, tokens, stream);
 }
 
 extern "C" int mixllm_kv4_append(const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t dtype,

@@ -82,6 +82,8 @@ _SIGS = {
     "mixllm_kv4_page_bytes": ([_i32, _i32, _i32], _sz),
     "mixllm_kv_plan": ([_vp, _vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
                         _vp], ctypes.c_int),
+    "mixllm_kv_plan_fit": ([_vp, _vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32,
+                            _vp], ctypes.c_int),
     "mixllm_kv4_append": ([_vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _sz, _i32, _i32, _i32, _i32, _vp],
                           ctypes.c_int),
     "mixllm_kv4_read": ([_vp, _sz, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp], ctypes.c_int),
@@ -523,11 +525,22 @@ def mixllm_kv_plan(fresh, lens, table, pool, count, page: int, pages: int, lens_
     """The page tables and slot maps of a step from request lengths, on the GPU: fresh, lens,
     lens_out: int32 [B] (B is fresh's size; give attention as many lengths); table: int32 [B,
     width] (rows may be strided); pool: int32 [F]; count: int32 [1 or more]; count_out: int32 [2];
-    cu: int32 [B + 1]; slots, pos: int32 [tokens]."""
+    cu: int32 [B + 1]; slots, pos: int32 [tokens], tokens at least the sum of what is added."""
+    _plan(_lib.mixllm_kv_plan, fresh, lens, table, pool, count, page, pages, lens_out, count_out, cu, slots, pos, stream)
+
+
+def mixllm_kv_plan_fit(fresh, lens, table, pool, count, page: int, pages: int, lens_out, count_out, cu, slots, pos,
+                       stream=None):
+    """mixllm_kv_plan, which also refuses the requests whose rows do not fit slots and pos."""
+    _plan(_lib.mixllm_kv_plan_fit, fresh, lens, table, pool, count, page, pages, lens_out, count_out, cu, slots, pos,
+          stream)
+
+
+def _plan(fn, fresh, lens, table, pool, count, page, pages, lens_out, count_out, cu, slots, pos, stream):
     b, tokens = fresh.numel(), slots.numel()
     dev = _gpu(fresh, "fresh")
     ptable, ldt, width = _table(table, b, dev)
-    _on(dev, stream, _lib.mixllm_kv_plan, _flat(fresh, "fresh", _i32t, dev, 0), _flat(lens, "lens", _i32t, dev, b), b,
+    _on(dev, stream, fn, _flat(fresh, "fresh", _i32t, dev, 0), _flat(lens, "lens", _i32t, dev, b), b,
         ptable, ldt, width, _flat(pool, "pool", _i32t, dev, 0), pool.numel(), _flat(count, "count", _i32t, dev, 1), page,
         pages, _flat(lens_out, "lens_out", _i32t, dev, b), _flat(count_out, "count_out", _i32t, dev, 2),
         _flat(cu, "cu", _i32t, dev, b + 1), _flat(slots, "slots", _i32t, dev, 0), _flat(pos, "pos", _i32t, dev, tokens),
@@ -748,7 +761,9 @@ class RequestPages:
     """Which pages the requests of a batch hold: the page table, the free pages and the lengths
     of up to ``requests`` requests over caches of ``pages`` pages (every layer's cache uses the
     same).  ``plan(fresh)`` moves it on by one step on the GPU and returns the step's slots
-    and row bounds; it can be captured.  Argument marshalling only."""
+    and row bounds; it can be captured.  A request that the pages, ``max_len`` or the ``tokens``
+    rows of a step have no room for is refused: its length stays, its rows have slot -1, and
+    ``count[1]`` counts it.  Argument marshalling only."""
 
     def __init__(self, requests: int, pages: int, page: int, max_len: int, tokens: int, device="cuda"):
         if pages <= 0 or max_len <= 0:
@@ -765,8 +780,8 @@ class RequestPages:
         """fresh: int32 [requests] tokens to add to each request; negative: it ended."""
         if fresh.numel() != self.lens.numel():  # the row bounds of the others would stay the last step's
             raise ValueError(f"fresh must have a count for each of the {self.lens.numel()} requests, has {fresh.numel()}")
-        mixllm_kv_plan(fresh, self.lens, self.table, self.pool, self.count, self.page, self.pages, self.lens, self.count,
-                       self.cu, self.slots, self.pos, stream)
+        mixllm_kv_plan_fit(fresh, self.lens, self.table, self.pool, self.count, self.page, self.pages, self.lens,
+                           self.count, self.cu, self.slots, self.pos, stream)
         return self
 
 
