@@ -64,3 +64,36 @@ def test_row_bounds_far_behind_the_buffer(L):
         out, lse = call(L, K.cuda(q, dtype), dev, table, [40, 30], cu, 16, 2000, 40, 0.1)
         K.compare(out[:cu[1] if cu[0] == 0 else 0], lse, q, kv, [40], [1 if cu[0] == 0 else 0], dtype, 0.1)
         assert torch.all(out[1 if cu[0] == 0 else 0:] == 9.0)
+
+
+@pytest.mark.parametrize("dim,heads,rows", [(64, 2, 1), (64, 8, 3), (128, 2, 1), (128, 8, 1), (128, 16, 1), (128, 8, 40),
+                                            (256, 2, 1), (256, 8, 5)])
+@pytest.mark.parametrize("length", [300, 3000])
+def test_tokens_before_the_window_need_not_be_written(L, dim, heads, rows, length):
+    """Only the tokens that a row sees are in the cache (a long prompt under a window appends no
+    others): the memory before them, in the same page, holds NaN.  The rows are those of a
+    cache that has all tokens, bit for bit."""
+    U.say("attention unwritten tokens before the window", dim, heads, rows, length)
+    window, dtype = 77, torch.float16
+    dev, table, kv = K.build([length], 2, dim, 64, dtype, 63)
+    first = length - rows - window + 1
+    assert first % 16                              # inside a run of 16 tokens, and of a page
+    pos = np.arange(first, length)
+    slots = K.i32(table[0, pos // 64] * 64 + pos % 64)
+    k = torch.zeros((len(pos), 2, dim), dtype=dtype, device="cuda")
+    v = torch.zeros_like(k)
+    holes = torch.full_like(dev, 255)
+    # the seen tokens' own bytes, from the definition of the cache's layout
+    part = np.full(holes.shape, 255, np.uint8)
+    kk, vv = K.key_values(length, 2, dim, dtype, 63 * 100)
+    S.kv4_write(part, slots.tolist(), kk[first:], vv[first:], 64)
+    holes.copy_(torch.from_numpy(part))
+    L.mixllm_kv4_read(holes, slots, k, v, 64)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    q = K.cuda(K.rounded(np.random.default_rng(5).normal(size=(rows, heads, dim)).astype(np.float32), dtype), dtype)
+    full = call(L, q, dev, table, [length], [0, rows], 64, rows, length, 0.1, window)
+    for t in (table, np.where(np.arange(table.shape[1]) < first // 64, -1, table)):
+        got = call(L, q, holes, t, [length], [0, rows], 64, rows, length, 0.1, window)
+        assert torch.equal(got[0], full[0]) and torch.equal(got[1], full[1])
+    K.compare(*full, q.float().cpu().numpy(), kv, [length], [rows], dtype, 0.1, window,
+              picks=lambda n: {0, n // 2, n - 1})

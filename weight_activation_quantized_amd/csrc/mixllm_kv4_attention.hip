@@ -457,11 +457,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int32_t tok = t0 + kRun * (z * V + part) + 4 * c + u;
-          const bool there = tok < to && (here >> (z * V + part) & 1);
+          const bool there = tok < to && tok >= from && (here >> (z * V + part) & 1);
 #pragma unroll
           for (int e = 0; e < CT; ++e)
-            s[e][z][u] = there && tok < row_hi[e] && tok >= row_lo[e] && tok >= from ? s[e][z][u] : -INFINITY;
-          // what lies behind the last token may be NaN: no part of a sum, not even times zero
+            s[e][z][u] = there && tok < row_hi[e] && tok >= row_lo[e] ? s[e][z][u] : -INFINITY;
+          // What lies behind the last token, or in its run before the first one that a row sees,
+          // may never have been written and be NaN: no part of a sum, not even times zero.
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const uint32_t w = __builtin_bit_cast(uint32_t, vp[z][u][g]);
