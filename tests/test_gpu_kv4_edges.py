@@ -97,3 +97,92 @@ def test_tokens_before_the_window_need_not_be_written(L, dim, heads, rows, lengt
         assert torch.equal(got[0], full[0]) and torch.equal(got[1], full[1])
     K.compare(*full, q.float().cpu().numpy(), kv, [length], [rows], dtype, 0.1, window,
               picks=lambda n: {0, n // 2, n - 1})
+
+
+def constant_keys(n, heads, dim, dtype, level, vscale, seed):
+    """Keys that are one number per token (held exactly: s = 0), values of a given size."""
+    k = np.broadcast_to(np.asarray(level, np.float64)[:, None, None], (n, heads, dim)).astype(np.float32)
+    v = vscale * (np.random.default_rng(seed).normal(size=(n, heads, dim)) + 0.3)
+    return k, K.rounded(v.astype(np.float32), dtype)
+
+
+def cached(L, k, v, dtype, page=16):
+    n, heads, dim = k.shape
+    pages = -(-n // page) + 1
+    cache = torch.full((pages, heads, page * dim * 9 // 8), 255, dtype=torch.uint8, device="cuda")
+    L.mixllm_kv4_append(K.cuda(k, dtype), K.cuda(v, dtype), K.i32(np.arange(n)), cache, page)
+    return cache, np.arange(pages, dtype=np.int32)[None], S.kv4_values(*S.kv4_quant(v))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("vscale", [2.0 ** -19, 0.002, 0.1, 3.0, 9000.0])
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 8), (256, 4)])
+def test_scores_of_any_size(L, dtype, vscale, dim, heads):
+    """Scores from 1e6 to 1e14, where a step of fp32 is larger than a power that keeps weights in
+    fp16.  The tokens with the largest key share its score to the last bit, all others are so far
+    below that their weights are zero: the output is the mean of 1 or 2 values.  Everything
+    before the output's rounding is a sum of at most two terms with weights that are powers of
+    two: 4 fp32 roundings of |m| + 15 s, and for the values' sum the two fp16 operands' 2^-22
+    (fp16) or one operand's 2^-11 (bf16) of its s c where a weight times a scale is subnormal: a
+    step of 2^-24 beside 2^-24 of the smallest scale, less than one step of its code: s.
+    lse: the score, 2 D + 16 roundings of equal terms of one sign."""
+    U.say("attention large scores", dtype, vscale, dim, heads)
+    n = 700
+    level = np.full(n, 100.0)
+    level[200:400] = 700.0                       # the running maximum moves by large steps
+    level[[450, 451, 452]] = [800.0, 900.0, 1000.0]
+    level[[500, 650]] = 1200.0                   # the largest, in two places
+    k, v = constant_keys(n, 2, dim, dtype, level, vscale, 5)
+    cache, table, vv = cached(L, k, v, dtype)
+    c, s, m = S.kv4_quant(v)
+    most = np.repeat(15 * s.astype(np.float64) + np.abs(m.astype(np.float64)), 64, -1).reshape(v.shape)
+    step = np.repeat(s.astype(np.float64), 64, -1).reshape(v.shape)
+    q = np.full((1, heads, dim), 2000.0, np.float32)
+    for upto, tops in ((700, [500, 650]), (600, [500])):
+        for e in range(-8, 20, 2):
+            scale = 2.0 ** e * 128 / dim
+            out, lse = call(L, K.cuda(q, dtype), cache, table, [upto], [0, 1], 16, 1, upto, scale)
+            k16 = K.rounded(np.float32([1200.0]), dtype).astype(np.float64)[0]
+            score = scale * dim * 2000.0 * k16
+            o = out.float().cpu().numpy().astype(np.float64)[0].reshape(2, heads // 2, dim)
+            want, f = vv[tops].mean(0)[:, None], torch.finfo(dtype)
+            tol = 4 * 2.0 ** -24 * most[tops].max(0)[:, None] + 2.0 ** -11 * step[tops].max(0)[:, None] * 15
+            tol = tol + f.eps / 2 * (np.abs(want) + tol) + float(f.smallest_normal) * f.eps / 2
+            err = np.abs(o - want)
+            assert np.all(err <= tol), (upto, e, (err / tol).max())
+            ls = lse.cpu().numpy().astype(np.float64)
+            assert np.all(np.abs(ls - score) <= (2 * dim + 20) * 2.0 ** -24 * score + 1), (upto, e)
+
+
+@pytest.mark.parametrize("top,scale", [(119.9, 0.0884), (119.9, 0.99), (100, 2.0 ** 19), (-90, 2.0 ** 119)])
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 2), (128, 40)])
+def test_queries_to_the_ends_of_their_range(L, top, scale, dim, heads):
+    """bf16 queries up to 2^120 and scales up to it: over keys of zero every score is zero, and the
+    outputs are the mean of the values; keys that bring the scores back to ordinary sizes give
+    ordinary results."""
+    U.say("attention large queries", top, scale, dim, heads)
+    dtype, n, rows = torch.bfloat16, 300, 2
+    rng = np.random.default_rng(6)
+    g = rng.normal(size=(rows, heads, dim))
+    q = K.rounded((2.0 ** top * g / np.abs(g).max()).astype(np.float32), dtype)
+    for level in (np.zeros(n), np.where(np.arange(n) % 3 == 1, 2.0 ** -24, 0.0)):
+        if level.any() and top + np.log2(scale) > 30:
+            continue                                # no fp16 key makes these scores small
+        k, v = constant_keys(n, 1, dim, dtype, level, 0.7, 7)
+        cache, table, vv = cached(L, k, v, dtype)
+        c, s, m = S.kv4_quant(v)
+        vmost = np.repeat(15 * s.astype(np.float64) + np.abs(m.astype(np.float64)), 64, -1).reshape(v.shape)
+        kv = [[k.astype(np.float64), np.abs(k).astype(np.float64), vv, vmost]]
+        out, lse = call(L, K.cuda(q, dtype), cache, table, [n], [0, rows], 16, rows, n, scale)
+        K.compare(out, lse, q, kv, [n], [rows], dtype, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_large_scale_and_small_queries(L, dtype):
+    """scale 2^115 with bf16 queries of 2^-115, 2^14 with fp16 ones of 2^-14: ordinary scores."""
+    e = 115 if dtype == torch.bfloat16 else 14
+    U.say("attention large scale", dtype)
+    dev, table, kv = K.build([90], 2, 128, 16, dtype, 64)
+    q = K.rounded((np.random.default_rng(3).normal(size=(3, 8, 128)) * 2.0 ** -e).astype(np.float32), dtype)
+    out, lse = call(L, K.cuda(q, dtype), dev, table, [90], [0, 3], 16, 3, 90, 0.1 * 2.0 ** e)
+    K.compare(out, lse, q, kv, [90], [3], dtype, 0.1 * 2.0 ** e)

@@ -108,8 +108,16 @@ __device__ __forceinline__ float quarters_sum(float v) {
   return __uint_as_float(a.x) + __uint_as_float(a.y);
 }
 
+// m - k rounded, or the next value above it where that is more than `most` below m: from
+// |m| = 2^23 on fp32's steps are 1 or more, and a power k rounded up by them would take a weight
+// times a value's scale past fp16.
+__device__ __forceinline__ float less(float m, float k, float most) {
+  const float x = m - k;
+  return m - x > most ? __uint_as_float(__float_as_uint(x) + (x > 0.0f ? 1 : -1)) : x;
+}
+
 // 8 codes of a dword as fp16 operands c 2^-20, in the nibble order 0 4 1 5 2 6 3 7.
-constexpr float kKeyUnit = 0x1p-20f;
+constexpr int kKeyBits = 20;
 __device__ __forceinline__ half8 codes8(uint32_t w) {
   constexpr uint32_t mask = 0x00F000F0u;
   const uint4v r = {w << 4 & mask, w & mask, w >> 4 & mask, w >> 8 & mask};
@@ -326,7 +334,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
     int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;  // top in [2^(e-1), 2^e)
     e = e < -100 ? -100 : e;
     const float mul = ldexpf(1.0f, 14 - e), factor = a.scale * kLog2e;
-    row_scale[z] = factor * (1.0f / kKeyUnit) * ldexpf(1.0f, e - 14);
+    row_scale[z] = ldexpf(factor, e - 14 + kKeyBits);  // in one step: neither part has to fit fp32
 #pragma unroll
     for (int g = 0; g < G; ++g) qsum[z][g] = 0.0f;
 #pragma unroll
@@ -503,9 +511,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
 #pragma unroll
       for (int e = 0; e < CT; ++e) {
         m[e] = fmaxf(m[e], quarters_max(top[e]));
-        const float next = m[e] - k, f = __builtin_amdgcn_exp2f(ref[e] - next);
+        limit[e] = -less(-m[e], kLazy, kLazy);
+        // weights reach 2^((limit - m) + (m - next)) <= 2^(kLazy + k)
+        const float next = less(m[e], k, k + (kLazy - (limit[e] - m[e])));
+        const float f = __builtin_amdgcn_exp2f(ref[e] - next);
         ref[e] = next;
-        limit[e] = m[e] + kLazy;
         l[e] *= f;
 #pragma unroll
         for (int g = 0; g < G; ++g) bias[e][g] *= f;
