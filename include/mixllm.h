@@ -382,7 +382,9 @@ int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  * query head x on key/value head x / (q_heads / kv_heads):
  *   S_t = scale * q . k_t;  out = sum_t softmax(S)_t v_t;  lse = log sum_t exp S_t.
  * A row that sees nothing has out 0 and lse -inf.  Softmax statistics and sums are fp32, the
- * products fp16 x 4-bit codes; out is rounded once to dtype.  Scores have fp32's range: a row is
+ * products fp16 x 4-bit codes, where a weight times a value's scale is held to 2^-22, or to 2^-11 for
+ * bf16 with more than 8 rows of a request and key/value head; out is rounded once to dtype.
+ * bf16 values of q 2^-38 below the row's largest count as 0.  Scores have fp32's range: a row is
  * defined with |scale|, |q| and |scale q| below 2^120 and dim |scale q| |k| below 2^118 for
  * its largest |q| and |k|.  One that is not (or holds no number) spoils no other row.
  *

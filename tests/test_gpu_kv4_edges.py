@@ -186,3 +186,21 @@ def test_a_large_scale_and_small_queries(L, dtype):
     q = K.rounded((np.random.default_rng(3).normal(size=(3, 8, 128)) * 2.0 ** -e).astype(np.float32), dtype)
     out, lse = call(L, K.cuda(q, dtype), dev, table, [90], [0, 3], 16, 3, 90, 0.1 * 2.0 ** e)
     K.compare(out, lse, q, kv, [90], [3], dtype, 0.1 * 2.0 ** e)
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (24, 3, 64), (16, 2, 256)])
+def test_bf16_outputs_of_single_rows_are_nearly_rounded(L, hq, hkv, dim):
+    """At most one in 20 is another number than the exact output rounded once.  What the two
+    operands of a weight add is 9e-5 of an output's size (see the fp16 test of the same name): beside
+    a step of 2^-8 to 2^-7 of the value, on average 0.0054, and an error of 0.8 of its root mean
+    square on average, a share a / x of the outputs of size x, a = 0.8 9e-5 / 0.0054 = 0.013, and
+    over normally distributed ones 0.8 a (1 + ln(1 / a)) = 5.6%, less what is lost above x = 1: 5%.
+    A weight in one operand adds more than twice of that."""
+    lens = [100] * 12
+    dev, table, kv = K.build(lens, hkv, dim, 16, torch.bfloat16, 71)
+    q = K.rounded(np.random.default_rng(8).normal(size=(len(lens), hq, dim)).astype(np.float32), torch.bfloat16)
+    U.say("attention bf16 outputs", hq, hkv, dim)
+    out, _ = K.attend(L, q, dev, table, lens, [1] * len(lens), 16, torch.bfloat16, dim ** -0.5)
+    want = np.stack([S.attention(q[b:b + 1], kv[b][0], kv[b][2], 100, dim ** -0.5, 0, ())[0][0] for b in range(len(lens))])
+    differ = np.mean(out.float().cpu().numpy() != S.bf16_round(want.astype(np.float32)))
+    assert differ <= 0.05, differ

@@ -29,7 +29,8 @@
 // nothing but values 2^-38 below the row's largest); the probability times the value's
 // scale is rounded to fp16 (relative 2^-11), scaled by a power of two that follows the
 // largest value scale seen so that it stays clear of fp16's subnormals, and for fp16 outputs
-// what that rounding leaves is a second operand.  Statistics, sums and outputs are fp32.
+// and few rows what that rounding leaves is a second operand.  Statistics, sums and outputs
+// are fp32.
 //
 // What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of up to 8192 tokens,
 // 946 MB: 189 us, 5.01 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
@@ -370,11 +371,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   // seen, up to kLazy, less a power k (the same in the wave) that keeps w times a value's
   // scale below 2^15 and far above fp16's subnormals.
   float4v o[CT][J];
-  // A weight times a value's scale is rounded to fp16 for the product.  Where the output is
-  // fp16 too that rounding would show beside the output's own (together 1.5 times its error),
-  // so what it leaves goes through the product as a second operand (prompts of 2 x 1024 rows
-  // 252 -> 266 us, decodes 0 to 1%).  A bf16 output's rounding is 8 times larger.
-  constexpr int kParts = BF16 ? 1 : 2;
+  // A weight times a value's scale is rounded to fp16 for the product, which would show beside
+  // the output's own rounding (fp16: 1.5 times its error, bf16: 1.04), so what it leaves goes
+  // through the product as a second operand.  Decodes wait for memory: it costs them 0 to 3% (bf16:
+  // 131071 tokens 35.1 -> 36.1 us, 128 requests 184.2 -> 184.4).  Prompts wait for the products (2 x
+  // 1024 rows, bf16: 222.7 -> 273.6), so there bf16, whose own rounding is 8 times larger, goes without.
+  constexpr int kParts = BF16 && V == 1 ? 1 : 2;
   float m[CT], ref[CT], limit[CT], l[CT], bias[CT][G], k = 0.0f;
 #pragma unroll
   for (int z = 0; z < CT; ++z) {
