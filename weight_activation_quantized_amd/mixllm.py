@@ -7,6 +7,7 @@ raises ``MixLLMError``.  Importing this module fails loudly when the library is 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -450,6 +451,16 @@ def _on(dev, stream, fn, *args):
         raise MixLLMError(status)
 
 
+def _current(stream, dev):
+    """A context in which a stream (a torch stream, a handle or None for the current one) is
+    torch's current one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=None, asum=None, rowop=None,
                          post_weight=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-5,
                          stream=None):
@@ -814,7 +825,8 @@ class AttentionBlock:
         """h: [M, hidden] the residual stream, updated in place by the block output x of the
         layer before (None for the first); req: RequestPages after its plan(); rotate: called
         with the views q [M, heads, dim], k and the positions before the keys are written, for
-        an embedding of positions (in place).  Returns the output projection's [M, hidden]."""
+        an embedding of positions (in place, on the stream that is current then, which is
+        ``stream``).  Returns the output projection's [M, hidden]."""
         b, bo = bufs["qkv"], bufs["o"]
         m = h.shape[0]
         mixllm_residual_norm(x, h, self.norm, h if x is not None else None, aq=b["aq"], sa=b["sa"], asum=b["asum"],
@@ -824,7 +836,8 @@ class AttentionBlock:
         q, k, v = q.unflatten(1, (self.q_heads, self.dim)), k.unflatten(1, (self.kv_heads, self.dim)), v.unflatten(
             1, (self.kv_heads, self.dim))
         if rotate is not None:
-            rotate(q, k, req.pos[:m])
+            with _current(stream, q.device):  # between the product and the write, on the same stream
+                rotate(q, k, req.pos[:m])
         mixllm_kv4_append(k, v, req.slots[:m], self.cache, self.page, stream)
         mixllm_kv4_attention(q, self.cache, req.table, req.lens, req.cu, bufs["attn"], self.page, bufs["max_rows"],
                              bufs["max_len"], window=self.window, workspace=bufs["ws"], stream=stream)
