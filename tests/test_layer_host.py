@@ -70,3 +70,26 @@ def test_a_plan_needs_a_count_for_every_request(calls):
     assert not calls
     req.plan(torch.zeros(3, dtype=torch.int32))
     assert [n for n, _ in calls] == ["mixllm_kv_plan_fit"]
+
+
+def attention_block(page=16, pages=6, **kw):
+    (wq, iq), (wk, ik), (wv, iv), (wo, io) = (weights(n, k, i) for i, (n, k) in enumerate(
+        ((256, 256), (128, 256), (128, 256), (256, 256))))
+    norm = torch.ones(256, dtype=torch.float16)
+    return L.AttentionBlock(wq, wk, wv, wo, iq, ik, iv, io, norm, 4, 2, pages, page, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("page,pages,fits", [(16, 6, True), (16, 5, True), (32, 3, False), (16, 7, False), (8, 6, False)])
+def test_requests_of_other_pages(calls, page, pages, fits):
+    """Slots and page numbers mean what they mean only for caches of the same pages; a cache may have
+    more of them than the requests use."""
+    att = attention_block()
+    req = L.RequestPages(2, pages, page, 60, 10, device="cpu")
+    h = torch.zeros((3, 256), dtype=torch.float16)
+    if fits:
+        att.forward(None, h, att.buffers(3, 2, 2, 60), req)
+        assert [n for n, _ in calls][2:4] == ["mixllm_kv4_append", "mixllm_kv4_attention"]
+    else:
+        with pytest.raises(ValueError, match="pages"):
+            att.forward(None, h, att.buffers(3, 2, 2, 60), req)
+        assert not calls

@@ -827,6 +827,9 @@ class AttentionBlock:
         with the views q [M, heads, dim], k and the positions before the keys are written, for
         an embedding of positions (in place, on the stream that is current then, which is
         ``stream``).  Returns the output projection's [M, hidden]."""
+        if req.page != self.page or req.pages > self.cache.shape[0]:
+            raise ValueError(f"the requests have {req.pages} pages of {req.page} tokens, the cache has "
+                             f"{self.cache.shape[0]} pages of {self.page}")
         b, bo = bufs["qkv"], bufs["o"]
         m = h.shape[0]
         mixllm_residual_norm(x, h, self.norm, h if x is not None else None, aq=b["aq"], sa=b["sa"], asum=b["asum"],
