@@ -85,3 +85,18 @@ def test_a_layers_attention_within_the_operators_bounds(L, hq, hkv, dim, window)
                                workspace=bufs["attention"]["ws"])
         assert torch.equal(out, bufs["attention"]["attn"])
         K.compare(out, lse, q.float().cpu().numpy(), kv, lens, fresh, torch.float16, dim ** -0.5, window)
+
+
+def test_a_gate_is_per_channel_or_per_token(L):
+    """A gate of any other shape is refused, and weights of another number of channels: only the
+    first N numbers of them would be read."""
+    m, n = 4, 256
+    x, one = torch.ones((m, n), dtype=torch.float16, device="cuda"), torch.ones(n, dtype=torch.float16, device="cuda")
+    y = torch.empty_like(x)
+    L.mixllm_residual_norm(x, x, one, y=y, gate=one, post_weight=one)
+    L.mixllm_residual_norm(x, x, one, y=y, gate=x, post_weight=one)
+    more = torch.ones(m * n, dtype=torch.float16, device="cuda")
+    for bad in (dict(gate=x[None]), dict(gate=more), dict(gate=one[:1]), dict(post_weight=more), dict(post_weight=x),
+                dict(pre_weight=more), dict(gate=torch.ones((), dtype=torch.float16, device="cuda"))):
+        with pytest.raises(ValueError):
+            L.mixllm_residual_norm(**{**dict(x=x, res=x, pre_weight=one, y=y), **bad})

@@ -419,6 +419,13 @@ def _flat(t, name, dtype, dev, numel):
                      f"{t.dtype} of shape {tuple(t.shape)} on {t.device}")
 
 
+def _channels(t, name, dtype, dev, n):
+    """The address of a tensor of one number per channel."""
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, one per channel, is of shape {tuple(t.shape)}")
+    return _flat(t, name, dtype, dev, n)
+
+
 def _table(t, b, dev):
     """(address, row stride, width) of a page table of at least b rows."""
     if t.dtype is _i32t and t.dim() == 2 and t.get_device() == dev:
@@ -488,14 +495,14 @@ def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=N
     if y is not None:
         ldy, py = _ld(y, "y", t16, dev, shape, n), y.data_ptr()
     if post_weight is not None:
-        ppost = _flat(post_weight, "post_weight", t16, dev, n)
+        ppost = _channels(post_weight, "post_weight", t16, dev, n)
     if pre_weight is not None:
-        ppre = _flat(pre_weight, "pre_weight", t16, dev, n)
+        ppre = _channels(pre_weight, "pre_weight", t16, dev, n)
     if gate is not None:
-        if gate.dim() == 2:
+        if gate.dim() != 1:
             ldgate, pgate = _ld(gate, "gate", t16, dev, shape, n), gate.data_ptr()
         else:
-            pgate = _flat(gate, "gate", t16, dev, n)
+            pgate = _channels(gate, "gate", t16, dev, n)
     if aq is not None:
         g = n // GROUP
         paq = _flat(aq, "aq", torch.int8, dev, m * n)
