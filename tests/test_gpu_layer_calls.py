@@ -100,3 +100,14 @@ def test_a_gate_is_per_channel_or_per_token(L):
                 dict(pre_weight=more), dict(gate=torch.ones((), dtype=torch.float16, device="cuda"))):
         with pytest.raises(ValueError):
             L.mixllm_residual_norm(**{**dict(x=x, res=x, pre_weight=one, y=y), **bad})
+
+
+def test_scales_and_sums_without_codes_are_refused(L):
+    """They belong to the codes: without them they would be left unwritten."""
+    m, n = 4, 256
+    x, one = torch.ones((m, n), dtype=torch.float16, device="cuda"), torch.ones(n, dtype=torch.float16, device="cuda")
+    y = torch.empty_like(x)
+    for bad in (dict(sa=torch.empty((2, m), device="cuda")), dict(asum=torch.empty((2, m), dtype=torch.int32, device="cuda")),
+                dict(rowop=L.rowop_buffer(m, n))):
+        with pytest.raises(ValueError, match="aq"):
+            L.mixllm_residual_norm(x, x, one, y=y, **bad)

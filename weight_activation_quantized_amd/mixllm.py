@@ -511,6 +511,8 @@ def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=N
         psa = _flat(sa, "sa", torch.float32, dev, g * m)
         psum = _flat(asum, "asum", _i32t, dev, g * m) if asum is not None else None
         pro4 = _flat(rowop, "rowop", _i32t, dev, g * m * 8) if rowop is not None else None
+    elif sa is not None or asum is not None or rowop is not None:
+        raise ValueError("sa, asum and rowop are outputs beside the codes: aq is required")
     _on(dev, stream, _lib.mixllm_residual_norm, px, ldx, ppost, pgate, ldgate, res.data_ptr(), ldr, pro, ldro, ppre, py,
         ldy, paq, psa, psum, pro4, m, n, GROUP, dtype, res_dtype, eps, alpha, beta)
 
