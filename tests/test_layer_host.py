@@ -93,3 +93,27 @@ def test_requests_of_other_pages(calls, page, pages, fits):
         with pytest.raises(ValueError, match="pages"):
             att.forward(None, h, att.buffers(3, 2, 2, 60), req)
         assert not calls
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 16, -2 ** 31 - 1, -2 ** 32])
+def test_numbers_past_32_bits(value):
+    """They would reach the library as their low 32 bits: a longest length of 2^32 as 0."""
+    z = torch.zeros((1, 4, 128), dtype=torch.float16)
+    i = torch.zeros(1, dtype=torch.int32)
+    att = dict(q=z, cache=torch.zeros((1, 2, 16 * 144), dtype=torch.uint8), table=i[None], lens=i, cu=i, out=z, page=16,
+               max_rows=1, max_len=16, window=0)
+    for name in ("max_rows", "max_len", "window"):
+        with pytest.raises(ValueError, match="32 bits"):
+            L.mixllm_kv4_attention(**{**att, name: value})
+    sizes = dict(t=1, b=1, q_heads=4, kv_heads=2, dim=128, max_rows=1, max_len=9000, window=0)
+    assert L.mixllm_kv4_attention_workspace_bytes(**sizes) > 0
+    for name in sizes:
+        with pytest.raises(ValueError, match="32 bits"):
+            L.mixllm_kv4_attention_workspace_bytes(**{**sizes, name: value})
+    for fn in (L.mixllm_kv_plan, L.mixllm_kv_plan_fit):
+        for page, pages in ((value, 4), (16, value)):
+            with pytest.raises(ValueError, match="32 bits"):
+                fn(i, i, i[None], i, i, page, pages, i, i, i, i, i)
+    for args in ((value, 8, 128), (16, value, 128), (16, 8, value)):
+        with pytest.raises(ValueError, match="32 bits"):
+            L.mixllm_kv4_page_bytes(*args)

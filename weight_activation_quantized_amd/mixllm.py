@@ -373,6 +373,13 @@ _raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", N
 _device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None)
 
 
+_HALF = 1 << 31  # (v + _HALF) >> 32 is 0 for what fits 32 bits with a sign
+
+
+def _past32(*values):
+    raise ValueError(f"a number does not fit 32 bits, the library's integers: one of {values}")
+
+
 def _dtype16(t, name):
     """The library's number of a 16-bit element type."""
     d = t.dtype
@@ -518,6 +525,8 @@ def mixllm_residual_norm(x, res, pre_weight, res_out=None, y=None, aq=None, sa=N
 
 
 def mixllm_kv4_page_bytes(page: int, heads: int, dim: int) -> int:
+    if (page + _HALF | heads + _HALF | dim + _HALF) >> 32:
+        _past32(page, heads, dim)
     return int(_lib.mixllm_kv4_page_bytes(page, heads, dim))
 
 
@@ -558,6 +567,8 @@ def mixllm_kv_plan_fit(fresh, lens, table, pool, count, page: int, pages: int, l
 
 def _plan(fn, fresh, lens, table, pool, count, page, pages, lens_out, count_out, cu, slots, pos, stream):
     b, tokens = fresh.numel(), slots.numel()
+    if (page + _HALF | pages + _HALF | tokens + _HALF | pool.numel() + _HALF) >> 32:
+        _past32(page, pages, tokens, pool.numel())
     dev = _gpu(fresh, "fresh")
     ptable, ldt, width = _table(table, b, dev)
     _on(dev, stream, fn, _flat(fresh, "fresh", _i32t, dev, 0), _flat(lens, "lens", _i32t, dev, b), b,
@@ -594,6 +605,9 @@ def mixllm_kv4_read(cache, slots, k, v, page: int, stream=None):
 
 def mixllm_kv4_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
                                          max_len: int, window: int = 0) -> int:
+    for v in (t, b, q_heads, kv_heads, dim, max_rows, max_len, window):
+        if (v + _HALF) >> 32:
+            _past32(v)
     return int(_lib.mixllm_kv4_attention_workspace_bytes(t, b, q_heads, kv_heads, dim, max_rows, max_len, window))
 
 
@@ -604,6 +618,8 @@ def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: in
     [B + 1] first row of each request; out: as q; lse: fp32 [T, q_heads] or None; scale: 1 /
     sqrt(dim) by default; workspace: a uint8 tensor of mixllm_kv4_attention_workspace_bytes(T,
     B, ..) for the same arguments (None where that is 0)."""
+    if (max_rows + _HALF | max_len + _HALF | window + _HALF) >> 32:
+        _past32(max_rows, max_len, window)
     t, hq, dim = shape = q.shape
     dev, pcache, size, pages, heads = _cache(cache, page, dim)
     dtype, t16, width = _dtype16(q, "q"), q.dtype, hq * dim
