@@ -117,3 +117,41 @@ def test_numbers_past_32_bits(value):
     for args in ((value, 8, 128), (16, value, 128), (16, 8, value)):
         with pytest.raises(ValueError, match="32 bits"):
             L.mixllm_kv4_page_bytes(*args)
+
+
+def test_device_calls_run_on_their_tensors_device(monkeypatch):
+    """On the stream of the device that holds the tensors, not of the current one."""
+    made = []
+    monkeypatch.setattr(L, "_on", lambda dev, stream, fn, *args: made.append((dev, stream, fn.__name__)))
+    monkeypatch.setattr(L, "_gpu", lambda t, name: 1)
+    monkeypatch.setattr(L, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(L, "_gemm_inputs", lambda *a: None)
+    a, y = torch.zeros((3, 256), dtype=torch.float16), torch.zeros((3, 64), dtype=torch.float16)
+    w, idx = weights(64, 256, 1)
+    blob = L.DeviceBlob(L.mixllm_pack_weights(w, idx), "cpu")
+    for stream in (None, 5):
+        del made[:]
+        L.mixllm_quant_act(a, a, a, stream=stream)
+        L.mixllm_silu_mul_quant(a, a, a, a, stream=stream)
+        L.mixllm_gemm_w4w8a8(a, a, a, a, 3, 64, 256, 5, blob, y, stream=stream)
+        L.mixllm_gemm_w4w8a8_partials(a, a, a, a, 3, 64, 256, 5, blob, 0, 64, y, stream=stream)
+        assert [m[:2] for m in made] == [(1, stream)] * 4
+        assert [m[2] for m in made] == ["mixllm_quant_act", "mixllm_silu_mul_quant", "mixllm_gemm_w4w8a8",
+                                        "mixllm_gemm_w4w8a8_partials"]
+
+
+def test_tensors_on_the_host_are_refused(monkeypatch):
+    """Every call on a device pointer names a tensor that has none."""
+    made = []
+    monkeypatch.setattr(L, "_on", lambda *a: made.append(a))
+    a = torch.zeros((3, 256), dtype=torch.float16)
+    w, idx = weights(64, 256, 1)
+    blob = L.DeviceBlob(L.mixllm_pack_weights(w, idx), "cpu")
+    monkeypatch.setattr(L, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(L, "_gemm_inputs", lambda *a: None)
+    for run in (lambda: L.mixllm_quant_act(a, a, a), lambda: L.mixllm_silu_mul_quant(a, a, a, a),
+                lambda: L.mixllm_gemm_w4w8a8(a, a, a, a, 3, 64, 256, 5, blob, a),
+                lambda: L.mixllm_gemm_w4w8a8_partials(a, a, a, a, 3, 64, 256, 5, blob, 0, 64, a)):
+        with pytest.raises(ValueError, match="CUDA"):
+            run()
+    assert not made

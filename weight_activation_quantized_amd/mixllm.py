@@ -224,14 +224,6 @@ def mixllm_assign_channels(scores, total_8bit: int):
 
 # ---------------------------------------------------------------------------- device calls
 
-def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -240,8 +232,9 @@ def mixllm_quant_act(a, aq, sa, asum=None, rowop=None, stream=None, lib=None):
     """a: fp16 [M, K] CUDA tensor (rows may be strided); aq: int8 [M, K];
     sa: fp32 [G, M]; asum: int32 [G, M] or None; rowop: 32-bit [G, M, 8] or None."""
     m, k = a.shape
-    if a.dtype != torch.float16 or a.stride(1) != 1 or not a.is_cuda:
+    if a.dtype != torch.float16 or a.stride(1) != 1:
         raise ValueError("a must be an fp16 CUDA tensor with unit column stride")
+    dev = _gpu(a, "a")
     if m:
         g = k // GROUP
         _need(aq, "aq", torch.int8, (m, k))
@@ -251,8 +244,8 @@ def mixllm_quant_act(a, aq, sa, asum=None, rowop=None, stream=None, lib=None):
         if rowop is not None:
             _need(rowop, "rowop", torch.int32, (g, m, 8))
     lda = a.stride(0) if m > 1 else k
-    _check((lib or _lib).mixllm_quant_act(_ptr(a), lda, m, k, GROUP, _ptr(aq), _ptr(sa), _ptr(asum),
-                                          _ptr(rowop), _stream(stream)))
+    _on(dev, stream, (lib or _lib).mixllm_quant_act, _ptr(a), lda, m, k, GROUP, _ptr(aq), _ptr(sa), _ptr(asum),
+        _ptr(rowop))
 
 
 def mixllm_silu_mul_quant(gate, up, aq, sa, asum=None, rowop=None, h=None, stream=None, lib=None):
@@ -263,6 +256,9 @@ def mixllm_silu_mul_quant(gate, up, aq, sa, asum=None, rowop=None, h=None, strea
         raise ValueError("gate and up must be fp16 with unit column stride")
     if up.shape != gate.shape or (m > 1 and up.stride(0) != gate.stride(0)):
         raise ValueError("gate and up must have the same shape and row stride")
+    dev = _gpu(gate, "gate")
+    if _gpu(up, "up") != dev:
+        raise ValueError("gate and up must be on the same device")
     if m:
         g = inter // GROUP
         _need(aq, "aq", torch.int8, (m, inter))
@@ -274,8 +270,8 @@ def mixllm_silu_mul_quant(gate, up, aq, sa, asum=None, rowop=None, h=None, strea
         if h is not None:
             _need(h, "h", torch.float16, (m, inter))
     ld = gate.stride(0) if m > 1 else inter
-    _check((lib or _lib).mixllm_silu_mul_quant(_ptr(gate), _ptr(up), ld, m, inter, GROUP, _ptr(aq), _ptr(sa),
-                                               _ptr(asum), _ptr(rowop), _ptr(h), _stream(stream)))
+    _on(dev, stream, (lib or _lib).mixllm_silu_mul_quant, _ptr(gate), _ptr(up), ld, m, inter, GROUP, _ptr(aq), _ptr(sa),
+        _ptr(asum), _ptr(rowop), _ptr(h))
 
 
 def mixllm_gemm_workspace_bytes(m: int, n: int, k: int, n8: int) -> int:
@@ -341,9 +337,8 @@ def mixllm_gemm_w4w8a8(aq, sa, asum, rowop, m: int, n: int, k: int, n8: int, blo
             raise ValueError("y must be 2-D")
     ldy = y.stride(0) if y is not None and y.dim() == 2 and m > 1 else n
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check((lib or _lib).mixllm_gemm_w4w8a8(_ptr(aq), _ptr(sa), _ptr(asum), _ptr(rowop), m, n, k, n8,
-                                            ctypes.byref(b.info), _ptr(b.dev), b.nbytes, _ptr(y), ldy,
-                                            _ptr(workspace), ws, _stream(stream)))
+    _on(_gpu(b.dev, "blob"), stream, (lib or _lib).mixllm_gemm_w4w8a8, _ptr(aq), _ptr(sa), _ptr(asum), _ptr(rowop), m, n,
+        k, n8, ctypes.byref(b.info), _ptr(b.dev), b.nbytes, _ptr(y), ldy, _ptr(workspace), ws)
 
 
 def mixllm_gemm_w4w8a8_partials(aq, sa, asum, rowop, m: int, n: int, k: int, n8: int, blob, n_begin: int,
@@ -355,9 +350,8 @@ def mixllm_gemm_w4w8a8_partials(aq, sa, asum, rowop, m: int, n: int, k: int, n8:
         _need(part, "part", torch.int32, (m, n_count, k // GROUP))
         if not part.is_contiguous():
             raise ValueError("part must be contiguous")
-    _check((lib or _lib).mixllm_gemm_w4w8a8_partials(_ptr(aq), _ptr(sa), _ptr(asum), _ptr(rowop), m, n, k, n8,
-                                                     ctypes.byref(b.info), _ptr(b.dev), b.nbytes, n_begin,
-                                                     n_count, _ptr(part), _stream(stream)))
+    _on(_gpu(b.dev, "blob"), stream, (lib or _lib).mixllm_gemm_w4w8a8_partials, _ptr(aq), _ptr(sa), _ptr(asum),
+        _ptr(rowop), m, n, k, n8, ctypes.byref(b.info), _ptr(b.dev), b.nbytes, n_begin, n_count, _ptr(part))
 
 
 # ------------------------------------------------------------- between the packed layers
