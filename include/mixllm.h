@@ -276,9 +276,10 @@ int mixllm_gemm_w4w8a8_partials(const int8_t *aq_dev, const float *sa_dev, const
  *              NULL for none; at least one of y and aq when pre is given.
  * dtype:       MIXLLM_FP16 or MIXLLM_BF16: x, post, gate, pre, y.
  * res_dtype:   dtype or MIXLLM_FP32: h and h'.
- * N <= 65536; any N, stride and element-aligned pointer without the int8 outputs; 16-byte
- * aligned rows (strides % 8 == 0) run faster.  With them N % 128 == 0, strides % 8 == 0
- * and 16-byte aligned pointers.  eps >= 0.
+ * N <= 65536, M below 2^26 up to N = 512, 2^24 up to 4096, 2^23 up to 16384, else 2^22.
+ * Any N, stride and element-aligned pointer without the int8 outputs; 16-byte aligned rows
+ * (strides % 8 == 0) run faster.  With them N % 128 == 0, strides % 8 == 0 and 16-byte
+ * aligned pointers.  eps >= 0.
  * Errors: E_NULL, E_SHAPE, E_GROUP, E_HIP.
  * ------------------------------------------------------------------------------------ */
 int mixllm_residual_norm(const void *x_dev, int64_t ldx, const void *post_dev, const void *gate_dev, int64_t ldgate,
@@ -359,6 +360,7 @@ int mixllm_kv_plan_fit(const int32_t *fresh_dev, const int32_t *lens_dev, int32_
  * Quantizes the keys and values of T rows and writes them to their slots (device).
  * k_dev, v_dev: [T][ldk], [T][ldv] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head h of a row at
  *               h * dim; strides >= heads * dim and % 8 == 0, so slices of one GEMM output do.
+ * T (in whole 16s) * heads below 2^28, heads below 2^16.
  * slots_dev:    [T]; rows without a slot are skipped, everything else in the cache is left
  *               as it was.  Two rows with one slot leave that token unspecified (no other).
  * Errors: E_NULL, E_SHAPE, E_SPACE (cache_bytes < pages * mixllm_kv4_page_bytes), E_HIP.

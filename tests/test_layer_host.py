@@ -4,10 +4,13 @@ needs a GPU."""
 import numpy as np
 import pytest
 
+from tests import test_serving_host as H
 from weight_activation_quantized_amd import workloads as WL
 
 L = pytest.importorskip("weight_activation_quantized_amd.mixllm")
 torch = pytest.importorskip("torch")
+
+H_WIDE = dict(ldx=16512, ldr=16512, ldro=16512, ldy=16512)
 
 
 @pytest.fixture
@@ -155,3 +158,13 @@ def test_tensors_on_the_host_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="CUDA"):
             run()
     assert not made
+
+
+@pytest.mark.parametrize("name,over", [
+    ("mixllm_residual_norm", dict(m=1 << 26)), ("mixllm_residual_norm", dict(m=1 << 24, n=640, **H_WIDE)), ("mixllm_residual_norm", dict(m=1 << 23, n=4224, **H_WIDE)),
+    ("mixllm_residual_norm", dict(m=1 << 22, n=16512, **H_WIDE)), ("mixllm_kv4_append", dict(t=(1 << 25) - 15)),
+    ("mixllm_kv4_read", dict(t=1 << 30)), ("mixllm_kv4_append", dict(t=2 ** 31 - 1))])
+def test_more_rows_than_a_launch_has_threads(name, over):
+    """Refused on the host, before any launch."""
+    base = {"mixllm_residual_norm": H.NORM, "mixllm_kv4_append": H.APPEND, "mixllm_kv4_read": H.READ}[name]
+    assert H.call(getattr(L.library_handle(), name), base, **over) == H.SHAPE

@@ -555,7 +555,9 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
   const int st = mixllm::kv4_check_cache(cache, cache_bytes, pages, page, heads, dim);
   if (st != MIXLLM_OK) return st;
   const int64_t width = (int64_t)heads * dim;
-  if (heads > 65535 || ((int64_t)T + 15) / 16 * heads > 0x7FFFFFFF || ldk < width || ldv < width || ldk % 8 != 0 || ldv % 8 != 0) return MIXLLM_E_SHAPE;
+  // a launch has fewer than 2^32 threads, 256 for 16 rows of a head
+  if (heads > 65535 || ((int64_t)T + 15) / 16 * heads >= 1 << 24) return MIXLLM_E_SHAPE;
+  if (ldk < width || ldv < width || ldk % 8 != 0 || ldv % 8 != 0) return MIXLLM_E_SHAPE;
   if (!k || !v || !slots) return MIXLLM_E_NULL;
   if (!mixllm::is_aligned16(k) || !mixllm::is_aligned16(v) || !mixllm::is_aligned4(slots)) return MIXLLM_E_SHAPE;
   return MIXLLM_OK;

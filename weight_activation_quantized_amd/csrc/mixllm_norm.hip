@@ -238,6 +238,8 @@ extern "C" int mixllm_residual_norm(const void *x, int64_t ldx, const void *post
                                     int32_t M, int32_t N, int32_t group, int32_t dtype, int32_t res_dtype, float eps,
                                     float alpha, float beta, void *stream) {
   if (group != MIXLLM_GROUP) return MIXLLM_E_GROUP;
+  // a launch has fewer than 2^32 threads; so many rows take 64, 256, 512 or 1024 each
+  if (M >= (N <= 512 ? 1 << 26 : N <= 4096 ? 1 << 24 : N <= 16384 ? 1 << 23 : 1 << 22)) return MIXLLM_E_SHAPE;
   if (M < 0 || N <= 0 || N > kMaxN || (dtype != MIXLLM_FP16 && dtype != MIXLLM_BF16) ||
       (res_dtype != dtype && res_dtype != MIXLLM_FP32) || !(eps >= 0.0f))
     return MIXLLM_E_SHAPE;
