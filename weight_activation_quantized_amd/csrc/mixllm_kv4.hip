@@ -7,8 +7,17 @@
 #include <stdint.h>
 
 #include "mixllm_kv4.h"
+#include "mixllm_lanes.h"
 
 namespace {
+
+using mixllm::down;
+using mixllm::kDppHalfMirror;
+using mixllm::kDppMirror;
+using mixllm::kDppXor1;
+using mixllm::kDppXor2;
+using mixllm::moved;
+using mixllm::up;
 
 // ---------------------------------------------------------------------------------------
 // The plan.
@@ -257,48 +266,21 @@ constexpr int32_t kPlanOneLaunch = 4096;
 // fp32 extremes, 15.3 as written (12 of it without any store); reading them back takes 8.8.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kDppXor1 = 0xB1;        // quad_perm [1, 0, 3, 2]
-constexpr int kDppXor2 = 0x4E;        // quad_perm [2, 3, 0, 1]
-constexpr int kDppHalfMirror = 0x141;
-constexpr int kDppMirror = 0x140;
-
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t moved(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
-}
-
 // Minimum and maximum over LANES (4, 8 or 16) neighbouring lanes of a quarter.
 template <int LANES>
 __device__ __forceinline__ void lanes_minmax(float &lo, float &hi) {
-  lo = fminf(lo, dpp<kDppXor1>(lo));
-  hi = fmaxf(hi, dpp<kDppXor1>(hi));
-  lo = fminf(lo, dpp<kDppXor2>(lo));
-  hi = fmaxf(hi, dpp<kDppXor2>(hi));
+  lo = fminf(lo, moved<kDppXor1>(lo));
+  hi = fmaxf(hi, moved<kDppXor1>(hi));
+  lo = fminf(lo, moved<kDppXor2>(lo));
+  hi = fmaxf(hi, moved<kDppXor2>(hi));
   if (LANES >= 8) {
-    lo = fminf(lo, dpp<kDppHalfMirror>(lo));
-    hi = fmaxf(hi, dpp<kDppHalfMirror>(hi));
+    lo = fminf(lo, moved<kDppHalfMirror>(lo));
+    hi = fmaxf(hi, moved<kDppHalfMirror>(hi));
   }
   if (LANES >= 16) {
-    lo = fminf(lo, dpp<kDppMirror>(lo));
-    hi = fmaxf(hi, dpp<kDppMirror>(hi));
+    lo = fminf(lo, moved<kDppMirror>(lo));
+    hi = fmaxf(hi, moved<kDppMirror>(hi));
   }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float to_f32(uint32_t bits) {
-  if (BF16) return __uint_as_float(bits << 16);
-  return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t from_f32(float v) {
-  if (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
 // NaN becomes 0 and infinities the largest fp16: a cache never holds a parameter that is
@@ -318,12 +300,12 @@ struct Group {
 // one; quotients too small for that round to 0 in fp16).
 __device__ __forceinline__ Group group_of(float lo, float hi) {
   Group g;
-  g.m16 = from_f32<false>(lo + 0.0f);  // -0 becomes 0
+  g.m16 = down<false>(lo + 0.0f);  // -0 becomes 0
   const float x = hi - lo, q = x * (1.0f / 15.0f);
-  g.s16 = from_f32<false>(fmaf(fmaf(-15.0f, q, x), 1.0f / 15.0f, q));
+  g.s16 = down<false>(fmaf(fmaf(-15.0f, q, x), 1.0f / 15.0f, q));
   if (g.s16 == 0 && hi > lo) g.s16 = 1;  // 2^-24
-  g.m = to_f32<false>(g.m16);
-  g.s = to_f32<false>(g.s16);
+  g.m = up<false>(g.m16);
+  g.s = up<false>(g.s16);
   g.r = g.s16 ? __builtin_amdgcn_rcpf(g.s) : 0.0f;
   return g;
 }
@@ -344,8 +326,8 @@ __device__ __forceinline__ Group measure(const uint32_t (&raw)[C / 2], float (&x
     const short2v key = w ^ ((w >> 15) & short2v{32767, 32767});
     hi = __builtin_elementwise_max(hi, key);
     lo = __builtin_elementwise_min(lo, key);
-    x[2 * j] = to_f32<BF16>(raw[j] & 0xFFFFu);
-    x[2 * j + 1] = to_f32<BF16>(raw[j] >> 16);
+    x[2 * j] = up<BF16>(raw[j] & 0xFFFFu);
+    x[2 * j + 1] = up<BF16>(raw[j] >> 16);
   }
   const int16_t top = hi.x > hi.y ? hi.x : hi.y, low = lo.x < lo.y ? lo.x : lo.y;
   short2v both = {top, (int16_t)~low};
@@ -368,7 +350,7 @@ __device__ __forceinline__ Group measure(const uint32_t (&raw)[C / 2], float (&x
   }
   const short2v ends = {both.x, (int16_t)~both.y};
   const uint32_t w = __builtin_bit_cast(uint32_t, ends ^ ((ends >> 15) & short2v{32767, 32767}));
-  return group_of(to_f32<BF16>(w >> 16), to_f32<BF16>(w & 0xFFFFu));
+  return group_of(up<BF16>(w >> 16), up<BF16>(w & 0xFFFFu));
 }
 
 // rne((x - m) / s) without a division: the quotient is below 32 (15, more where s is a
@@ -514,7 +496,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(TokenArgs a) {
   if (!blk) return;
   {
     const uint16_t *par = reinterpret_cast<const uint16_t *>(blk + a.page * D + tok * (4 * G));
-    const float s = to_f32<false>(par[i / (64 / C)]), m = to_f32<false>(par[G + i / (64 / C)]);
+    const float s = up<false>(par[i / (64 / C)]), m = up<false>(par[G + i / (64 / C)]);
     const uint8_t *src = blk + tok * (D / 2) + key_byte<D>(i);
     alignas(16) uint16_t out[C];
 #pragma unroll
@@ -523,7 +505,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(TokenArgs a) {
                                    : *reinterpret_cast<const uint32_t *>(src + w * (D / 8));
 #pragma unroll
       for (int j = 0; j < (C < 8 ? C : 8); ++j)
-        out[8 * w + j] = (uint16_t)from_f32<BF16>(m + s * (float)((word >> (4 * j)) & 15));
+        out[8 * w + j] = (uint16_t)down<BF16>(m + s * (float)((word >> (4 * j)) & 15));
     }
     copy16<C>(a.k + (int64_t)row * a.ldk + head * D + i * C, out);
   }
@@ -541,7 +523,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(TokenArgs a) {
     for (int j = 0; j < C; ++j) {
       const uint32_t c = (word[j / 8] >> (4 * (j % 8))) & 15;
       turn[quarter][16 * j + i] =
-          (uint16_t)from_f32<BF16>(to_f32<false>(par[G + j / 4]) + to_f32<false>(par[j / 4]) * (float)c);
+          (uint16_t)down<BF16>(up<false>(par[G + j / 4]) + up<false>(par[j / 4]) * (float)c);
     }
     in_quarter();
     copy16<C>(a.v + (int64_t)row * a.ldv + head * D + i * C, &turn[quarter][i * C]);

@@ -41,8 +41,12 @@
 #include <stdint.h>
 
 #include "mixllm_kv4.h"
+#include "mixllm_lanes.h"
 
 namespace {
+
+using mixllm::down;
+using mixllm::up;
 
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -50,7 +54,6 @@ typedef float float2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
@@ -74,18 +77,6 @@ struct Args {
   int32_t tiles, tile_rows;  // row tiles of a request and head, rows of a full tile
   int32_t splits;            // workgroups along the tokens of a tile
 };
-
-template <bool BF16>
-__device__ __forceinline__ float up(uint32_t bits) {
-  return BF16 ? __uint_as_float(bits << 16)
-              : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t down(float v) {
-  if (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-}
 
 // Maximum and sum over the four lanes n, n + 16, n + 32, n + 48 of a query row.
 __device__ __forceinline__ float quarters_max(float v) {

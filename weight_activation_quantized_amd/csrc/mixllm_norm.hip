@@ -20,9 +20,13 @@
 
 #include "mixllm.h"
 #include "mixllm_kv4.h"
+#include "mixllm_lanes.h"
 #include "mixllm_quant_pair.h"
 
 namespace {
+
+using mixllm::down;
+using mixllm::up;
 
 struct NormArgs {
   const uint16_t *x, *post, *gate, *pre;
@@ -38,17 +42,6 @@ struct NormArgs {
   float eps, alpha, beta;
   int32_t wide;  // rows can be read and written 8 elements at a time
 };
-
-template <bool BF16>
-__device__ __forceinline__ float up(uint32_t bits) {
-  return BF16 ? __uint_as_float(bits << 16) : mixllm::h2f(bits & 0xFFFFu);
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t down(float v) {
-  if (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-}
 
 // A thread's elements of a row: with wide accesses chunks of 8 neighbours, chunk c of
 // thread t at (c * THREADS + t) * 8; else single elements, element c * 8 + j of thread t at
