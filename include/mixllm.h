@@ -264,8 +264,9 @@ int mixllm_gemm_w4w8a8_partials(const int8_t *aq_dev, const float *sa_dev, const
  *   h' = alpha * h + beta * gate * u   (gate 1 when NULL; h' = alpha * h when x is NULL)
  *   y  = h' / rms(h') * pre,    rms(v) = sqrt(mean(v^2) + eps)
  *
- * All in fp32.  h' is rounded once to the residual's type, y (from the unrounded h') once
- * to the type of x; the int8 outputs are mixllm_quant_act's for that y.
+ * All in fp32, which the sum of a row's squares has to fit.  h' is rounded once to the
+ * residual's type, y (from the unrounded h') once to the type of x; the int8 outputs are
+ * mixllm_quant_act's for that y.
  *
  * x_dev:       [M][ldx] output of the block, or NULL (no block before: the first norm).
  * post_dev, pre_dev: [N] norm weights; post NULL for no post norm; pre NULL for no second
@@ -338,7 +339,9 @@ size_t mixllm_kv4_page_bytes(int32_t page, int32_t heads, int32_t dim);
  * (those past F are dropped; the rows keep their entries); new pages are then taken from
  * the top in the order of the requests.  A request is refused if it would grow past
  * width * page tokens, or if it needs pages and those needed up to and including it exceed
- * the free ones.  Lengths outside [0, width * page] are taken as the nearest bound.
+ * the free ones.  Lengths outside [0, width * page] are taken as the nearest bound.  The rows of
+ * a refused request stay rows: attention gives them results over the tokens that it holds, which
+ * mean nothing.
  * One launch up to 4096 rows of `tokens`, two above.  Errors: E_NULL, E_SHAPE, E_HIP.
  */
 int mixllm_kv_plan(const int32_t *fresh_dev, const int32_t *lens_dev, int32_t B, int32_t *table_dev, int64_t ldt,
@@ -370,7 +373,8 @@ int mixllm_kv4_append(const void *k_dev, int64_t ldk, const void *v_dev, int64_t
                       int32_t page, int32_t heads, int32_t dim, void *stream);
 
 /*
- * The way back: the values m + s c of the tokens at T slots, rounded to dtype (device).
+ * The way back: the values m + s c of the tokens at T slots, rounded to dtype (device; at the ends
+ * of fp16 m + s c can pass its range and be infinite there).
  * Rows without a slot are left as they were.  Arguments and errors as mixllm_kv4_append.
  */
 int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, int32_t page, int32_t heads,
@@ -384,18 +388,23 @@ int mixllm_kv4_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  * query head x on key/value head x / (q_heads / kv_heads):
  *   S_t = scale * q . k_t;  out = sum_t softmax(S)_t v_t;  lse = log sum_t exp S_t.
  * A row that sees nothing has out 0 and lse -inf.  Softmax statistics and sums are fp32, the
- * products fp16 x 4-bit codes, where a weight times a value's scale is held to 2^-22, or to 2^-11 for
- * bf16 with more than 8 rows of a request and key/value head; out is rounded once to dtype.
- * bf16 values of q 2^-38 below the row's largest count as 0.  Scores have fp32's range: a row is
- * defined with |scale|, |q| and |scale q| below 2^120 and dim |scale q| |k| below 2^118 for
- * its largest |q| and |k|.  One that is not (or holds no number) spoils no other row.
+ * products fp16 x 4-bit codes; out is rounded once to dtype.
+ *   A weight times a value's scale is held to 2^-22 of itself, or 2^-11 for bf16 where
+ *   max_rows * q_heads / kv_heads > 8, and to 2^-33 of the largest scale that the rows around
+ *   it read.  bf16 values of q 2^-38 below the row's largest count as 0.
+ *   Scores have fp32's range: a row is defined with |scale|, |q| and |scale q| below 2^120 and
+ *   dim |scale q| |k| below 2^118 for its largest |q| and |k|.  One that is not (or holds no
+ *   number) spoils no other row.
  *
  * q_dev, out_dev: [T][ldq], [T][ldo] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head x of a row
  *               at x * dim; strides >= q_heads * dim and % 8 == 0.
  * table_dev, lens_dev, cu_dev: as mixllm_kv_plan leaves them (its lens_out), of the same B.
  *               Rows from T on are left out, and count in n_b.
- * max_rows, max_len: bounds the caller promises for n_b and lens[b]; rows and tokens beyond
- *               them are ignored.  They size the launch: keep them near the truth.
+ * max_rows, max_len: bounds the caller promises for n_b and lens[b].  Rows past max_rows are left
+ *               out; a length past max_len or width * page counts as that bound, a negative one
+ *               as 0.  They size the launch and cut the work, one way for all requests: keep
+ *               them near the truth, and give prompts and decoding requests, or lengths that
+ *               are far apart, to calls of their own.
  * Rows outside cu[0] .. cu[B]-1 of out and lse are left as they were.
  * lse_dev:      fp32 [T][q_heads] or NULL.
  * workspace_dev: mixllm_kv4_attention_workspace_bytes(..) for the same arguments (0: NULL is

@@ -818,8 +818,11 @@ class RequestPages:
 class AttentionBlock:
     """The attention half of a decoder layer on packed layers and a cache in 4 bits: the residual
     sum and norm quantized for the q/k/v projections, one GEMM over q, k and v, the write into
-    the cache, attention, and the output projection.  Seven launches on one stream (eight where
-    attention splits the tokens).  Argument marshalling only."""
+    the cache, attention, and the quantization and GEMM of the output projection.  Six launches on
+    one stream (seven where attention splits the tokens).  ``norm`` is the weight of the norm
+    before the projections; ``post_norm``, for layers that norm what a block gives, is the one of
+    the block *before* this one (its output x is normed as it is added).  Argument marshalling
+    only."""
 
     def __init__(self, w_q, w_k, w_v, w_o, idx8_q, idx8_k, idx8_v, idx8_o, norm, q_heads: int, kv_heads: int,
                  pages: int, page: int, post_norm=None, eps: float = 1e-5, window: int = 0, device="cuda"):
@@ -841,8 +844,9 @@ class AttentionBlock:
                     ws=torch.empty(size, dtype=torch.uint8, device=self.device) if size else None)
 
     def forward(self, x, h, bufs, req, rotate=None, stream=None):
-        """h: [M, hidden] the residual stream, updated in place by the block output x of the
-        layer before (None for the first); req: RequestPages after its plan(); rotate: called
+        """h: [M, hidden] the residual stream (fp16 or fp32), updated in place by the block output
+        x of the layer before (None for the first); M the rows that the plan counts or more (rows
+        missing here leave tokens that were counted unwritten); req: RequestPages after its plan(); rotate: called
         with the views q [M, heads, dim], k and the positions before the keys are written, for
         an embedding of positions (in place, on the stream that is current then, which is
         ``stream``).  Returns the output projection's [M, hidden]."""
@@ -868,8 +872,11 @@ class AttentionBlock:
 
 class DecoderLayer:
     """A decoder layer: AttentionBlock, the norm between, MLPBlock.  The layer's output is left
-    to the next layer's first norm (or a last mixllm_residual_norm) to add.  Argument
-    marshalling only."""
+    to the next layer's first norm (or a last mixllm_residual_norm) to add.  ``norm`` is the
+    weight before the MLP block, ``post_norm`` that of the attention block's output; the MLP
+    block's output is normed by the next layer's ``AttentionBlock.post_norm``.  The blocks are
+    added as they are: gates and factors are mixllm_residual_norm's own.  Argument marshalling
+    only."""
 
     def __init__(self, attention: AttentionBlock, mlp: MLPBlock, norm, post_norm=None):
         self.attention, self.mlp, self.norm, self.post_norm = attention, mlp, norm, post_norm
