@@ -204,3 +204,16 @@ def test_bf16_outputs_of_single_rows_are_nearly_rounded(L, hq, hkv, dim):
     want = np.stack([S.attention(q[b:b + 1], kv[b][0], kv[b][2], 100, dim ** -0.5, 0, ())[0][0] for b in range(len(lens))])
     differ = np.mean(out.float().cpu().numpy() != S.bf16_round(want.astype(np.float32)))
     assert differ <= 0.05, differ
+
+
+def test_rows_that_belong_to_no_request_are_left(L):
+    """Row bounds that start behind the first row and end before the last, long and short."""
+    U.say("attention rows of no request")
+    dtype = torch.bfloat16
+    dev, table, kv = K.build([40, 2100], 2, 128, 16, dtype, 65)
+    q = K.rounded(np.random.default_rng(4).normal(size=(9, 8, 128)).astype(np.float32), dtype)
+    for max_len in (2100, 40000):
+        out, lse = call(L, K.cuda(q, dtype), dev, table, [40, 2100], [3, 5, 6], 16, 2, max_len, 0.1)
+        K.compare(out[3:6], lse[3:6], q[3:6], kv, [40, 2100], [2, 1], dtype, 0.1)
+        for rest in (slice(0, 3), slice(6, 9)):
+            assert torch.all(out[rest] == 9.0) and torch.all(lse[rest] == 9.0)

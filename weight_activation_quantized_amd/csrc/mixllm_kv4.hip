@@ -26,8 +26,8 @@ using mixllm::up;
 // added) and then a scatter of independent items.  The traffic is a few bytes per request
 // and 8 bytes per token, so the time is latency: the sums run in one workgroup, all of them
 // at once and across lanes without LDS, and its threads also move the pages.  256 requests of
-// one token: 5.1 us (the sums one after the other through LDS shuffles: 14.0 us; a launch
-// alone takes about 4).
+// one token: 5.1 us (0.1 of it the row limit's; the sums one after the other through LDS
+// shuffles: 14.0 us; a launch alone takes about 4).
 // ---------------------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
@@ -262,8 +262,10 @@ constexpr int32_t kPlanOneLaunch = 4096;
 // group of 64 go over 64 / (D/16) lanes.  Keys are stored from there; the values' codes change
 // places through LDS so that lane n has channels 16 j + n: its word is then complete, and the
 // four quarters' words of consecutive tokens are neighbours in the cache.  Long prompts are
-// bound by the vector units: 8191 tokens of 8 heads of 128 take 18.5 us with divisions and
-// fp32 extremes, 15.3 as written (12 of it without any store); reading them back takes 8.8.
+// bound inside the unit: 8191 tokens of 8 heads of 128 take 18.5 us with divisions and fp32
+// extremes, 15.3 as written, 12 of it without any store.  About half of that is vector operations
+// (13 to 16 per value); the rest was not measured apart: the turn through LDS, a byte at a time,
+// and two chains of lane moves, one after the other.  Reading them back takes 8.8.
 // ---------------------------------------------------------------------------------------
 
 // Minimum and maximum over LANES (4, 8 or 16) neighbouring lanes of a quarter.

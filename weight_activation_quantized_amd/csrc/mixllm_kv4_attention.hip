@@ -35,8 +35,9 @@
 // What bounds it, at 128 channels: the cache's bytes for decodes (128 requests of up to 8192 tokens,
 // 946 MB: 189 us, 5.01 TB/s; the copies alone, nothing computed, 170 us); latency, the join and
 // the last workgroups where there is less (32 requests, 127 MB: 36 us, 21.7 at the copy's
-// rate); for prompts (2 x 1024 rows: 273 us, 400 TFLOP/s) the registers, which leave 2 waves
-// per SIMD to hide the making of operands and the softmax between the matrix instructions.
+// rate); for prompts (2 x 1024 rows: 273 us, 400 TFLOP/s) the registers and the 66 KB of LDS that
+// the join of the waves takes, which leave 2 waves per SIMD to hide the making of operands and
+// the softmax between the matrix instructions.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -365,8 +366,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(Args a) {
   // A weight times a value's scale is rounded to fp16 for the product, which would show beside
   // the output's own rounding (fp16: 1.5 times its error, bf16: 1.04), so what it leaves goes
   // through the product as a second operand.  Decodes wait for memory: it costs them 0 to 3% (bf16:
-  // 131071 tokens 35.1 -> 36.1 us, 128 requests 184.2 -> 184.4).  Prompts wait for the products (2 x
-  // 1024 rows, bf16: 222.7 -> 273.6), so there bf16, whose own rounding is 8 times larger, goes without.
+  // 131071 tokens 35.1 -> 36.1 us, 128 requests 184.2 -> 184.4).  Tiles of more rows wait for the
+  // products (bf16: prompts of 2 x 1024 rows 222.7 -> 273.6, 32 requests of 5 drafted rows over 4001
+  // tokens 43.3 -> 49.6), so there bf16, whose own rounding is 8 times larger, goes without.
   constexpr int kParts = BF16 && V == 1 ? 1 : 2;
   float m[CT], ref[CT], limit[CT], l[CT], bias[CT][G], k = 0.0f;
 #pragma unroll
