@@ -845,11 +845,11 @@ class AttentionBlock:
 
     def forward(self, x, h, bufs, req, rotate=None, stream=None):
         """h: [M, hidden] the residual stream (fp16 or fp32), updated in place by the block output
-        x of the layer before (None for the first); M the rows that the plan counts or more (rows
-        missing here leave tokens that were counted unwritten); req: RequestPages after its plan(); rotate: called
-        with the views q [M, heads, dim], k and the positions before the keys are written, for
-        an embedding of positions (in place, on the stream that is current then, which is
-        ``stream``).  Returns the output projection's [M, hidden]."""
+        x of the layer before (None for the first); M the rows that the plan counts or more (a
+        token whose row is missing here is counted and never written); req: RequestPages after
+        its plan(); rotate: called with the views q [M, heads, dim], k and the positions before
+        the keys are written, for an embedding of positions (in place, on the stream that is
+        current then, which is ``stream``).  Returns the output projection's [M, hidden]."""
         if req.page != self.page or req.pages > self.cache.shape[0]:
             raise ValueError(f"the requests have {req.pages} pages of {req.page} tokens, the cache has "
                              f"{self.cache.shape[0]} pages of {self.page}")
