@@ -425,6 +425,123 @@ int mixllm_kv4_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t 
                          int32_t window, void *out_dev, int64_t ldo, float *lse_dev, void *workspace_dev,
                          size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * The norms of queries and keys per head and the rotation by position, in one pass
+ * (device), between the projections and the write into a cache.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * w   per head of `dim` channels (y = x without a norm)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t),  t = pos * inv_freq[i], i < rot / 2
+ *
+ * in fp32, which the sum of a head's squares has to fit, and rounded once.  The pair i of a
+ * head is its channels i and i + rot / 2 (neighbours 0) or 2 i and 2 i + 1 (neighbours 1);
+ * channels from rot on are not turned.  The angle's product and its reduction are fp64.
+ *
+ * q_dev, k_dev: [T][ldq], [T][ldk] of dtype (MIXLLM_FP16 or MIXLLM_BF16), head h of a row at
+ *               h * dim, so slices of one GEMM output do; q_out_dev, k_out_dev the results,
+ *               which may be q_dev and k_dev with their strides.  NULL is taken for the ones
+ *               of no heads.
+ * pos_dev:      int32 [T], inv_freq_dev: fp32 [rot / 2] (both may be NULL for rot 0).
+ * q_norm_dev, k_norm_dev: [dim] of dtype, or NULL for no norm.
+ * dim, rot even, dim <= 512, 0 <= rot <= dim; T below 2^24 and T * heads below 2^26.
+ * Any stride and element-aligned pointer; dim % 8 == 0, rot % 8 == 0, strides % 4 == 0 and
+ * 8-byte aligned pointers run faster.
+ * Errors: E_NULL, E_SHAPE, E_HIP.
+ * ------------------------------------------------------------------------------------ */
+int mixllm_head_norm_rotate(const void *q_dev, int64_t ldq, const void *k_dev, int64_t ldk, void *q_out_dev,
+                            int64_t ldqo, void *k_out_dev, int64_t ldko, const int32_t *pos_dev,
+                            const float *inv_freq_dev, const void *q_norm_dev, const void *k_norm_dev, int32_t T,
+                            int32_t q_heads, int32_t kv_heads, int32_t dim, int32_t rot, int32_t neighbours,
+                            int32_t dtype, float eps, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * The cache in 8 bits: keys and values of one attention layer, in pages.
+ *
+ * Pages, heads, slots and page tables as for the cache in 4 bits.  A run, 16 tokens that
+ * follow one another in a page, has one fp32 scale for all channels of its keys of a head
+ * and one for its values; x is kept as s c, -127 <= c <= 127, a byte c + 128.  A call that
+ * writes to a run sets, in fp32 steps with IEEE division,
+ *   s  = max(s_held, max |x| / 127) over the call's tokens of the run,
+ *   c  = clamp(rne(x / s), -127, 127) for them (0 where s = 0),
+ *   c' = clamp(rne(c (s_held / s)), -127, 127) for the tokens it holds,
+ * where s_held = 0 if the call writes the run's first token (the run begins anew: places that
+ * the call does not write become 0) or if what is held is no positive finite number.
+ * NaN counts as 0 and values beyond +-65504 as that, so what a cache holds is finite.
+ *
+ * A block of page p and head h starts at byte (p * heads + h) * (2 * page * dim + page / 2
+ * rounded up to a multiple of 128):
+ *   K codes (page * dim bytes): run r from byte r * 16 dim; in it channel ch of token t at
+ *     ch / 64 * 1024 + ch / 16 % 4 * 256 + t * 16 + ch % 16;
+ *   V codes (page * dim): the same runs; in one channel ch of token t at
+ *     ch / 64 * 1024 + t / 4 * 256 + ch % 16 * 16 + ch / 16 % 4 * 4 + t % 4;
+ *   scales: of run r the fp32 pair (keys', values') at 8 r.
+ * ------------------------------------------------------------------------------------ */
+
+/* Bytes of one page over all heads, or 0 if the parameters are invalid. */
+size_t mixllm_kv8_page_bytes(int32_t page, int32_t heads, int32_t dim);
+
+/*
+ * Quantizes the keys and values of T rows and writes them to their slots (device).  Arguments
+ * as mixllm_kv4_append, with T (in whole 16s) * heads below 2^27.
+ * Rows of one run have to follow one another, in the order of their slots, as a plan leaves
+ * them: rows of it that do not, and a slot given twice, leave the tokens of that run
+ * unspecified (no others).  Rows without a slot are skipped; runs that get no token are left as
+ * they were.
+ */
+int mixllm_kv8_append(const void *k_dev, int64_t ldk, const void *v_dev, int64_t ldv, int32_t dtype,
+                      const int32_t *slots_dev, int32_t T, void *cache_dev, size_t cache_bytes, int32_t pages,
+                      int32_t page, int32_t heads, int32_t dim, void *stream);
+
+/*
+ * The way back: the values s c of the tokens at T slots, rounded to dtype (device).  Rows without
+ * a slot are left as they were.  Arguments and errors as mixllm_kv8_append.
+ */
+int mixllm_kv8_read(const void *cache_dev, size_t cache_bytes, int32_t pages, int32_t page, int32_t heads,
+                    int32_t dim, const int32_t *slots_dev, int32_t T, void *k_dev, int64_t ldk, void *v_dev,
+                    int64_t ldv, int32_t dtype, void *stream);
+
+/*
+ * Attention over the cache in 8 bits (device): arguments, results, limits and errors as
+ * mixllm_kv4_attention, its workspace mixllm_kv8_attention_workspace_bytes(..).
+ *   A weight times a value's scale is held to 2^-22 of itself and to 2^-33 of the row's largest
+ *   one.  Scales of values that a row sees lie within a factor of 2^100 of one another.
+ *   bf16 values of q 2^-38 below the row's largest count as 0.
+ *   Scores have fp32's range, with the bounds of mixllm_kv4_attention; a row that passes them
+ *   (or holds no number) spoils no other row.
+ */
+size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                            int32_t max_rows, int32_t max_len, int32_t window);
+
+int mixllm_kv8_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t T, int32_t q_heads,
+                         const void *cache_dev, size_t cache_bytes, int32_t pages, int32_t page, int32_t kv_heads,
+                         int32_t dim, const int32_t *table_dev, int64_t ldt, int32_t width, const int32_t *lens_dev,
+                         const int32_t *cu_dev, int32_t B, int32_t max_rows, int32_t max_len, float scale,
+                         int32_t window, void *out_dev, int64_t ldo, float *lse_dev, void *workspace_dev,
+                         size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * The linear layer in 8 bits with one scale per token and one per output channel (device):
+ * for layers kept wholly in 8 bits whose inputs do not need a scale per group.
+ *
+ * mixllm_quant_rows: per row m of a (a token's activations, or an output channel's weights)
+ *   s[m] = max |a[m]| / 127,  q[m][k] = clamp(rne(a[m][k] / s[m]), -127, 127)
+ * in fp32 with IEEE divisions; s = 0 and q = 0 for a row of zeros.
+ * a_dev: [M][lda] of dtype (MIXLLM_FP16 or MIXLLM_BF16), lda % 8 == 0; q_dev: int8 [M][ldq],
+ * ldq % 16 == 0; s_dev: fp32 [M].  K % 16 == 0, K <= 131072, M below 2^22.
+ *
+ * mixllm_gemm_w8a8: y[m][n] = (sum_k aq[m][k] w[n][k]) * (sa[m] * sw[n]), the sum exact in
+ *   int32 for codes of -127 .. 127 (mixllm_quant_rows gives no others), rounded once to dtype.
+ * aq_dev: int8 [M][lda]; w_dev: int8 [N][ldw]; strides % 16 == 0; sa_dev: fp32 [M], sw_dev: fp32
+ * [N]; y_dev: [M][ldy] of dtype, ldy >= N, element-aligned.  K % 16 == 0, K <= 131072; M / 32 * N
+ * / 32 below 2^26.
+ * Errors: E_NULL, E_SHAPE, E_HIP.
+ * ------------------------------------------------------------------------------------ */
+int mixllm_quant_rows(const void *a_dev, int64_t lda, int32_t dtype, int32_t M, int32_t K, int8_t *q_dev, int64_t ldq,
+                      float *s_dev, void *stream);
+
+int mixllm_gemm_w8a8(const int8_t *aq_dev, int64_t lda, const float *sa_dev, const int8_t *w_dev, int64_t ldw,
+                     const float *sw_dev, int32_t M, int32_t N, int32_t K, void *y_dev, int64_t ldy, int32_t dtype,
+                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,422 @@
+// Attention over the paged key/value cache held in 8 bits (layout: mixllm_kv8.h), for decoded
+// tokens and for the rows of prompts.
+//
+// For one query row with position p of a request, over the keys t in (p - window, p], with one
+// scale for the keys (k) and one for the values (v) of each run r of 16 tokens:
+//   S_t = scale * k_r (q . c_t);   O = sum_t P_t v_r c'_t / sum_t P_t,  P_t = exp(S_t - max S)
+// so codes enter the 16 x 16 x 32 fp16 matrix instruction as they are (whole numbers of 8 bits
+// are exact in fp16) and a run's scale multiplies 16 x 16 scores or weights at once.
+//
+// Both products are computed transposed: S^T = K Q^T leaves in lane (n, c) the scores of query
+// row n with tokens 4c .. 4c+3 of a run, and O^T = V^T P^T takes from lane (n, c) the weights of
+// row n for the tokens that quarter c holds, which are the same.  The cache's order makes both
+// operands of codes 16-byte loads of the lane that needs them, straight from memory.
+//
+// A byte b of a code c = b - 128 becomes fp16 by placing it under the exponent of 1024, 1024 + b,
+// and taking 1152 away, exactly: two operations for two codes.
+//
+// Weights 2^(S - ref) times a run's scale v are rounded to fp16 for the product, after a power of
+// two per row that follows the largest such product (`shift`), so that rows whose large
+// values hardly count lose nothing; what the rounding leaves is a second operand.  Statistics,
+// sums and outputs are fp32.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mixllm_attend.h"
+#include "mixllm_kv8.h"
+#include "mixllm_lanes.h"
+
+namespace {
+
+// 8 codes as fp16, exactly.
+__device__ __forceinline__ half8 codes8(uint32_t lo, uint32_t hi) {
+  constexpr uint32_t k1024 = 0x64646464u;
+  const uint4v b = {__builtin_amdgcn_perm(k1024, lo, 0x04010400u), __builtin_amdgcn_perm(k1024, lo, 0x04030402u),
+                    __builtin_amdgcn_perm(k1024, hi, 0x04010400u), __builtin_amdgcn_perm(k1024, hi, 0x04030402u)};
+  return __builtin_bit_cast(half8, b) - (_Float16)(1024 + mixllm::kKv8Zero);
+}
+
+constexpr int kTokens = 2 * kRun;  // of a step: two runs fill an operand of the second product
+constexpr float kTop = 14.0f;      // weights times scales stay below 2^kTop, fp16 ends at 2^16
+constexpr float kRoom = 5.0f;      // and are moved there or kRoom below
+
+// One step's codes, as loaded.
+template <int D>
+struct Stage {
+  uint4v k[2][D / 64], v[2][D / 64];
+};
+
+// CT: column blocks of 16 rows that share the operands made of codes.
+template <int D, int CT, bool BF16>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kernel(Args a) {
+  constexpr int U = D / 64, E = D / 32, J = D / 16;
+  constexpr int kStride = D + 4;  // floats of a row of partial outputs in LDS
+  constexpr int kAll = CT * kCols;
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves * kAll * kStride];
+  __shared__ float s_m[kWaves][kAll], s_l[kWaves][kAll];
+
+  const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, b = blockIdx.z;
+  const int32_t rt = a.tiles - 1 - (int32_t)blockIdx.y;  // a request's last rows see most tokens: their tiles first
+  const Tile t = tile_of(a, b, h, rt);
+  if (t.rows <= 0) return;
+  const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
+  if (split >= nchunks && !(split == 0 && a.splits == 1)) return;
+  const int32_t begin = base_of(t) + split * chunk;
+  const int32_t from = begin > t.lo ? begin : t.lo;
+  const int32_t to = t.hi - begin > chunk ? begin + chunk : t.hi;
+
+  const int32_t P = 1 << a.page_log2, block = mixllm::kv8_block_bytes(P, D);
+  const int32_t *table = a.table + b * a.ldt;
+
+  // This wave takes every fourth step, in batches whose pages and scales one load each fetches:
+  // lane 2 j + x has those of run x of the batch's step j; page -1 for none.
+  constexpr int32_t kStride4 = kWaves * kTokens, kBatch = 32;
+  int32_t tb = (from & ~(kRun - 1)) + wave * kTokens, steps = 0, pages = -1;
+  float k_scale = 0.0f, v_scale = 0.0f;
+  uint64_t there = 0;
+  auto load = [&](Stage<D> &st, int32_t j) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int32_t pg = __builtin_amdgcn_readlane(pages, 2 * j + x);
+      const int32_t in = (tb + j * kStride4 + kRun * x) & (P - 1);
+      // an absent run reads any memory of the cache; its scores are masked
+      const uint8_t *src = a.cache + ((int64_t)(pg < 0 ? 0 : pg) * a.hkv + h) * block + (int64_t)in * D;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        st.k[x][u] = *reinterpret_cast<const uint4v *>(src + u * 1024 + lane * 16);
+        st.v[x][u] = *reinterpret_cast<const uint4v *>(src + P * D + u * 1024 + lane * 16);
+      }
+    }
+  };
+  auto fetch = [&]() {  // for the batch at tb < to
+    const int32_t tok = tb + lane / 2 * kStride4 + lane % 2 * kRun;
+    pages = tok < to ? table[tok >> a.page_log2] : -1;
+    pages = (uint32_t)pages < (uint32_t)a.pages ? pages : -1;
+    there = __ballot(pages >= 0);
+    const int32_t left = (to - tb + kStride4 - 1) / kStride4;
+    steps = left < kBatch ? left : kBatch;
+    k_scale = v_scale = 0.0f;
+    if (pages >= 0) {
+      const float2v s = *reinterpret_cast<const float2v *>(a.cache + ((int64_t)pages * a.hkv + h) * block +
+                                                           mixllm::kv8_scale_offset(P, D) + (tok & (P - 1)) / kRun * 8);
+      k_scale = s.x, v_scale = s.y;
+    }
+  };
+  Stage<D> st0, st1;
+  if (tb < to) {
+    fetch();
+    load(st0, 0);
+  }
+
+  // The query rows of this lane, as operands: step e has the channels 64 (e/2) + 16 c + 8 (e%2) on.
+  half8 q[CT][E];
+  float row_scale[CT];
+  int32_t row_hi[CT], row_lo[CT];  // the row sees tokens [row_lo, row_hi)
+#pragma unroll
+  for (int z = 0; z < CT; ++z) {
+    const int32_t row = kCols * z + n, r = t.row0 + (row < t.rows ? row : t.rows - 1);
+    const int32_t i = r / a.group, head = h * a.group + r % a.group;
+    const uint16_t *qp = a.q + (int64_t)(t.q0 + i) * a.ldq + (int64_t)head * D + 16 * c;
+    uint4v raw[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) raw[e] = *reinterpret_cast<const uint4v *>(qp + e / 2 * 64 + e % 2 * 8);
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        top = fmaxf(top, fmaxf(fabsf(up<BF16>(raw[e][w] & 0xFFFFu)), fabsf(up<BF16>(raw[e][w] >> 16))));
+    top = quarters_max(top);
+    // a power of two brings the row below 2^14: bf16 fits fp16 but for values 2^-38 below the largest
+    int p = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;  // top in [2^(p-1), 2^p)
+    p = p < -100 ? -100 : p;
+    const float mul = ldexpf(1.0f, 14 - p);
+    row_scale[z] = ldexpf(a.scale * kLog2e, p - 14);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        q[z][e][2 * w] = (_Float16)(up<BF16>(raw[e][w] & 0xFFFFu) * mul);
+        q[z][e][2 * w + 1] = (_Float16)(up<BF16>(raw[e][w] >> 16) * mul);
+      }
+    const int32_t pos = t.pos0 + i;
+    row_hi[z] = pos + 1;
+    row_lo[z] = a.window ? pos - a.window + 1 : 0;
+  }
+  // [all_lo, all_hi): tokens that every row of the tile sees
+  const int32_t all_hi = t.pos0 + t.row0 / a.group + 1;
+  const int32_t all_lo = a.window ? t.pos0 + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
+
+  // l = sum 2^(s - ref) and o = sum 2^(s - ref) v c 2^-shift of the tokens so far.  `ref` is the
+  // largest score seen, up to kLazy, `peak` the largest s - ref + log2 v, up to kRoom.
+  float4v o[CT][J];
+  float ref[CT], l[CT], limit[CT], peak[CT];
+  int32_t shift[CT];
+#pragma unroll
+  for (int z = 0; z < CT; ++z) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) o[z][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    ref[z] = limit[z] = kLow;
+    l[z] = 0.0f;
+    shift[z] = -200;
+    peak[z] = -1000.0f;
+  }
+
+  auto compute = [&](const Stage<D> &st, int32_t j) __attribute__((always_inline)) {
+    const int32_t t0 = tb + j * kStride4;
+    const uint32_t here = (uint32_t)(there >> (2 * j)) & 3u;
+    float ks[2], vs[2];
+    int32_t ve[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      ks[x] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k_scale), 2 * j + x));
+      vs[x] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v_scale), 2 * j + x));
+      ve[x] = vs[x] > 0.0f ? __builtin_amdgcn_frexp_expf(vs[x]) : -1000;  // v < 2^ve
+    }
+    float s[CT][2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float4v acc[CT];
+#pragma unroll
+      for (int z = 0; z < CT; ++z) acc[z] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const half8 w = codes8(st.k[x][e / 2][e % 2 * 2], st.k[x][e / 2][e % 2 * 2 + 1]);
+#pragma unroll
+        for (int z = 0; z < CT; ++z) acc[z] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, q[z][e], acc[z], 0, 0, 0);
+      }
+#pragma unroll
+      for (int z = 0; z < CT; ++z) {
+        const float f = row_scale[z] * ks[x];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[z][x][u] = acc[z][u] * f;
+      }
+    }
+    if (!(t0 >= all_lo && t0 >= from && t0 + kTokens <= all_hi && t0 + kTokens <= to && here == 3u)) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int32_t tok = t0 + kRun * x + 4 * c + u;
+          const bool seen = tok < to && tok >= from && (here >> x & 1);
+#pragma unroll
+          for (int z = 0; z < CT; ++z)
+            s[z][x][u] = seen && tok < row_hi[z] && tok >= row_lo[z] ? s[z][x][u] : -INFINITY;
+        }
+    }
+    float top[CT], m[CT][2];
+    bool over = false;
+#pragma unroll
+    for (int z = 0; z < CT; ++z) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) m[z][x] = fmaxf(fmaxf(s[z][x][0], s[z][x][1]), fmaxf(s[z][x][2], s[z][x][3]));
+      top[z] = fmaxf(m[z][0], m[z][1]);
+      over = over || top[z] > limit[z] ||
+             fmaxf(m[z][0] - ref[z] + (float)ve[0], m[z][1] - ref[z] + (float)ve[1]) > (float)shift[z] + kTop;
+    }
+    if (__any(over)) {
+#pragma unroll
+      for (int z = 0; z < CT; ++z) {
+        const float high = quarters_max(top[z]), next = high > limit[z] ? high : ref[z];
+        const float back = ref[z] - next;  // kLow stands for no score so far
+        peak[z] = fmaxf(peak[z] + back, quarters_max(fmaxf(m[z][0] - next + (float)ve[0], m[z][1] - next + (float)ve[1])));
+        const int32_t to_shift = (int32_t)fminf(fmaxf(ceilf(peak[z]), -180.0f), 180.0f) - (int32_t)(kTop - kRoom);
+        const float fl = __builtin_amdgcn_exp2f(back), fo = __builtin_amdgcn_exp2f(back + (float)(shift[z] - to_shift));
+        ref[z] = next;
+        limit[z] = next + kLazy;
+        shift[z] = to_shift;
+        l[z] *= fl;
+#pragma unroll
+        for (int jj = 0; jj < J; ++jj) o[z][jj] *= fo;
+      }
+    }
+    uint4v ph[CT], pl[CT];
+#pragma unroll
+    for (int z = 0; z < CT; ++z)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float g = fminf(ldexpf(vs[x], -shift[z]), 0x1p120f);  // where it ends, weights are 0
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          half2v hi, lo;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = __builtin_amdgcn_exp2f(s[z][x][u + e] - ref[z]);
+            l[z] += w;
+            const float p = w * g;
+            hi[e] = (_Float16)p;
+            lo[e] = (_Float16)(p - (float)hi[e]);
+          }
+          ph[z][2 * x + u / 2] = __builtin_bit_cast(uint32_t, hi);
+          pl[z][2 * x + u / 2] = __builtin_bit_cast(uint32_t, lo);
+        }
+      }
+#pragma unroll
+    for (int jj = 0; jj < J; ++jj) {
+      const half8 w = codes8(st.v[0][jj / 4][jj % 4], st.v[1][jj / 4][jj % 4]);
+#pragma unroll
+      for (int z = 0; z < CT; ++z) {
+        o[z][jj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(half8, ph[z]), o[z][jj], 0, 0, 0);
+        o[z][jj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(half8, pl[z]), o[z][jj], 0, 0, 0);
+      }
+    }
+  };
+
+  while (tb < to) {
+    for (int32_t j = 0;;) {
+      if (j + 1 < steps) load(st1, j + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(st0, j);
+      if (++j == steps) break;
+      if (j + 1 < steps) load(st0, j + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(st1, j);
+      if (++j == steps) break;
+    }
+    tb += kBatch * kStride4;
+    if (tb < to) {
+      fetch();
+      load(st0, 0);
+    }
+  }
+
+  // The waves' statistics and outputs of each row, joined.
+#pragma unroll
+  for (int z = 0; z < CT; ++z) {
+    l[z] = quarters_sum(l[z]);
+    if (c == 0) {
+      s_m[wave][kCols * z + n] = ref[z];
+      s_l[wave][kCols * z + n] = l[z];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int z = 0; z < CT; ++z) {
+    float best = ref[z];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_m[w][kCols * z + n]);
+    const float f = __builtin_amdgcn_exp2f(ref[z] - best);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float4v v;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = ldexpf(o[z][j][u], shift[z]) * f;
+      *reinterpret_cast<float4v *>(s_o + (wave * kAll + kCols * z + n) * kStride + 16 * j + 4 * c) = v;
+    }
+  }
+  __syncthreads();
+  const int64_t place = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits + split;
+  for (int e = threadIdx.x; e < t.rows * (D / 8); e += kThreads) {
+    const int rr = e / (D / 8), ch = e % (D / 8) * 8;
+    float top = kLow * 2.0f, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w][rr]);
+    float4v v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      sum = fmaf(s_l[w][rr], __builtin_amdgcn_exp2f(s_m[w][rr] - top), sum);
+      const float *src = s_o + (w * kAll + rr) * kStride + ch;
+      v0 += *reinterpret_cast<const float4v *>(src);
+      v1 += *reinterpret_cast<const float4v *>(src + 4);
+    }
+    if (a.splits > 1) {
+      float *dst = a.ws_o + (place * a.tile_rows + rr) * D + ch;
+      *reinterpret_cast<float4v *>(dst) = v0;
+      *reinterpret_cast<float4v *>(dst + 4) = v1;
+      if (ch == 0) *reinterpret_cast<float2v *>(a.ws_ml + (place * a.tile_rows + rr) * 2) = float2v{top, sum};
+    } else {
+      const int32_t rg = t.row0 + rr, ii = t.q0 + rg / a.group, hh = h * a.group + rg % a.group;
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays NaN
+      uint4v w;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        w[u] = down<BF16>(v0[2 * u] * inv) | down<BF16>(v0[2 * u + 1] * inv) << 16;
+        w[2 + u] = down<BF16>(v1[2 * u] * inv) | down<BF16>(v1[2 * u + 1] * inv) << 16;
+      }
+      *reinterpret_cast<uint4v *>(a.out + (int64_t)ii * a.ldo + (int64_t)hh * D + ch) = w;
+      if (ch == 0 && a.lse) a.lse[(int64_t)ii * a.hq + hh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+  }
+}
+
+// How the work of a call is cut.  Rows: tiles of 16 or 32 (row, head) pairs of one key/value
+// head.  Tokens: so many equal chunks of each tile that about kTarget workgroups run at the
+// longest length; 256 CUs hold 2 of them each.
+constexpr int64_t kTarget = 512;
+
+Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
+  Cut k;
+  const int64_t rows = (int64_t)max_rows * (hq / hkv);
+  k.tile_rows = rows <= 16 || dim == 256 ? 16 : 32;
+  k.tiles = (int32_t)((rows + k.tile_rows - 1) / k.tile_rows);
+  int64_t span = max_len;
+  // a tile's rows are at most tile_rows positions, its first chunk starts at a whole run
+  if (window && (int64_t)window + k.tile_rows + kRun < span) span = (int64_t)window + k.tile_rows + kRun;
+  const int64_t groups = (int64_t)B * hkv * k.tiles;
+  const int64_t most = (span + kMinChunk - 1) / kMinChunk, want = (kTarget + groups - 1) / groups;
+  k.splits = (int32_t)(most < 1 || want <= 1 ? 1 : want < most ? want : most);
+  return k;
+}
+
+template <int D, bool BF16>
+void launch(const Args &a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
+  if (D < 256 && a.tile_rows == 32)
+    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, BF16>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((kv8_attention_kernel<D, 1, BF16>), grid, threads, 0, s, a);
+  if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
+  launch_join<D, BF16>(a, s);
+}
+
+template <int D>
+void launch(const Args &a, int32_t dtype, hipStream_t s) {
+  if (dtype == MIXLLM_BF16) launch<D, true>(a, s);
+  else launch<D, false>(a, s);
+}
+
+}  // namespace
+
+extern "C" size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads,
+                                                       int32_t dim, int32_t max_rows, int32_t max_len,
+                                                       int32_t window) {
+  if (!shape_ok(T, B, q_heads, kv_heads, dim, max_rows, max_len, window) || T == 0 || B == 0 || max_rows == 0) return 0;
+  const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
+  if (k.splits == 1) return 0;
+  return (size_t)B * k.tiles * kv_heads * k.splits * k.tile_rows * (dim + 2) * sizeof(float);
+}
+
+extern "C" int mixllm_kv8_attention(const void *q, int64_t ldq, int32_t dtype, int32_t T, int32_t q_heads,
+                                    const void *cache, size_t cache_bytes, int32_t pages, int32_t page,
+                                    int32_t kv_heads, int32_t dim, const int32_t *table, int64_t ldt, int32_t width,
+                                    const int32_t *lens, const int32_t *cu, int32_t B, int32_t max_rows,
+                                    int32_t max_len, float scale, int32_t window, void *out, int64_t ldo, float *lse,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+  if (!shape_ok(T, B, q_heads, kv_heads, dim, max_rows, max_len, window) ||
+      (dtype != MIXLLM_FP16 && dtype != MIXLLM_BF16))
+    return MIXLLM_E_SHAPE;
+  if (T == 0 || B == 0 || max_rows == 0) return MIXLLM_OK;
+  const int st = mixllm::kv8_check_cache(cache, cache_bytes, pages, page, kv_heads, dim);
+  if (st != MIXLLM_OK) return st;
+  const int bad = check_call(q, ldq, q_heads, dim, table, ldt, width, lens, cu, out, ldo, lse, workspace);
+  if (bad != MIXLLM_OK) return bad;
+  const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
+  const int64_t parts = (int64_t)B * k.tiles * kv_heads * k.splits;
+  if (parts > 0x7FFFFFFF || B > 65535 || k.tiles > 65535 || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
+    return MIXLLM_E_SHAPE;
+  float *ws = static_cast<float *>(workspace);
+  if (k.splits > 1) {
+    if (workspace_bytes < (size_t)parts * k.tile_rows * (dim + 2) * sizeof(float)) return MIXLLM_E_SPACE;
+    if (!ws) return MIXLLM_E_NULL;
+  }
+  const Args a = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(cache), table, lens, cu,
+                  static_cast<uint16_t *>(out), lse, ws, ws ? ws + parts * k.tile_rows * dim : nullptr,
+                  ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
+                  mixllm::log2_of(page), width, B, max_rows,
+                  max_len, window, k.tiles, k.tile_rows, k.splits};
+  if (dim == 64) launch<64>(a, dtype, (hipStream_t)stream);
+  else if (dim == 128) launch<128>(a, dtype, (hipStream_t)stream);
+  else launch<256>(a, dtype, (hipStream_t)stream);
+  return mixllm::launch_status();
+}

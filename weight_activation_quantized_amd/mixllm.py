@@ -91,7 +91,13 @@ _SIGS = {
     "mixllm_kv4_attention_workspace_bytes": ([_i32] * 8, _sz),
     "mixllm_kv4_attention": ([_vp, _i64, _i32, _i32, _i32, _vp, _sz, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _vp,
                               _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "mixllm_head_norm_rotate": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                 _i32, _i32, _i32, _f32, _vp], ctypes.c_int),
+    "mixllm_quant_rows": ([_vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp], ctypes.c_int),
+    "mixllm_gemm_w8a8": ([_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _vp], ctypes.c_int),
 }
+for _call in ("page_bytes", "append", "read", "attention_workspace_bytes", "attention"):  # the caches' calls are alike
+    _SIGS[f"mixllm_kv8_{_call}"] = _SIGS[f"mixllm_kv4_{_call}"]
 def _bind(lib):
     for name, (args, res) in _SIGS.items():
         fn = getattr(lib, name)
@@ -572,50 +578,41 @@ def _plan(fn, fresh, lens, table, pool, count, page, pages, lens_out, count_out,
         tokens)
 
 
-def mixllm_kv4_append(k, v, slots, cache, page: int, stream=None):
-    """Writes k and v ([T, heads, dim] fp16 or bf16, rows may be strided) into the cache at
-    slots (int32 [T], negative: skip the row)."""
+# The calls of both caches: `fn` is the library's, `shape_of` the check of its cache.
+
+def _append(fn, shape_of, k, v, slots, cache, page, stream):
     t, _, dim = shape = k.shape
-    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dev, pcache, size, pages, heads = shape_of(cache, page, dim)
     dtype, t16, width = _dtype16(k, "k"), k.dtype, heads * dim
     if shape[1] != heads:
         raise ValueError(f"k has {shape[1]} heads, the cache {heads}")
-    _on(dev, stream, _lib.mixllm_kv4_append, k.data_ptr(), _ld(k, "k", t16, dev, shape, width), v.data_ptr(),
+    _on(dev, stream, fn, k.data_ptr(), _ld(k, "k", t16, dev, shape, width), v.data_ptr(),
         _ld(v, "v", t16, dev, shape, width), dtype, _flat(slots, "slots", _i32t, dev, t), t, pcache, size, pages, page,
         heads, dim)
 
 
-def mixllm_kv4_read(cache, slots, k, v, page: int, stream=None):
-    """The values of the tokens at slots (int32 [T]) into k and v ([T, heads, dim] fp16 or
-    bf16); rows with a negative slot are left as they were."""
+def _read(fn, shape_of, cache, slots, k, v, page, stream):
     t, _, dim = shape = k.shape
-    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dev, pcache, size, pages, heads = shape_of(cache, page, dim)
     dtype, t16, width = _dtype16(k, "k"), k.dtype, heads * dim
     if shape[1] != heads:
         raise ValueError(f"k has {shape[1]} heads, the cache {heads}")
-    _on(dev, stream, _lib.mixllm_kv4_read, pcache, size, pages, page, heads, dim, _flat(slots, "slots", _i32t, dev, t), t,
+    _on(dev, stream, fn, pcache, size, pages, page, heads, dim, _flat(slots, "slots", _i32t, dev, t), t,
         k.data_ptr(), _ld(k, "k", t16, dev, shape, width), v.data_ptr(), _ld(v, "v", t16, dev, shape, width), dtype)
 
 
-def mixllm_kv4_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
-                                         max_len: int, window: int = 0) -> int:
-    for v in (t, b, q_heads, kv_heads, dim, max_rows, max_len, window):
+def _attention_bytes(fn, *sizes):
+    for v in sizes:
         if (v + _HALF) >> 32:
             _past32(v)
-    return int(_lib.mixllm_kv4_attention_workspace_bytes(t, b, q_heads, kv_heads, dim, max_rows, max_len, window))
+    return int(fn(*sizes))
 
 
-def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: int, max_len: int, scale=None,
-                         window: int = 0, lse=None, workspace=None, stream=None):
-    """Attention of the rows q ([T, q_heads, dim] fp16 or bf16) of B requests over the cache:
-    table: int32 [B, width]; lens: int32 [B] tokens cached (these rows' among them); cu: int32
-    [B + 1] first row of each request; out: as q; lse: fp32 [T, q_heads] or None; scale: 1 /
-    sqrt(dim) by default; workspace: a uint8 tensor of mixllm_kv4_attention_workspace_bytes(T,
-    B, ..) for the same arguments (None where that is 0)."""
+def _attention(fn, shape_of, q, cache, table, lens, cu, out, page, max_rows, max_len, scale, window, lse, workspace, stream):
     if (max_rows + _HALF | max_len + _HALF | window + _HALF) >> 32:
         _past32(max_rows, max_len, window)
     t, hq, dim = shape = q.shape
-    dev, pcache, size, pages, heads = _cache(cache, page, dim)
+    dev, pcache, size, pages, heads = shape_of(cache, page, dim)
     dtype, t16, width = _dtype16(q, "q"), q.dtype, hq * dim
     b = lens.numel()
     ptable, ldt, tw = _table(table, b, dev)
@@ -628,10 +625,152 @@ def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: in
     if workspace is not None:
         ws = workspace.numel()
         pws = _flat(workspace, "workspace", _u8t, dev, 0)
-    _on(dev, stream, _lib.mixllm_kv4_attention, q.data_ptr(), _ld(q, "q", t16, dev, shape, width), dtype, t, hq, pcache,
+    _on(dev, stream, fn, q.data_ptr(), _ld(q, "q", t16, dev, shape, width), dtype, t, hq, pcache,
         size, pages, page, heads, dim, ptable, ldt, tw, _flat(lens, "lens", _i32t, dev, 0),
         _flat(cu, "cu", _i32t, dev, b + 1), b, max_rows, max_len, dim ** -0.5 if scale is None else scale, window,
         out.data_ptr(), _ld(out, "out", t16, dev, shape, width), plse, pws, ws)
+
+
+def mixllm_kv4_append(k, v, slots, cache, page: int, stream=None):
+    """Writes k and v ([T, heads, dim] fp16 or bf16, rows may be strided) into the cache at
+    slots (int32 [T], negative: skip the row)."""
+    _append(_lib.mixllm_kv4_append, _cache, k, v, slots, cache, page, stream)
+
+
+def mixllm_kv4_read(cache, slots, k, v, page: int, stream=None):
+    """The values of the tokens at slots (int32 [T]) into k and v ([T, heads, dim] fp16 or
+    bf16); rows with a negative slot are left as they were."""
+    _read(_lib.mixllm_kv4_read, _cache, cache, slots, k, v, page, stream)
+
+
+def mixllm_kv4_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
+                                         max_len: int, window: int = 0) -> int:
+    return _attention_bytes(_lib.mixllm_kv4_attention_workspace_bytes, t, b, q_heads, kv_heads, dim, max_rows, max_len,
+                            window)
+
+
+def mixllm_kv4_attention(q, cache, table, lens, cu, out, page: int, max_rows: int, max_len: int, scale=None,
+                         window: int = 0, lse=None, workspace=None, stream=None):
+    """Attention of the rows q ([T, q_heads, dim] fp16 or bf16) of B requests over the cache:
+    table: int32 [B, width]; lens: int32 [B] tokens cached (these rows' among them); cu: int32
+    [B + 1] first row of each request; out: as q; lse: fp32 [T, q_heads] or None; scale: 1 /
+    sqrt(dim) by default; workspace: a uint8 tensor of mixllm_kv4_attention_workspace_bytes(T,
+    B, ..) for the same arguments (None where that is 0)."""
+    _attention(_lib.mixllm_kv4_attention, _cache, q, cache, table, lens, cu, out, page, max_rows, max_len, scale, window,
+               lse, workspace, stream)
+
+
+def mixllm_head_norm_rotate(q, k, pos, inv_freq, q_out=None, k_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                            neighbours: bool = False, stream=None):
+    """The norms of queries and keys per head and the rotation by position.  q, k: [T, heads,
+    dim] fp16 or bf16 (rows may be strided; one of them may be None); pos: int32 [T]; inv_freq:
+    fp32 [rot / 2], the first rot channels are turned (None: none); q_out, k_out: by default q and
+    k, in place; q_norm, k_norm: [dim] norm weights or None; neighbours: pairs (2i, 2i + 1)
+    instead of (i, i + rot / 2)."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q or k is required")
+    dtype, t16, dev = _dtype16(lead, "q or k"), lead.dtype, _gpu(lead, "q or k")
+    if lead.dim() != 3:
+        raise ValueError(f"q and k must be [T, heads, dim], got {tuple(lead.shape)}")
+    t, _, dim = lead.shape
+    side = []
+    for x, out, w, name in ((q, q_out, q_norm, "q"), (k, k_out, k_norm, "k")):
+        if x is None:
+            if out is not None or w is not None:
+                raise ValueError(f"{name}_out and {name}_norm go with {name}, which is None")
+            side.append((None, 0, None, 0, None, 0))
+            continue
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != t or shape[2] != dim:
+            raise ValueError(f"q and k must be [T, heads, dim] with one T and dim, {name} is {tuple(shape)}")
+        width = shape[1] * dim
+        out = x if out is None else out
+        side.append((x.data_ptr(), _ld(x, name, t16, dev, shape, width), out.data_ptr(),
+                     _ld(out, name + "_out", t16, dev, shape, width),
+                     None if w is None else _channels(w, name + "_norm", t16, dev, dim), shape[1]))
+    (pq, ldq, pqo, ldqo, pqn, hq), (pk, ldk, pko, ldko, pkn, hk) = side
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot and pos is None:
+        raise ValueError("pos is required for a rotation")
+    _on(dev, stream, _lib.mixllm_head_norm_rotate, pq, ldq, pk, ldk, pqo, ldqo, pko, ldko,
+        _flat(pos, "pos", _i32t, dev, t) if rot else None,
+        _flat(inv_freq, "inv_freq", torch.float32, dev, 0) if rot else None, pqn, pkn, t, hq, hk, dim, rot,
+        1 if neighbours else 0, dtype, eps)
+
+
+def mixllm_kv8_page_bytes(page: int, heads: int, dim: int) -> int:
+    if (page + _HALF | heads + _HALF | dim + _HALF) >> 32:
+        _past32(page, heads, dim)
+    return int(_lib.mixllm_kv8_page_bytes(page, heads, dim))
+
+
+def kv8_cache(pages: int, page: int, heads: int, dim: int, device="cuda"):
+    """Storage of one layer's cache in 8 bits: uint8 [pages, heads, bytes of a (page, head) block]."""
+    size = mixllm_kv8_page_bytes(page, heads, dim)
+    if not size or pages <= 0:
+        raise ValueError("pages and heads must be positive, page a power of two of 16 .. 1024, dim 64, 128 or 256")
+    return torch.empty((pages, heads, size // heads), dtype=torch.uint8, device=device)
+
+
+def _cache8(cache, page, dim):
+    """As _cache, of a cache in 8 bits."""
+    block = 2 * page * dim + (page // 2 + 127) // 128 * 128
+    if cache.dtype is _u8t and cache.dim() == 3 and cache.is_contiguous() and cache.shape[2] == block:
+        pages, heads, _ = cache.shape
+        return _gpu(cache, "cache"), cache.data_ptr(), pages * heads * block, pages, heads
+    raise ValueError(f"cache must be a contiguous uint8 tensor [pages, heads, {block}] for page {page} and dim {dim}, is "
+                     f"{cache.dtype} of shape {tuple(cache.shape)}")
+
+
+def mixllm_kv8_append(k, v, slots, cache, page: int, stream=None):
+    """Writes k and v ([T, heads, dim] fp16 or bf16, rows may be strided) into the cache in 8 bits
+    at slots (int32 [T], negative: skip the row; rows of one run of 16 tokens follow one another
+    in the order of their slots)."""
+    _append(_lib.mixllm_kv8_append, _cache8, k, v, slots, cache, page, stream)
+
+
+def mixllm_kv8_read(cache, slots, k, v, page: int, stream=None):
+    """The values of the tokens at slots (int32 [T]) into k and v ([T, heads, dim] fp16 or
+    bf16); rows with a negative slot are left as they were."""
+    _read(_lib.mixllm_kv8_read, _cache8, cache, slots, k, v, page, stream)
+
+
+def mixllm_kv8_attention_workspace_bytes(t: int, b: int, q_heads: int, kv_heads: int, dim: int, max_rows: int,
+                                         max_len: int, window: int = 0) -> int:
+    return _attention_bytes(_lib.mixllm_kv8_attention_workspace_bytes, t, b, q_heads, kv_heads, dim, max_rows, max_len,
+                            window)
+
+
+def mixllm_kv8_attention(q, cache, table, lens, cu, out, page: int, max_rows: int, max_len: int, scale=None,
+                         window: int = 0, lse=None, workspace=None, stream=None):
+    """mixllm_kv4_attention over a cache in 8 bits; workspace: a uint8 tensor of
+    mixllm_kv8_attention_workspace_bytes(T, B, ..) for the same arguments (None where that is 0)."""
+    _attention(_lib.mixllm_kv8_attention, _cache8, q, cache, table, lens, cu, out, page, max_rows, max_len, scale, window,
+               lse, workspace, stream)
+
+
+def mixllm_quant_rows(a, q, s, stream=None):
+    """Quantizes the rows of a ([M, K] fp16 or bf16, rows may be strided) to q (int8 [M, K]) with
+    one scale per row in s (fp32 [M])."""
+    if a.dim() != 2:
+        raise ValueError(f"a must be [M, K], is {tuple(a.shape)}")
+    m, k = shape = a.shape
+    dtype, t16, dev = _dtype16(a, "a"), a.dtype, _gpu(a, "a")
+    _on(dev, stream, _lib.mixllm_quant_rows, a.data_ptr(), _ld(a, "a", t16, dev, shape, k), dtype, m, k, q.data_ptr(),
+        _ld(q, "q", torch.int8, dev, shape, k), _flat(s, "s", torch.float32, dev, m))
+
+
+def mixllm_gemm_w8a8(aq, sa, w, sw, y, stream=None):
+    """y = (aq w^T) sa sw: aq: int8 [M, K], w: int8 [N, K] (rows may be strided), sa: fp32 [M], sw:
+    fp32 [N], y: fp16 or bf16 [M, N] (rows may be strided)."""
+    if aq.dim() != 2 or w.dim() != 2 or aq.shape[1] != w.shape[1]:
+        raise ValueError(f"aq and w must be [M, K] and [N, K], are {tuple(aq.shape)} and {tuple(w.shape)}")
+    (m, k), n = aq.shape, w.shape[0]
+    dtype, dev = _dtype16(y, "y"), _gpu(aq, "aq")
+    _on(dev, stream, _lib.mixllm_gemm_w8a8, aq.data_ptr(), _ld(aq, "aq", torch.int8, dev, aq.shape, k),
+        _flat(sa, "sa", torch.float32, dev, m), w.data_ptr(), _ld(w, "w", torch.int8, dev, w.shape, k),
+        _flat(sw, "sw", torch.float32, dev, n), m, n, k, y.data_ptr(), _ld(y, "y", y.dtype, dev, (m, n), n), dtype)
 
 
 def rowop_buffer(m: int, k: int, device="cuda"):
