@@ -118,6 +118,6 @@ def quant_rows(a):
 
 
 def gemm_w8a8(aq, sa, w, sw):
-    """The product in 64 bits."""
-    acc = aq.astype(np.int64) @ w.astype(np.int64).T
+    """The product in 64 bits, where its sums of whole numbers are exact."""
+    acc = aq.astype(np.float64) @ w.astype(np.float64).T
     return acc * np.asarray(sa, np.float64)[:, None] * np.asarray(sw, np.float64)

@@ -79,7 +79,7 @@ def test_quant_rows_refusals(over, status):
     (dict(k=131088, lda=1 << 18, ldw=1 << 18), SHAPE), (dict(dtype=2), SHAPE), (dict(lda=4080), SHAPE), (dict(lda=4104), SHAPE),
     (dict(ldw=4080), SHAPE), (dict(ldw=4104), SHAPE), (dict(ldy=99), SHAPE), (dict(aq=None), NULL), (dict(sa=None), NULL),
     (dict(w=None), NULL), (dict(sw=None), NULL), (dict(y=None), NULL), (dict(aq=P8), SHAPE), (dict(w=P8), SHAPE),
-    (dict(sa=P2), SHAPE), (dict(sw=ODD), SHAPE), (dict(y=ODD), SHAPE), (dict(m=1 << 30, n=1 << 10, ldy=1 << 10), SHAPE),
+    (dict(sa=P2), SHAPE), (dict(sw=ODD), SHAPE), (dict(y=ODD), SHAPE), (dict(m=1 << 30, n=1 << 10, ldy=1 << 10), SHAPE), (dict(lda=1 << 23), SHAPE), (dict(ldw=1 << 23), SHAPE),
     (dict(m=0, aq=None), 0),
 ])
 def test_gemm_refusals(over, status):

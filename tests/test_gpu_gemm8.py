@@ -65,7 +65,7 @@ def check(y, aq, sa, w, sw, dtype):
 SHAPES = [(1, 1, 16), (1, 512, 1024), (2, 33, 48), (3, 4096, 4096), (4, 1000, 8192), (5, 64, 14336), (8, 256, 144), (15, 130, 2064),
           (16, 1024, 512), (17, 96, 80), (31, 31, 31 * 16), (32, 300, 4096), (33, 257, 1040), (48, 640, 128), (64, 4096, 512),
           (65, 70, 64), (100, 1000, 1008), (127, 129, 272), (128, 512, 4096), (129, 511, 256), (200, 2000, 4096), (256, 256, 128),
-          (257, 255, 144), (300, 4097, 512), (512, 768, 1024), (700, 515, 96), (1025, 1100, 528), (2049, 300, 128), (2047, 4096, 64)]
+          (257, 255, 144), (300, 4097, 512), (512, 768, 1024), (700, 515, 96), (1025, 1100, 528), (2049, 300, 128), (2047, 4096, 64), (3900, 3601, 112)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
