@@ -15,6 +15,7 @@ using mixllm::up;
 
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------------- the quantizer
 
@@ -243,8 +244,9 @@ struct TileShape {
 
 template <class T, bool BF16>
 __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[T::kStage], s1[T::kStage], s2[T::ST > 2 ? T::kStage : 16],
-      s3[T::ST > 3 ? T::kStage : 16];
+  // One array: the compiler then leaves the reads of a stage to the waits below.  With an array per
+  // stage it waits for every copy in flight before each stage's reads.
+  __shared__ __attribute__((aligned(1024))) uint8_t sm[T::ST * T::kStage];
   const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM % T::WN, slice = wave / (T::WM * T::WN);
@@ -271,12 +273,7 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
     ow[p] = (uint32_t)(n0 + row < a.N ? row : a.N - 1 - n0) * (uint32_t)a.ldw;
     kw[p] = ((lane % T::kChunks) ^ T::turn(row)) * 16;
   }
-  auto at = [&](auto stage) {
-    constexpr int S = decltype(stage)::value;
-    return S == 0 ? s0 : S == 1 ? s1 : S == 2 ? s2 : s3;
-  };
-  auto issue = [&](auto stage, int32_t k0) {
-    uint8_t *dst = at(stage);
+  auto issue = [&](uint8_t *dst, int32_t k0) {
     const int32_t last = a.K - 16;  // inputs past the row are read as its last ones and count as zero below
 #pragma unroll
     for (int p = 0; p < T::PA; ++p) {
@@ -298,8 +295,8 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
     for (int u = 0; u < T::TM; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[t][u][i] = 0;
-  auto compute = [&](auto stage, int32_t k0) __attribute__((always_inline)) {
-    const uint8_t *xa = at(stage) + (wm * T::TM * 32 + r) * T::BK, *xw = at(stage) + (T::BM + wn * T::TN * 32 + r) * T::BK;
+  auto compute = [&](const uint8_t *src, auto last, int32_t k0) __attribute__((always_inline)) {
+    const uint8_t *xa = src + (wm * T::TM * 32 + r) * T::BK, *xw = src + (T::BM + wn * T::TN * 32 + r) * T::BK;
 #pragma unroll
     for (int s = 0; s < T::kSteps; ++s) {
       const int chunk = 2 * (slice * T::kSteps + s) + half, place = (chunk ^ T::turn(r)) * 16;
@@ -308,7 +305,7 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
       for (int t = 0; t < T::TN; ++t) w[t] = *reinterpret_cast<const int4v *>(xw + t * 32 * T::BK + place);
 #pragma unroll
       for (int u = 0; u < T::TM; ++u) x[u] = *reinterpret_cast<const int4v *>(xa + u * 32 * T::BK + place);
-      if (k0 + T::BK > a.K) {
+      if constexpr (decltype(last)::value) {
 #pragma unroll
         for (int t = 0; t < T::TN; ++t)
           if (k0 + 16 * chunk >= a.K) w[t] = int4v{0, 0, 0, 0};
@@ -322,35 +319,30 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
 
   constexpr int kAhead = T::ST - 1, kLoads = T::PA + T::PW;
   const int32_t stages = (a.K + T::BK - 1) / T::BK;
-  issue(Const<0>(), 0);
-  if (kAhead > 1 && stages > 1) issue(Const<1>(), T::BK);
-  if (kAhead > 2 && stages > 2) issue(Const<(T::ST > 3 ? 2 : 0)>(), 2 * T::BK);
-  int32_t j = 0;
-  auto step = [&](auto stage) __attribute__((always_inline)) {
-    constexpr int S = decltype(stage)::value;
+  for (int i = 0; i < kAhead && i < stages; ++i) issue(sm + i * T::kStage, i * T::BK);
+  int32_t now = 0, next = kAhead * T::kStage;  // where stage j is, and where stage j + kAhead goes
+  auto ready = [&](int32_t j) __attribute__((always_inline)) {
     // stage j has landed for all, and all have read stage j - 1
     if (j + kAhead - 1 < stages) wait_and_meet<(kAhead - 1) * kLoads>();
     else wait_and_meet<0>();
-    if (j + kAhead < stages) issue(Const<(S + kAhead) % T::ST>(), (j + kAhead) * T::BK);
-    compute(stage, j * T::BK);
-    return ++j == stages;
+    if (j + kAhead < stages) issue(sm + next, (j + kAhead) * T::BK);
   };
-  for (;;) {
-    if (step(Const<0>())) break;
-    if (step(Const<1>())) break;
-    if constexpr (T::ST > 2) {
-      if (step(Const<2>())) break;
-    }
-    if constexpr (T::ST > 3) {
-      if (step(Const<3>())) break;
-    }
+  const int32_t whole = a.K / T::BK;
+  for (int32_t j = 0; j < whole; ++j) {
+    ready(j);
+    compute(sm + now, Const<0>(), 0);
+    now = now + T::kStage == T::ST * T::kStage ? 0 : now + T::kStage;
+    next = next + T::kStage == T::ST * T::kStage ? 0 : next + T::kStage;
+  }
+  if (whole < stages) {
+    ready(whole);
+    compute(sm + now, Const<1>(), whole * T::BK);
   }
 
   if constexpr (T::KS == 2) {  // the second slice's sums go to the first one through LDS
-    static_assert(T::TN * T::TM * 1024 * T::WM * T::WN * 4 <= 2 * T::kStage, "");
+    static_assert(T::TN * T::TM * 1024 * T::WM * T::WN * 4 <= T::ST * T::kStage, "");
     wait_and_meet<0>();
-    int4v *mine = reinterpret_cast<int4v *>(wave % (T::WM * T::WN) < T::WM * T::WN / 2 ? s0 : s1) +
-                  wave % (T::WM * T::WN / 2) * (T::TN * T::TM * 256) + lane;
+    int4v *mine = reinterpret_cast<int4v *>(sm) + wave % (T::WM * T::WN) * (T::TN * T::TM * 256) + lane;
     if (slice == 1) {
 #pragma unroll
       for (int t = 0; t < T::TN; ++t)
@@ -374,13 +366,38 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
           for (int i = 0; i < 4; ++i) acc[t][u][4 * g + i] += v[i];
         }
   }
+  const int32_t mw = m0 + wm * T::TM * 32 + r, nw = n0 + wn * T::TN * 32 + half * 4;
+  if (a.wide && n0 + T::BN <= a.N) {
+    float4v sw[T::TN][4];
+#pragma unroll
+    for (int t = 0; t < T::TN; ++t)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) __builtin_memcpy(&sw[t][g], a.sw + nw + t * 32 + g * 8, 16);
+#pragma unroll
+    for (int u = 0; u < T::TM; ++u) {
+      const int32_t m = mw + u * 32;
+      if (m >= a.M) continue;
+      const float sa = a.sa[m];
+      uint16_t *dst = a.y + (int64_t)m * a.ldy + nw;
+#pragma unroll
+      for (int t = 0; t < T::TN; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = down<BF16>((float)acc[t][u][4 * g + i] * (sa * sw[t][g][i]));
+          *reinterpret_cast<uint2 *>(dst + t * 32 + g * 8) = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        }
+    }
+    return;
+  }
 #pragma unroll
   for (int u = 0; u < T::TM; ++u)
 #pragma unroll
     for (int t = 0; t < T::TN; ++t)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        store4<BF16>(a, m0 + (wm * T::TM + u) * 32 + r, n0 + (wn * T::TN + t) * 32 + g * 8 + half * 4,
+        store4<BF16>(a, mw + u * 32, nw + t * 32 + g * 8,
                      int4v{acc[t][u][4 * g], acc[t][u][4 * g + 1], acc[t][u][4 * g + 2], acc[t][u][4 * g + 3]});
 }
 
