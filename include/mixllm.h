@@ -532,7 +532,7 @@ int mixllm_kv8_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t 
  *   int32 for codes of -127 .. 127 (mixllm_quant_rows gives no others), rounded once to dtype.
  * aq_dev: int8 [M][lda]; w_dev: int8 [N][ldw]; strides % 16 == 0 and below 2^23; sa_dev: fp32 [M],
  * sw_dev: fp32 [N]; y_dev: [M][ldy] of dtype, ldy >= N, element-aligned (ldy % 4 == 0 and 8-byte
- * alignment run faster).  K % 16 == 0, K <= 131072; M in 64s times N in 16s below 2^23.
+ * alignment run faster).  K % 16 == 0, K <= 131072; M in 32s times N in 32s below 2^23.
  * Errors: E_NULL, E_SHAPE, E_HIP.
  * ------------------------------------------------------------------------------------ */
 int mixllm_quant_rows(const void *a_dev, int64_t lda, int32_t dtype, int32_t M, int32_t K, int8_t *q_dev, int64_t ldq,

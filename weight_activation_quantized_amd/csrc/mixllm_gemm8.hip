@@ -27,33 +27,46 @@ struct RowsArgs {
   int32_t M, K;
 };
 
-// A workgroup takes a row, 16 values a thread and chunk, held in registers between the maximum
-// and the codes.
-template <int THREADS, int CHUNKS, bool BF16>
-__global__ __launch_bounds__(THREADS) void quant_rows_kernel(RowsArgs a) {
-  __shared__ float tops[THREADS / 64];
-  const int64_t m = blockIdx.x;
-  const uint16_t *src = a.a + m * a.lda;
-  uint4 raw[CHUNKS][2];
-  float top = 0.0f;
-#pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    const int32_t e = (c * THREADS + (int)threadIdx.x) * 16;
-    raw[c][0] = raw[c][1] = make_uint4(0, 0, 0, 0);
-    if (e < a.K) {
-      raw[c][0] = *reinterpret_cast<const uint4 *>(src + e);
-      raw[c][1] = *reinterpret_cast<const uint4 *>(src + e + 8);
-    }
+// The 16 values of a lane, their largest size and their codes.
+struct Values {
+  uint4 raw[2];
+  __device__ __forceinline__ void load(const uint16_t *src) {
+    raw[0] = *reinterpret_cast<const uint4 *>(src);
+    raw[1] = *reinterpret_cast<const uint4 *>(src + 8);
   }
-  auto value = [&](int c, int j) {
-    const uint4 &r = raw[c][j / 8];
+  template <bool BF16>
+  __device__ __forceinline__ float at(int j) const {
+    const uint4 &r = raw[j / 8];
     const uint32_t w = j % 8 / 2 == 0 ? r.x : j % 8 / 2 == 1 ? r.y : j % 8 / 2 == 2 ? r.z : r.w;
     return up<BF16>(w >> (16 * (j % 2)) & 0xFFFFu);
-  };
+  }
+  template <bool BF16>
+  __device__ __forceinline__ float top() const {
+    float t = 0.0f;
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c)
+    for (int j = 0; j < 16; ++j) t = fmaxf(t, fabsf(at<BF16>(j)));
+    return t;
+  }
+  // rne(x / s) by the reciprocal r of s: x r is within 6e-5 of the quotient (|x / s| <= 127), so
+  // it rounds to the same number unless it lies within 2^-12 of a half; those divide, and so do
+  // all where s is so small that r may not be a number (r = NaN).
+  template <bool BF16>
+  __device__ __forceinline__ uint4 codes(float s, float r) const {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(value(c, j)));
+    for (int j = 0; j < 16; ++j) {
+      const float x = at<BF16>(j), t = x * r;
+      float q = __builtin_rintf(t);
+      if (!(fabsf(t - q) <= 0.5f - 0x1p-12f)) q = s > 0.0f ? __builtin_rintf(x / s) : 0.0f;
+      q = fminf(fmaxf(q, -127.0f), 127.0f);
+      w[j / 4] |= ((uint32_t)(int)q & 0xFFu) << (8 * (j % 4));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <int THREADS>
+__device__ __forceinline__ float row_top(float top, float *tops) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   if (THREADS > 64) {
@@ -62,20 +75,48 @@ __global__ __launch_bounds__(THREADS) void quant_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) top = fmaxf(top, tops[w]);
   }
-  const float s = top / 127.0f;
-  if (threadIdx.x == 0) a.s[m] = s;
+  return top;
+}
+
+__device__ __forceinline__ float inverse(float s) { return s >= 0x1p-100f ? __builtin_amdgcn_rcpf(s) : NAN; }
+
+// A workgroup takes a row, 16 values a thread and chunk, held in registers between the maximum
+// and the codes; without chunks rows of any length, which it reads twice.
+template <int THREADS, int CHUNKS, bool BF16>
+__global__ __launch_bounds__(THREADS) void quant_rows_kernel(RowsArgs a) {
+  __shared__ float tops[THREADS / 64];
+  const int64_t m = blockIdx.x;
+  const uint16_t *src = a.a + m * a.lda;
   int8_t *dst = a.q + m * a.ldq;
+  const int32_t first = (int32_t)threadIdx.x * 16;
+  float top = 0.0f;
+  if constexpr (CHUNKS > 0) {
+    Values v[CHUNKS];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    const int32_t e = (c * THREADS + (int)threadIdx.x) * 16;
-    if (e >= a.K) continue;
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float q = s > 0.0f ? fminf(fmaxf(__builtin_rintf(value(c, j) / s), -127.0f), 127.0f) : 0.0f;
-      w[j / 4] |= ((uint32_t)(int)q & 0xFFu) << (8 * (j % 4));
+    for (int c = 0; c < CHUNKS; ++c) {
+      v[c].raw[0] = v[c].raw[1] = make_uint4(0, 0, 0, 0);
+      if (first + c * THREADS * 16 < a.K) v[c].load(src + first + c * THREADS * 16);
     }
-    *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) top = fmaxf(top, v[c].template top<BF16>());
+    const float s = row_top<THREADS>(top, tops) / 127.0f, r = inverse(s);
+    if (threadIdx.x == 0) a.s[m] = s;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+      if (first + c * THREADS * 16 < a.K)
+        *reinterpret_cast<uint4 *>(dst + first + c * THREADS * 16) = v[c].template codes<BF16>(s, r);
+  } else {
+    Values v;
+    for (int32_t e = first; e < a.K; e += THREADS * 16) {
+      v.load(src + e);
+      top = fmaxf(top, v.template top<BF16>());
+    }
+    const float s = row_top<THREADS>(top, tops) / 127.0f, r = inverse(s);
+    if (threadIdx.x == 0) a.s[m] = s;
+    for (int32_t e = first; e < a.K; e += THREADS * 16) {
+      v.load(src + e);
+      *reinterpret_cast<uint4 *>(dst + e) = v.template codes<BF16>(s, r);
+    }
   }
 }
 
@@ -89,7 +130,7 @@ void launch_rows(const RowsArgs &a, hipStream_t s) {
   else if (a.K <= 8192) hipLaunchKernelGGL((quant_rows_kernel<512, 1, BF16>), grid, dim3(512), 0, s, a);
   else if (a.K <= 16384) hipLaunchKernelGGL((quant_rows_kernel<512, 2, BF16>), grid, dim3(512), 0, s, a);
   else if (a.K <= 32768) hipLaunchKernelGGL((quant_rows_kernel<1024, 2, BF16>), grid, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((quant_rows_kernel<1024, 8, BF16>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((quant_rows_kernel<1024, 0, BF16>), grid, dim3(1024), 0, s, a);
 }
 
 // --------------------------------------------------------------------------- the product
@@ -119,88 +160,6 @@ __device__ __forceinline__ void store4(const Gemm8Args &a, int32_t m, int32_t n,
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (n + i < a.N) dst[i] = (uint16_t)v[i];
-  }
-}
-
-// Few tokens: the weights are read once, straight into the matrix instruction's operands.  A
-// workgroup takes 16 NT channels and 16 MT tokens, its 8 waves blocks of 64 S inputs in turn, and
-// adds their sums through LDS.
-constexpr int kStreamWaves = 8;
-
-template <int MT, int NT, bool BF16>
-__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(Gemm8Args a) {
-  constexpr int S = MT > 2 ? 2 : 4, kStreamBlock = 64 * S;
-  __shared__ int4v red[kStreamWaves][NT * MT][64];
-  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t n0 = blockIdx.x * (16 * NT);
-  const int8_t *pw[NT], *pa[MT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) pw[t] = a.w + (int64_t)(n0 + 16 * t + r < a.N ? n0 + 16 * t + r : a.N - 1) * a.ldw;
-#pragma unroll
-  for (int u = 0; u < MT; ++u) pa[u] = a.a + (int64_t)(16 * u + r < a.M ? 16 * u + r : a.M - 1) * a.lda;
-  struct Block {
-    int4v w[NT][S], x[MT][S];
-  };
-  auto load = [&](Block &b, int32_t k0) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      int32_t k = k0 + 64 * s + 16 * c;
-      k = k < a.K ? k : a.K - 16;  // what is past the row counts as zero below
-#pragma unroll
-      for (int t = 0; t < NT; ++t) b.w[t][s] = *reinterpret_cast<const int4v *>(pw[t] + k);
-#pragma unroll
-      for (int u = 0; u < MT; ++u) b.x[u][s] = *reinterpret_cast<const int4v *>(pa[u] + k);
-    }
-  };
-  int4v acc[NT][MT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int u = 0; u < MT; ++u) acc[t][u] = int4v{0, 0, 0, 0};
-  auto add = [&](Block &b, int32_t k0) {
-    if (k0 + kStreamBlock > a.K) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (k0 + 64 * s + 16 * c >= a.K) b.w[t][s] = int4v{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-          acc[t][u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[t][s], b.x[u][s], acc[t][u], 0, 0, 0);
-  };
-  constexpr int32_t kStep = kStreamWaves * kStreamBlock;
-  int32_t k = wave * kStreamBlock;
-  if (k < a.K) {
-    Block b0, b1;
-    load(b0, k);
-    for (;;) {
-      if (k + kStep < a.K) load(b1, k + kStep);
-      __builtin_amdgcn_sched_barrier(0);
-      add(b0, k);
-      if ((k += kStep) >= a.K) break;
-      if (k + kStep < a.K) load(b0, k + kStep);
-      __builtin_amdgcn_sched_barrier(0);
-      add(b1, k);
-      if ((k += kStep) >= a.K) break;
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int u = 0; u < MT; ++u) red[wave][t * MT + u][lane] = acc[t][u];
-  __syncthreads();
-  for (int e = threadIdx.x; e < NT * MT * 64; e += 64 * kStreamWaves) {
-    const int tile = e >> 6, l = e & 63;
-    int4v sum = red[0][tile][l];
-#pragma unroll
-    for (int w = 1; w < kStreamWaves; ++w) sum += red[w][tile][l];
-    store4<BF16>(a, tile % MT * 16 + (l & 15), n0 + tile / MT * 16 + (l >> 4) * 4, sum);
   }
 }
 
@@ -238,8 +197,8 @@ struct TileShape {
   static constexpr int kStage = (BM + BN) * BK;
   static constexpr int PA = BM * BK / 1024 / kWaves, PW = BN * BK / 1024 / kWaves;  // copies of a wave and stage
   static_assert(PA * kWaves * 1024 == BM * BK && PW * kWaves * 1024 == BN * BK, "whole copies");
-  static_assert((BK == 64 || BK == 128) && ST >= 2 && ST <= 4, "");
-  static __device__ __forceinline__ int turn(int row) { return BK == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
+  static_assert((BK == 128 || BK == 256) && ST >= 2, "");
+  static __device__ __forceinline__ int turn(int row) { return BK == 128 ? (row >> 1) & 7 : row & 15; }
 };
 
 template <class T, bool BF16>
@@ -295,25 +254,30 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
     for (int u = 0; u < T::TM; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[t][u][i] = 0;
-  auto compute = [&](const uint8_t *src, auto last, int32_t k0) __attribute__((always_inline)) {
+  // A step's operands are read while the step before is multiplied: two sets.
+  int4v w[2][T::TN], x[2][T::TM];
+  auto read = [&](const uint8_t *src, int s) __attribute__((always_inline)) {
     const uint8_t *xa = src + (wm * T::TM * 32 + r) * T::BK, *xw = src + (T::BM + wn * T::TN * 32 + r) * T::BK;
+    const int place = ((2 * (slice * T::kSteps + s) + half) ^ T::turn(r)) * 16;
 #pragma unroll
-    for (int s = 0; s < T::kSteps; ++s) {
-      const int chunk = 2 * (slice * T::kSteps + s) + half, place = (chunk ^ T::turn(r)) * 16;
-      int4v w[T::TN], x[T::TM];
+    for (int t = 0; t < T::TN; ++t) w[s % 2][t] = *reinterpret_cast<const int4v *>(xw + t * 32 * T::BK + place);
 #pragma unroll
-      for (int t = 0; t < T::TN; ++t) w[t] = *reinterpret_cast<const int4v *>(xw + t * 32 * T::BK + place);
+    for (int u = 0; u < T::TM; ++u) x[s % 2][u] = *reinterpret_cast<const int4v *>(xa + u * 32 * T::BK + place);
+  };
+  auto multiply = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < T::TM; ++u) x[u] = *reinterpret_cast<const int4v *>(xa + u * 32 * T::BK + place);
-      if constexpr (decltype(last)::value) {
+    for (int t = 0; t < T::TN; ++t)
 #pragma unroll
-        for (int t = 0; t < T::TN; ++t)
-          if (k0 + 16 * chunk >= a.K) w[t] = int4v{0, 0, 0, 0};
-      }
+      for (int u = 0; u < T::TM; ++u)
+        acc[t][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[s % 2][t], x[s % 2][u], acc[t][u], 0, 0, 0);
+  };
+  // The order of a step: one read after each of the first products.
+  auto mixed = [&]() __attribute__((always_inline)) {
+    constexpr int kReads = T::TN + T::TM, kProducts = T::TN * T::TM;
 #pragma unroll
-      for (int t = 0; t < T::TN; ++t)
-#pragma unroll
-        for (int u = 0; u < T::TM; ++u) acc[t][u] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[t], x[u], acc[t][u], 0, 0, 0);
+    for (int i = 0; i < (kProducts > kReads ? kProducts : kReads); ++i) {
+      if (i < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i < kProducts) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     }
   };
 
@@ -328,43 +292,63 @@ __global__ __launch_bounds__(T::kThreads) void tile_kernel(Gemm8Args a) {
     if (j + kAhead < stages) issue(sm + next, (j + kAhead) * T::BK);
   };
   const int32_t whole = a.K / T::BK;
+  static_assert(T::kSteps % 2 == 0, "the last step of a stage is in the second set");
+  ready(0);
+  read(sm, 0);
   for (int32_t j = 0; j < whole; ++j) {
-    ready(j);
-    compute(sm + now, Const<0>(), 0);
+#pragma unroll
+    for (int s = 0; s + 1 < T::kSteps; ++s) {
+      read(sm + now, s + 1);
+      multiply(s);
+      mixed();
+    }
     now = now + T::kStage == T::ST * T::kStage ? 0 : now + T::kStage;
     next = next + T::kStage == T::ST * T::kStage ? 0 : next + T::kStage;
+    ready(j + 1);       // while the last step's operands are in registers
+    read(sm + now, 0);  // behind the last stage: read and not used
+    multiply(T::kSteps - 1);
+    mixed();
   }
   if (whole < stages) {
-    ready(whole);
-    compute(sm + now, Const<1>(), whole * T::BK);
+#pragma unroll
+    for (int s = 0; s < T::kSteps; ++s) {
+      if (s) read(sm + now, s);
+#pragma unroll
+      for (int t = 0; t < T::TN; ++t)
+        if (whole * T::BK + 16 * (2 * (slice * T::kSteps + s) + half) >= a.K) w[s % 2][t] = int4v{0, 0, 0, 0};
+      multiply(s);
+    }
   }
 
-  if constexpr (T::KS == 2) {  // the second slice's sums go to the first one through LDS
-    static_assert(T::TN * T::TM * 1024 * T::WM * T::WN * 4 <= T::ST * T::kStage, "");
+  if constexpr (T::KS > 1) {  // the other slices' sums go to the first one through LDS
+    constexpr int kSums = T::TN * T::TM * 4 * 64, kGroup = T::WM * T::WN;
+    static_assert((T::KS - 1) * kGroup * kSums * 16 <= T::ST * T::kStage, "");
     wait_and_meet<0>();
-    int4v *mine = reinterpret_cast<int4v *>(sm) + wave % (T::WM * T::WN) * (T::TN * T::TM * 256) + lane;
-    if (slice == 1) {
+    int4v *sums = reinterpret_cast<int4v *>(sm) + lane;
+    if (slice) {
 #pragma unroll
       for (int t = 0; t < T::TN; ++t)
 #pragma unroll
         for (int u = 0; u < T::TM; ++u)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            mine[((t * T::TM + u) * 4 + g) * 64] =
+            sums[(wave - kGroup) * kSums + ((t * T::TM + u) * 4 + g) * 64] =
                 int4v{acc[t][u][4 * g], acc[t][u][4 * g + 1], acc[t][u][4 * g + 2], acc[t][u][4 * g + 3]};
     }
     __syncthreads();
-    if (slice == 1) return;
+    if (slice) return;
 #pragma unroll
-    for (int t = 0; t < T::TN; ++t)
+    for (int q = 0; q + 1 < T::KS; ++q)
 #pragma unroll
-      for (int u = 0; u < T::TM; ++u)
+      for (int t = 0; t < T::TN; ++t)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int4v v = mine[((t * T::TM + u) * 4 + g) * 64];
+        for (int u = 0; u < T::TM; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][u][4 * g + i] += v[i];
-        }
+          for (int g = 0; g < 4; ++g) {
+            const int4v v = sums[(wave + q * kGroup) * kSums + ((t * T::TM + u) * 4 + g) * 64];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][u][4 * g + i] += v[i];
+          }
   }
   const int32_t mw = m0 + wm * T::TM * 32 + r, nw = n0 + wn * T::TN * 32 + half * 4;
   if (a.wide && n0 + T::BN <= a.N) {
@@ -407,31 +391,46 @@ void launch_tiles(Gemm8Args a, hipStream_t s) {
   hipLaunchKernelGGL((tile_kernel<T, BF16>), dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(T::kThreads), 0, s, a);
 }
 
-template <int MT, int NT, bool BF16>
-void launch_stream(const Gemm8Args &a, hipStream_t s) {
-  hipLaunchKernelGGL((stream_kernel<MT, NT, BF16>), dim3((unsigned)((a.N + 16 * NT - 1) / (16 * NT))),
-                     dim3(64 * kStreamWaves), 0, s, a);
-}
+using Tile256x256 = TileShape<256, 256, 2, 4, 1, 128, 2>;
+using Tile256x128 = TileShape<256, 128, 4, 2, 1, 128, 3>;
+using Tile128x128 = TileShape<128, 128, 2, 2, 2, 128, 4>;
+using Tile64x128 = TileShape<64, 128, 2, 2, 2, 128, 4>;
+using Tile64x64 = TileShape<64, 64, 2, 2, 2, 128, 4>;
+using Tile32x64 = TileShape<32, 64, 1, 2, 4, 256, 3>;
+using Tile32x32 = TileShape<32, 32, 1, 1, 4, 256, 4>;
 
-using Large = TileShape<256, 256, 2, 4, 1, 64, 4>;
-using Middle = TileShape<128, 128, 2, 2, 2, 128, 4>;
-using Small = TileShape<64, 128, 2, 2, 2, 128, 3>;
-
+// The tile: how long the tiles' rounds of 256 CUs take (measured for 4096 inputs, while the
+// device is not full, where a small tile waits for its copies and a large one for the products),
+// and not less than the inputs' bytes.  Measured, us, 4096 inputs, from the largest tile down
+// (- : not measured):
+//    4 x 4096:     -   -  17  11.6   8.6  7.3  7.2      64 x 4096:     -  -  17  12.4  9.1  7.8  7.3
+//  128 x 4096:    43   -  18  12.5   9.4  9.2  9.3     256 x 4096:    48 28  18  12.8 10.4   -    -
+//  512 x 4096:    48  29  19  15.0  17.5   -    -      1024 x 4096:   49 30  25  26.4 32.5   -    -
+// 2047 x 4096:    54  43  52  58    78     -    -      1024 x 14336:  67 77  96 101  124     -    -
+// A tile with room for the tokens twice over is left out.
 template <bool BF16>
 void launch_gemm(const Gemm8Args &a, hipStream_t s) {
-  if (a.M <= 16) {
-    if (a.N >= 16384) launch_stream<1, 4, BF16>(a, s);
-    else if (a.N >= 8192) launch_stream<1, 2, BF16>(a, s);
-    else launch_stream<1, 1, BF16>(a, s);
-  } else if (a.M <= 32) {
-    launch_stream<2, 2, BF16>(a, s);
-  } else if (a.M <= 64) {
-    launch_stream<4, 2, BF16>(a, s);
-  } else {
-    auto tiles = [&](int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= 200) launch_tiles<Large, BF16>(a, s);
-    else if (tiles(128, 128) >= 200) launch_tiles<Middle, BF16>(a, s);
-    else launch_tiles<Small, BF16>(a, s);
+  constexpr struct {
+    int32_t m, n;
+    float us;
+  } kind[] = {{32, 32, 7.2f}, {32, 64, 7.6f}, {64, 64, 9.1f}, {64, 128, 12.4f}, {128, 128, 17.9f}, {256, 128, 28.1f}, {256, 256, 42.4f}};
+  const float bytes_us = ((float)a.M * (float)a.K + (float)a.N * (float)a.K + 2.0f * (float)a.M * (float)a.N) / 5.5e6f;
+  int best = 0;
+  float least = INFINITY;
+  for (int i = 0; i < 7 && (i == 0 || kind[i].m < 2 * (int64_t)a.M); ++i) {
+    const int64_t tiles = ((int64_t)a.M + kind[i].m - 1) / kind[i].m * (((int64_t)a.N + kind[i].n - 1) / kind[i].n);
+    const float rounds_us = (float)((tiles + 255) / 256) * kind[i].us * (float)a.K / 4096.0f;
+    const float us = (rounds_us > bytes_us ? rounds_us : bytes_us) + 0.1f * rounds_us;
+    if (us < least) least = us, best = i;
+  }
+  switch (best) {
+    case 0: return launch_tiles<Tile32x32, BF16>(a, s);
+    case 1: return launch_tiles<Tile32x64, BF16>(a, s);
+    case 2: return launch_tiles<Tile64x64, BF16>(a, s);
+    case 3: return launch_tiles<Tile64x128, BF16>(a, s);
+    case 4: return launch_tiles<Tile128x128, BF16>(a, s);
+    case 5: return launch_tiles<Tile256x128, BF16>(a, s);
+    default: return launch_tiles<Tile256x256, BF16>(a, s);
   }
 }
 
@@ -463,7 +462,7 @@ extern "C" int mixllm_gemm_w8a8(const int8_t *aq, int64_t lda, const float *sa, 
       (reinterpret_cast<uintptr_t>(y) & 1))
     return MIXLLM_E_SHAPE;
   // rows of a tile are reached by 32-bit offsets, and tiles counted in 32 bits
-  if (lda >= 1 << 23 || ldw >= 1 << 23 || ((int64_t)M + 63) / 64 * (((int64_t)N + 15) / 16) >= 1 << 23) return MIXLLM_E_SHAPE;
+  if (lda >= 1 << 23 || ldw >= 1 << 23 || ((int64_t)M + 31) / 32 * (((int64_t)N + 31) / 32) >= 1 << 23) return MIXLLM_E_SHAPE;
   const Gemm8Args g = {aq, w, sa, sw, static_cast<uint16_t *>(y), lda, ldw, ldy, M, N, K, 0, 0,
                        ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0};
   if (dtype == MIXLLM_BF16) launch_gemm<true>(g, (hipStream_t)stream);
