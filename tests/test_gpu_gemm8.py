@@ -24,7 +24,7 @@ def L():
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("m,k", [(1, 16), (3, 1024), (5, 1040), (2, 4096), (7, 4112), (1, 8208), (2, 16400), (1, 32784),
-                                 (1, 131072), (300, 128)])
+                                 (1, 131072), (300, 128), (1500, 2032), (1100, 4080), (1030, 8176)])
 def test_quant_rows(L, m, k, dtype):
     U.say("quant rows", m, k, dtype)
     rng = np.random.default_rng(m + k)

@@ -26,7 +26,8 @@ struct RotateArgs {
   const uint16_t *qn, *kn;
   int64_t ldq, ldk, ldqo, ldko;
   int32_t T, hq, heads, dim, rot;  // heads: of queries and keys
-  float eps;
+  int32_t parts;                   // waves that share a token
+  float eps, inv_dim;
 };
 
 // cos and sin of pos * freq.  The product and its share of a turn are formed with what their
@@ -57,90 +58,129 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// The 8 values of 16 bytes, and back.
 template <bool BF16>
-__device__ __forceinline__ void unpack4(uint2 w, float *x) {
-  x[0] = up<BF16>(w.x & 0xFFFFu), x[1] = up<BF16>(w.x >> 16);
-  x[2] = up<BF16>(w.y & 0xFFFFu), x[3] = up<BF16>(w.y >> 16);
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint2 pack4(const float *x) {
-  return make_uint2(down<BF16>(x[0]) | down<BF16>(x[1]) << 16, down<BF16>(x[2]) | down<BF16>(x[3]) << 16);
-}
-
-// A wave takes one token and 64 / L of its heads at a time; L lanes hold a head, 8 channels
-// each, so that a lane has both channels of its four pairs and nothing but the norm's sum
-// crosses lanes.  A lane's cosines and sines are those of all heads: formed once.
-template <int L, bool BF16, bool NEXT>
-__global__ void rotate_kernel(RotateArgs a) {
-  const int lane = threadIdx.x & 63, u = lane & (L - 1);
-  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int64_t t = blockIdx.x;
-  const bool live = u < a.dim / 8, turned = u < a.rot / 8;
-  const int e0 = !NEXT && turned ? 4 * u : 8 * u, e1 = !NEXT && turned ? a.rot / 2 + 4 * u : 8 * u + 4;
-  const int step = waves * (64 / L);
-  int32_t h = wave * (64 / L) + lane / L;
-  uint2 raw0 = make_uint2(0, 0), raw1 = raw0;
-  auto load = [&](int32_t head) {
-    if (head >= a.heads || !live) return;
-    const uint16_t *src = head < a.hq ? a.q + t * a.ldq + (int64_t)head * a.dim
-                                      : a.k + t * a.ldk + (int64_t)(head - a.hq) * a.dim;
-    raw0 = *reinterpret_cast<const uint2 *>(src + e0);
-    raw1 = *reinterpret_cast<const uint2 *>(src + e1);
-  };
-  load(h);
-  float cs[4], sn[4], w[2][8];
+__device__ __forceinline__ void unpack8(uint4 v, float *x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[0][j] = w[1][j] = 1.0f;
+  for (int j = 0; j < 4; ++j) x[2 * j] = up<BF16>(w[j] & 0xFFFFu), x[2 * j + 1] = up<BF16>(w[j] >> 16);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float *x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = down<BF16>(x[2 * j]) | down<BF16>(x[2 * j + 1]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 either(bool first, uint4 a, uint4 b) {
+  return make_uint4(first ? a.x : b.x, first ? a.y : b.y, first ? a.z : b.z, first ? a.w : b.w);
+}
+
+constexpr int kWavesOfBlock = 4;
+
+// A wave takes a token, or one of `parts` shares of its heads, and 64 / L heads at a time; L lanes
+// hold a head, 16 channels each, so that a lane has both channels of its eight pairs and nothing
+// but the norm's sum crosses lanes.  The cosines and sines of a token are formed once, a pair a
+// lane, and dealt out through LDS.
+template <int L, bool BF16, bool NEXT>
+__global__ __launch_bounds__(64 * kWavesOfBlock) void rotate_kernel(RotateArgs a) {
+  constexpr int kPairs = 8 * L;  // of the longest head, room for
+  __shared__ float2 turns[kWavesOfBlock][kPairs];
+  const int lane = threadIdx.x & 63, u = lane & (L - 1), wave = threadIdx.x >> 6;
+  const int64_t id = (int64_t)blockIdx.x * kWavesOfBlock + wave, t = id / a.parts;
+  if (t >= a.T) return;  // whole waves: none waits for another
+  const bool live = u < a.dim / 16, turned = u < a.rot / 16;
+  const int e0 = !NEXT && turned ? 8 * u : 16 * u, e1 = !NEXT && turned ? a.rot / 2 + 8 * u : 16 * u + 8;
+  const int step = a.parts * (64 / L);
+  int32_t h = (int32_t)(id - t * a.parts) * (64 / L) + lane / L;
+  auto place = [&](int32_t head, bool key, const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk) {
+    return key ? k + t * ldk + (int64_t)(head - a.hq) * a.dim : q + t * ldq + (int64_t)head * a.dim;
+  };
+  uint4 raw0[2], raw1[2];
+  auto load = [&](uint4 (&to)[2], int32_t head) __attribute__((always_inline)) {
+    to[0] = to[1] = make_uint4(0, 0, 0, 0);
+    if (head >= a.heads || !live) return;
+    const uint16_t *src = place(head, head >= a.hq, a.q, a.ldq, a.k, a.ldk);
+    to[0] = *reinterpret_cast<const uint4 *>(src + e0);
+    to[1] = *reinterpret_cast<const uint4 *>(src + e1);
+  };
+  load(raw0, h);
+  load(raw1, h + step);
+  uint4 w[2][2];
 #pragma unroll
   for (int z = 0; z < 2; ++z) {
     const uint16_t *src = z ? a.kn : a.qn;
+    w[z][0] = w[z][1] = make_uint4(0, 0, 0, 0);
     if (src && live) {
-      unpack4<BF16>(*reinterpret_cast<const uint2 *>(src + e0), w[z]);
-      unpack4<BF16>(*reinterpret_cast<const uint2 *>(src + e1), w[z] + 4);
+      w[z][0] = *reinterpret_cast<const uint4 *>(src + e0);
+      w[z][1] = *reinterpret_cast<const uint4 *>(src + e1);
     }
   }
-  const int32_t pos = a.rot ? a.pos[t] : 0;
+  float cs[8], sn[8];
+  if (a.rot) {
+    const int32_t pos = a.pos[t];
+    for (int p = lane; p < a.rot / 2; p += 64) {
+      float c, s;
+      turn_of(pos, a.freq[p], c, s);
+      turns[wave][p] = make_float2(c, s);
+    }
+    // a wave's LDS operations are done in order, so only the compiler has to be held
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    cs[j] = 1.0f, sn[j] = 0.0f;
-    if (turned) turn_of(pos, a.freq[4 * u + j], cs[j], sn[j]);
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = turns[wave][8 * u + j];
+      cs[j] = v.x, sn[j] = v.y;
+    }
   }
-  for (; h - lane / L < a.heads; h += step) {
-    const bool there = h < a.heads && live;
-    float x[8];
-    unpack4<BF16>(raw0, x);
-    unpack4<BF16>(raw1, x + 4);
-    load(h + step);
-    const bool key = h >= a.hq;
+  auto one = [&](uint4 (&now)[2]) __attribute__((always_inline)) {
+    const bool there = h < a.heads && live, key = h >= a.hq;
+    float x[16];
+    unpack8<BF16>(now[0], x);
+    unpack8<BF16>(now[1], x + 8);
+    load(now, h + 2 * step);
     if (a.qn || a.kn) {
       float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-      ss = lanes_sum<L>(there ? ss : 0.0f);
-      const float r = 1.0f / sqrtf(ss / (float)a.dim + a.eps);
+      for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
+      ss = lanes_sum<L>(ss);
       if (key ? a.kn != nullptr : a.qn != nullptr) {
+        const float r = __builtin_amdgcn_rsqf(ss * a.inv_dim + a.eps);  // within 1 ulp
+        float g[16];
+        unpack8<BF16>(either(key, w[1][0], w[0][0]), g);
+        unpack8<BF16>(either(key, w[1][1], w[0][1]), g + 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r * (key ? w[1][j] : w[0][j]);
+        for (int j = 0; j < 16; ++j) x[j] *= r * g[j];
       }
     }
     if (turned) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float &p = NEXT ? x[2 * j] : x[j], &q = NEXT ? x[2 * j + 1] : x[4 + j];
-        const float first = p * cs[j] - q * sn[j], second = fmaf(p, sn[j], q * cs[j]);
+      for (int j = 0; j < 8; ++j) {
+        float &p = NEXT ? x[2 * j] : x[j], &q = NEXT ? x[2 * j + 1] : x[8 + j];
+        const float first = fmaf(p, cs[j], -(q * sn[j])), second = fmaf(p, sn[j], q * cs[j]);
         p = first, q = second;
       }
     }
     if (there) {
-      uint16_t *dst = key ? a.ko + t * a.ldko + (int64_t)(h - a.hq) * a.dim : a.qo + t * a.ldqo + (int64_t)h * a.dim;
-      *reinterpret_cast<uint2 *>(dst + e0) = pack4<BF16>(x);
-      *reinterpret_cast<uint2 *>(dst + e1) = pack4<BF16>(x + 4);
+      uint16_t *dst = const_cast<uint16_t *>(place(h, key, a.qo, a.ldqo, a.ko, a.ldko));
+      *reinterpret_cast<uint4 *>(dst + e0) = pack8<BF16>(x);
+      *reinterpret_cast<uint4 *>(dst + e1) = pack8<BF16>(x + 8);
     }
+    h += step;
+  };
+  const int32_t end = a.heads + lane / L;  // the wave's first head is past the last one
+  while (h < end) {
+    one(raw0);
+    if (h >= end) break;
+    one(raw1);
   }
 }
 
 constexpr int32_t kMaxDim = 512;
+constexpr int32_t kEnoughWaves = 4096;
 
 // Any even number of channels and element-aligned rows: a wave takes one head, a lane single
 // pairs of it.
@@ -192,12 +232,12 @@ __global__ __launch_bounds__(256) void rotate_any_kernel(RotateArgs a) {
   }
 }
 
+// Few tokens are shared by waves until each has one head group, or there are about 4096.
 template <int L, bool BF16>
-void launch(const RotateArgs &a, bool next, hipStream_t s) {
-  const int heads_a_wave = 64 / L, all = (a.heads + heads_a_wave - 1) / heads_a_wave;
-  int waves = a.T >= 1024 ? 4 : 16;
-  waves = waves < all ? waves : all;
-  const dim3 grid((unsigned)a.T), block((unsigned)(64 * waves));
+void launch(RotateArgs a, bool next, hipStream_t s) {
+  const int all = (a.heads + 64 / L - 1) / (64 / L), want = (kEnoughWaves + a.T - 1) / a.T;
+  a.parts = want < all ? want : all;
+  const dim3 grid((unsigned)(((int64_t)a.T * a.parts + kWavesOfBlock - 1) / kWavesOfBlock)), block(64 * kWavesOfBlock);
   if (next) hipLaunchKernelGGL((rotate_kernel<L, BF16, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((rotate_kernel<L, BF16, false>), grid, block, 0, s, a);
 }
@@ -209,13 +249,13 @@ void launch(const RotateArgs &a, bool next, bool wide, hipStream_t s) {
     if (next) hipLaunchKernelGGL((rotate_any_kernel<BF16, true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((rotate_any_kernel<BF16, false>), grid, dim3(256), 0, s, a);
   } else if (a.dim <= 64) {
-    launch<8, BF16>(a, next, s);
+    launch<4, BF16>(a, next, s);
   } else if (a.dim <= 128) {
-    launch<16, BF16>(a, next, s);
+    launch<8, BF16>(a, next, s);
   } else if (a.dim <= 256) {
-    launch<32, BF16>(a, next, s);
+    launch<16, BF16>(a, next, s);
   } else {
-    launch<64, BF16>(a, next, s);
+    launch<32, BF16>(a, next, s);
   }
 }
 
@@ -231,7 +271,7 @@ extern "C" int mixllm_head_norm_rotate(const void *q, int64_t ldq, const void *k
       !(eps >= 0.0f) || q_heads > 65535 || kv_heads > 65535)
     return MIXLLM_E_SHAPE;
   const int32_t heads = q_heads + kv_heads;
-  // a launch has fewer than 2^32 threads: 64 for a head, or 256 or fewer for each of so many tokens
+  // a launch has fewer than 2^32 threads: 64 at most for a head of a token
   if (T >= 1 << 24 || (int64_t)T * heads >= 1 << 26) return MIXLLM_E_SHAPE;
   if (T == 0 || heads == 0) return MIXLLM_OK;
   if ((q_heads && (!q || !q_out)) || (kv_heads && (!k || !k_out)) || (rot && (!pos || !inv_freq)) ||
@@ -240,17 +280,17 @@ extern "C" int mixllm_head_norm_rotate(const void *q, int64_t ldq, const void *k
   const int64_t qw = (int64_t)q_heads * dim, kw = (int64_t)kv_heads * dim;
   if (ldq < qw || ldqo < qw || ldk < kw || ldko < kw) return MIXLLM_E_SHAPE;
   const void *all[] = {q, k, q_out, k_out, q_norm, k_norm};
-  bool wide = dim % 8 == 0 && rot % 8 == 0;
+  bool wide = dim % 16 == 0 && rot % 16 == 0;
   for (const void *p : all) {
     if (reinterpret_cast<uintptr_t>(p) & 1) return MIXLLM_E_SHAPE;
-    wide = wide && (reinterpret_cast<uintptr_t>(p) & 7) == 0;
+    wide = wide && mixllm::is_aligned16(p);
   }
-  wide = wide && (ldq | ldqo) % 4 == 0 && (ldk | ldko) % 4 == 0;
+  wide = wide && (ldq | ldqo) % 8 == 0 && (ldk | ldko) % 8 == 0;
   if (!mixllm::is_aligned4(pos) || !mixllm::is_aligned4(inv_freq)) return MIXLLM_E_SHAPE;
   const RotateArgs a = {static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
                         static_cast<uint16_t *>(q_out), static_cast<uint16_t *>(k_out), pos, inv_freq,
                         static_cast<const uint16_t *>(q_norm), static_cast<const uint16_t *>(k_norm),
-                        ldq, ldk, ldqo, ldko, T, q_heads, heads, dim, rot, eps};
+                        ldq, ldk, ldqo, ldko, T, q_heads, heads, dim, rot, 1, eps, 1.0f / (float)dim};
   if (dtype == MIXLLM_BF16) launch<true>(a, neighbours != 0, wide, (hipStream_t)stream);
   else launch<false>(a, neighbours != 0, wide, (hipStream_t)stream);
   return mixllm::launch_status();
