@@ -472,3 +472,47 @@ def test_binding_refuses(L):
             call()
     with pytest.raises(L.MixLLMError):      # splits need a workspace
         L.mixllm_kv8_attention(x[:1], cache, i32([[0] * 256]), s[:1], s[:2], torch.empty_like(x[:1]), 16, 1, 4096)
+
+
+def some_table(requests, per, page, seed):
+    rng = np.random.default_rng(seed)
+    return rng.permutation(requests * per + 3)[:requests * per].reshape(requests, per)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,heads,requests", [(64, 8, 600), (128, 3, 1400), (256, 2, 2100)])
+def test_append_of_many_requests(L, dim, heads, requests, dtype):
+    """Steps of single tokens and of a few each, of so many requests that workgroups take many rows."""
+    U.say("append8 many", dim, heads, requests, dtype)
+    page, held = 16, np.arange(requests) * 5 % 23
+    table = some_table(requests, 3, page, 1)
+    want = new_cache(3 * requests + 3, heads, page, dim)
+    dev = cuda(want)
+    for i, most in enumerate((23, 1, 3)):
+        add = held if i == 0 else 1 + np.arange(requests) * 7 % most
+        at = np.zeros(requests, int) if i == 0 else held
+        slots = np.concatenate([slots_of(table[b], np.arange(at[b], at[b] + add[b]), page) for b in range(requests)])
+        held = at + add
+        k, v = key_values(len(slots), heads, dim, dtype, i)
+        L.mixllm_kv8_append(cuda(k, dtype), cuda(v, dtype), i32(slots), dev, page)
+        E.kv8_write(want, slots, k, v, page)
+        got = dev.cpu().numpy()
+        assert np.array_equal(got, want), (i, np.argwhere(got != want)[:5])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_quotients_at_halves(L, dtype):
+    """Values whose quotients are halves or next to them, over many scales: rounded as the division says."""
+    dim, heads, page, runs = 64, 2, 64, 40
+    rng = np.random.default_rng(4)
+    x = (rng.integers(-254, 255, (16 * runs, heads, dim)) / 2).astype(np.float32)
+    x[::16, :, 0] = 127
+    s = np.exp2(rng.integers(-9, 6, (runs, heads)).astype(np.float32)) * rng.choice([1, 1.0009765625, 0.99951171875, 1.25], (runs, heads))
+    x = rounded((x.reshape(runs, 16, heads, dim) * s[:, None, :, None]).reshape(-1, heads, dim).astype(np.float32), dtype)
+    v = rounded(x[::-1] * np.float32(0.37), dtype)
+    want = new_cache(runs * 16 // page, heads, page, dim)
+    dev = cuda(want)
+    slots = np.arange(16 * runs, dtype=np.int32)
+    L.mixllm_kv8_append(cuda(x, dtype), cuda(v, dtype), i32(slots), dev, page)
+    E.kv8_write(want, slots, x, v, page)
+    assert np.array_equal(dev.cpu().numpy(), want)

@@ -56,139 +56,220 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float r) {
   return out;
 }
 
-constexpr int kRows = 16;              // rows whose runs a workgroup takes
-constexpr int kWindow = 2 * kRows;     // rows it looks at: a run that begins in the last goes on
-constexpr int kAppendThreads = 16 * kWindow;
-constexpr int kAppendWaves = kAppendThreads / 64;
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+
+// The largest size of a lane's C values, as the bits of a 16-bit type: those of infinities and NaN
+// are above all others.
+template <int C>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&raw)[C / 2]) {
+  ushort2v top = {0, 0};
+#pragma unroll
+  for (int j = 0; j < C / 2; ++j)
+    top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2v, raw[j] & 0x7FFF7FFFu));
+  return top.x > top.y ? top.x : top.y;
+}
+
+template <bool BF16>
+constexpr uint32_t kLargest = BF16 ? 0x477Fu : 0x7BFFu;  // bits of the largest value within +-65504
+
+// The codes of a lane's C values as bytes, four to a dword.  By the reciprocal r of s: x r is within
+// 6e-5 of the quotient (|x / s| <= 127), and the sum with 1.5 2^23 rounds it to a whole number
+// with its byte in the lowest bits; it is the number of rne(x / s) unless x r lies within 2^-12 of a
+// half.  A lane with such a value divides, and so do those with a scale so small that r may be no
+// number (r = NaN) or with values past +-65504.
+template <int C, bool BF16>
+__device__ __forceinline__ void codes_of(const uint32_t (&raw)[C / 2], bool within, float s, float r, uint32_t (&w)[C / 4]) {
+  constexpr float kWhole = 12582912.0f + kKv8Zero;
+  uint32_t c[C];
+  float off = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const float t = up<BF16>(raw[j / 2] >> (16 * (j % 2)) & 0xFFFFu) * r, sum = t + kWhole;
+    off = fmaxf(off, fabsf(t - (sum - kWhole)));
+    c[j] = __float_as_uint(sum);
+  }
+  if (!(within && r == r && off <= 0.5f - 0x1p-12f)) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const float x = finite(up<BF16>(raw[j / 2] >> (16 * (j % 2)) & 0xFFFFu));
+      c[j] = code_byte(s > 0.0f ? fminf(fmaxf(__builtin_rintf(x / s), -127.0f), 127.0f) : 0.0f);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < C / 4; ++j)
+    w[j] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[4 * j + 3], c[4 * j + 2], 0x0C0C0400u),
+                                 __builtin_amdgcn_perm(c[4 * j + 1], c[4 * j], 0x0C0C0400u), 0x05040100u);
+}
+
+constexpr int64_t kFewRows = 4096;  // rows times heads
 
 // A row begins a piece of a run if the row before it is of another run (or of none, or not
-// before it in the run).  A workgroup takes the pieces that begin in its 16 rows; 16 lanes
-// hold a row, then a wave each writes the whole runs: the codes held before, rounded again
-// where the scale grew, and the new ones between them.
-template <int D, bool BF16>
-__global__ __launch_bounds__(kAppendThreads) void kv8_append_kernel(Kv8Args a) {
-  constexpr int C = D / 16, U = D / 64;  // channels of a lane; 1024-byte units of a run
+// before it in the run).  A workgroup takes the pieces that begin in its ROWS rows and looks at 16
+// rows more, where the last ones end.  16 lanes hold a row until its codes are in LDS; then a wave
+// each writes the 1024-byte units of the runs: what was held, rounded again where the scale
+// grew, with the new codes in their places.  Values go to LDS in the order of channels 16 j + n
+// -> 4 n + j, so that a unit's lane has its four channels of a token in one dword.
+template <int D, int ROWS, bool BF16>
+__global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Args a) {
+  constexpr int C = D / 16, U = D / 64;  // channels of a lane; units of a run's keys or values
+  constexpr int kWindow = ROWS + kKv8Run, kWaves = kWindow / 4, kBatch = 4;
+  static_assert(kWindow % 4 == 0 && kWindow <= 64, "a lane for each row");
   __shared__ __attribute__((aligned(16))) uint8_t codes[2][kWindow][D];
-  __shared__ float tops[2][kWindow];
+  __shared__ float tops[2][kWindow], scales[2][kWindow][2];            // of a piece's first row: held, new
+  __shared__ __attribute__((aligned(16))) int8_t rows[kWindow][kKv8Run];  // and the rows of the run's places
   const int lane = threadIdx.x & 63, i = threadIdx.x & 15, quarter = threadIdx.x >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t group = blockIdx.x / a.heads, head = blockIdx.x - group * a.heads;
-  const int32_t row0 = group * kRows, row = row0 + quarter;
+  const int32_t row0 = group * ROWS, row = row0 + quarter;
   const uint32_t tokens = (uint32_t)a.pages * (uint32_t)a.page;
 
-  // The window's rows, a lane each: bit r of `live`: row r has a slot; of `begins`: it begins a piece.
-  const int32_t mine = row0 + (lane & (kWindow - 1));
-  const int32_t slot = mine < a.T ? a.slots[mine] : -1, prev = mine > 0 && mine <= a.T ? a.slots[mine - 1] : -1;
-  const bool has = (uint32_t)slot < tokens, had = (uint32_t)prev < tokens;
-  const uint32_t live = (uint32_t)__ballot(has);
-  const uint32_t begins = (uint32_t)__ballot(has && !(had && prev / kKv8Run == slot / kKv8Run && prev < slot));
-  // the row that begins the piece of row r, or -1: before this window
-  auto head_of = [&](int r) {
-    const uint32_t before = begins & (0xFFFFFFFFu >> (kWindow - 1 - r));
-    return before ? 31 - __builtin_clz(before) : -1;
-  };
-  const int lead = live >> quarter & 1 ? head_of(quarter) : -1;
-  const bool take = lead >= 0 && lead < kRows;
-
   alignas(16) uint32_t raw[2][C / 2];
-  float x[2][C];
-  if (take) {
+  auto load = [&]() __attribute__((always_inline)) {
     copy16<C>(reinterpret_cast<uint16_t *>(raw[0]), a.k + (int64_t)row * a.ldk + (int64_t)head * D + i * C);
     copy16<C>(reinterpret_cast<uint16_t *>(raw[1]), a.v + (int64_t)row * a.ldv + (int64_t)head * D + i * C);
-  }
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      x[z][j] = take ? finite(up<BF16>(raw[z][j / 2] >> (16 * (j % 2)) & 0xFFFFu)) : 0.0f;
-      top = fmaxf(top, fabsf(x[z][j]));
-    }
-    top = quarter_max(top);
-    if (i == 0) tops[z][quarter] = top;
-  }
-  __syncthreads();
+  };
+  if (quarter < ROWS && row < a.T) load();  // beside the slots, not after them
 
-  // Where a run is, and its scale before and after.  Rows of a piece: from `first` on.
-  auto block_of = [&](int32_t s) { return a.cache + ((int64_t)(s >> a.page_log2) * a.heads + head) * mixllm::kv8_block_bytes(a.page, D); };
+  // The window's rows, a lane each: bit r of `live`: row r has a slot; of `begins`: it begins a piece.
+  const int32_t mine = row0 + lane;
+  const int32_t slot = lane < kWindow && mine < a.T ? a.slots[mine] : -1;
+  const int32_t prev = lane < kWindow && mine > 0 && mine <= a.T ? a.slots[mine - 1] : -1;
+  const bool has = (uint32_t)slot < tokens, had = (uint32_t)prev < tokens;
+  const uint64_t live = __ballot(has);
+  const uint64_t begins = __ballot(has && !(had && prev / kKv8Run == slot / kKv8Run && prev < slot));
+  rows[quarter][i] = -1;
+  // the row that begins the piece of row r, or -1: before this window
+  auto head_of = [&](int r) {
+    const uint64_t before = begins & (~0ull >> (63 - r));
+    return before ? 63 - __builtin_clzll(before) : -1;
+  };
   auto end_of = [&](int first) {  // the row behind the piece
-    const uint32_t after = first < kWindow - 1 ? (begins | ~live) & (0xFFFFFFFEu << first) : 0;
-    return after ? __builtin_ctz(after) : kWindow;
+    const uint64_t after = (begins | ~live) & (~1ull << first);
+    return after ? __builtin_ctzll(after) : 64;
   };
-  auto held_of = [&](const uint8_t *blk, int32_t s, int z) {
-    const float old = s % kKv8Run ? reinterpret_cast<const float *>(blk + mixllm::kv8_scale_offset(a.page, D))[(s & (a.page - 1)) / kKv8Run * 2 + z] : 0.0f;
-    return old > 0.0f && old < INFINITY ? old : 0.0f;
+  const int lead = live >> quarter & 1 ? head_of(quarter) : -1;
+  const bool take = lead >= 0 && lead < ROWS;
+  const int32_t slot0 = __shfl(slot, take ? lead : 0), own = __shfl(slot, quarter);  // every lane takes part
+
+  auto block_of = [&](int32_t s) {
+    return a.cache + ((int64_t)(s >> a.page_log2) * a.heads + head) * mixllm::kv8_block_bytes(a.page, D);
   };
-  auto top_of = [&](int first, int end, int z) {
-    float top = 0.0f;
-    for (int r = first; r < end && r < first + kKv8Run; ++r) top = fmaxf(top, tops[z][r]);
-    return top;
+  auto scales_of = [&](int32_t s) {
+    return reinterpret_cast<float *>(block_of(s) + mixllm::kv8_scale_offset(a.page, D)) + (s & (a.page - 1)) / kKv8Run * 2;
+  };
+  if (quarter >= ROWS && take) load();
+  // A wave's jobs: units job = (piece, keys or values, unit), every kWaves-th, kBatch of them at a
+  // time.  The first batch's held units are on their way before anything is computed.
+  const uint64_t pieces = begins & ((1ull << ROWS) - 1);
+  const int jobs = __builtin_popcountll(pieces) * (2 * U);
+  auto first_of = [&](int piece) {
+    uint64_t left = pieces;
+    for (; piece > 0; --piece) left &= left - 1;
+    return __builtin_ctzll(left);
+  };
+  auto unit_of = [&](int first, int part) {  // part: unit of the keys, then of the values
+    const int32_t s0 = __builtin_amdgcn_readlane(slot, first);
+    return reinterpret_cast<uint4 *>(block_of(s0) + part / U * a.page * D + (s0 & (a.page - 1)) / kKv8Run * (kKv8Run * D) +
+                                     part % U * 1024) + lane;
+  };
+  uint4 old[kBatch];
+  auto fetch = [&](int job0) {
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int job = job0 + e * kWaves;
+      old[e] = make_uint4(0, 0, 0, 0);
+      if (job >= jobs) continue;
+      const int first = first_of(job / (2 * U));
+      if (__builtin_amdgcn_readlane(slot, first) % kKv8Run) old[e] = *unit_of(first, job % (2 * U));
+    }
   };
 
-  const int32_t s0_of_mine = __shfl(slot, take ? lead : 0);  // every lane takes part
+  fetch(wave);
+  float held[2] = {0.0f, 0.0f};
+  if (take && slot0 % kKv8Run) held[0] = scales_of(slot0)[0], held[1] = scales_of(slot0)[1];
+  bool within[2] = {true, true};
   if (take) {
-    const int32_t s0 = s0_of_mine;
-    const uint8_t *blk = block_of(s0);
-    const int end = end_of(lead);
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const float s = fmaxf(held_of(blk, s0, z), top_of(lead, end, z) / 127.0f);
+      const uint32_t bits = largest<C>(raw[z]);
+      within[z] = bits <= kLargest<BF16>;
+      float top = up<BF16>(bits);
+      if (!within[z]) {
+        top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const float c = s > 0.0f ? fminf(fmaxf(__builtin_rintf(x[z][j] / s), -127.0f), 127.0f) : 0.0f;
-        codes[z][quarter][i * C + j] = (uint8_t)code_byte(c);
+        for (int j = 0; j < C; ++j) top = fmaxf(top, fabsf(finite(up<BF16>(raw[z][j / 2] >> (16 * (j % 2)) & 0xFFFFu))));
+      }
+      top = quarter_max(top);
+      if (i == 0) tops[z][quarter] = top;
+    }
+  }
+  __syncthreads();
+  if (take) {
+    const int end = end_of(lead);
+    if (i == 0) rows[lead][own % kKv8Run] = (int8_t)quarter;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const float top = quarter_max(lead + i < end ? tops[z][lead + i] : 0.0f);  // 16 rows at most, a lane each
+      const float was = held[z] > 0.0f && held[z] < INFINITY ? held[z] : 0.0f, s = fmaxf(was, top / 127.0f);
+      if (i == 0 && quarter == lead) scales[z][lead][0] = was, scales[z][lead][1] = s;
+      const float r = s >= 0x1p-100f ? __builtin_amdgcn_rcpf(s) : NAN;
+      uint32_t w[C / 4];
+      codes_of<C, BF16>(raw[z], within[z], s, r, w);
+#pragma unroll
+      for (int j = 0; j < C / 4; ++j) {
+        if (z == 0) {
+          reinterpret_cast<uint32_t *>(&codes[0][quarter][i * C])[j] = w[j];
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int ch = i * C + 4 * j + b;
+            codes[1][quarter][ch / 64 * 64 + ch % 16 * 4 + ch / 16 % 4] = (uint8_t)(w[j] >> (8 * b));
+          }
+        }
       }
     }
   }
   __syncthreads();
 
-  const int n = lane & 15, c = lane >> 4;
-  int piece = 0;
-  for (uint32_t left = begins & ((1u << kRows) - 1); left; left &= left - 1, ++piece) {
-    if (piece % kAppendWaves != wave) continue;
-    const int first = __builtin_ctz(left), end = end_of(first);
-    const int32_t s0 = __builtin_amdgcn_readlane(slot, first);
-    uint8_t *blk = block_of(s0);
-    // the row of each place of the run, or -1: lane t < 16 looks for place t
-    int from = -1;
-    for (int r = first; r < end && r < first + kKv8Run; ++r)
-      if (__builtin_amdgcn_readlane(slot, r) % kKv8Run == n) from = r;
-    float *scales = reinterpret_cast<float *>(blk + mixllm::kv8_scale_offset(a.page, D)) + (s0 & (a.page - 1)) / kKv8Run * 2;
-    const int32_t at = (s0 & (a.page - 1)) / kKv8Run * (kKv8Run * D);
+  const int n = lane & 15, q = lane >> 4;
+  for (int job0 = wave; job0 < jobs; job0 += kBatch * kWaves) {
+    if (job0 != wave) fetch(job0);
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const float old = held_of(blk, s0, z), s = fmaxf(old, top_of(first, end, z) / 127.0f);
-      const float r = s > 0.0f ? old / s : 0.0f;
-      uint8_t *run = blk + z * a.page * D + at;
-      if (lane == 0) scales[z] = s;
+    for (int e = 0; e < kBatch; ++e) {
+      const int job = job0 + e * kWaves;
+      if (job >= jobs) break;
+      const int first = first_of(job / (2 * U)), part = job % (2 * U), z = part / U, u = part % U;
+      const float was = scales[z][first][0], s = scales[z][first][1], r = s > 0.0f ? was / s : 0.0f;
+      uint32_t w[4] = {old[e].x, old[e].y, old[e].z, old[e].w};
+      if (r != 1.0f) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint4 *unit = reinterpret_cast<uint4 *>(run + u * 1024) + lane;
-        uint4 held = make_uint4(0, 0, 0, 0);
-        if (s0 % kKv8Run) held = *unit;
-        uint32_t w[4] = {held.x, held.y, held.z, held.w};
-        if (r != 1.0f) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = rescaled(w[j], r);
-        }
-        if (z == 0) {  // 16 channels of token n
-          if (from >= 0) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(&codes[0][from][64 * u + 16 * c]);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-          }
-        } else {  // tokens 4c .. 4c+3 of the channels 16 j + n
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int src = __shfl(from, 4 * c + t);
-            if (src >= 0) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = (w[j] & ~(0xFFu << (8 * t))) | (uint32_t)codes[1][src][64 * u + 16 * j + n] << (8 * t);
-            }
-          }
-        }
-        *unit = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) w[j] = r == 0.0f ? kKv8Zero * 0x01010101u : rescaled(w[j], r);
       }
+      if (z == 0) {  // 16 channels of token n
+        const int from = rows[first][n];
+        if (from >= 0) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(&codes[0][from][64 * u + 16 * q]);
+          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
+      } else {  // tokens 4q .. 4q+3 of the channels 16 j + n
+        const uint32_t from = *reinterpret_cast<const uint32_t *>(&rows[first][4 * q]);
+        uint32_t v[4], keep = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int at = (int8_t)(from >> (8 * t));
+          v[t] = at < 0 ? 0u : *reinterpret_cast<const uint32_t *>(&codes[1][at][64 * u + 4 * n]);
+          keep |= at < 0 ? 0xFFu << (8 * t) : 0u;
+        }
+        // 4 tokens x 4 channels of bytes, turned
+        const uint32_t a0 = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u), a1 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
+        const uint32_t b0 = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u), b1 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602u);
+        const uint32_t t0 = __builtin_amdgcn_perm(b0, a0, 0x05040100u), t1 = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+        const uint32_t t2 = __builtin_amdgcn_perm(b1, a1, 0x05040100u), t3 = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+        w[0] = (w[0] & keep) | (t0 & ~keep), w[1] = (w[1] & keep) | (t1 & ~keep);
+        w[2] = (w[2] & keep) | (t2 & ~keep), w[3] = (w[3] & keep) | (t3 & ~keep);
+      }
+      *unit_of(first, part) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (u == 0 && lane == 0) scales_of(__builtin_amdgcn_readlane(slot, first))[z] = s;
     }
   }
 }
@@ -246,7 +327,7 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
   const int st = mixllm::kv8_check_cache(cache, cache_bytes, pages, page, heads, dim);
   if (st != MIXLLM_OK) return st;
   const int64_t width = (int64_t)heads * dim;
-  // a launch has fewer than 2^32 threads, 512 for 16 rows of a head
+  // a launch has fewer than 2^32 threads, 512 for 16 rows of a head at most
   if (heads > 65535 || ((int64_t)T + 15) / 16 * heads >= 1 << 23) return MIXLLM_E_SHAPE;
   if (ldk < width || ldv < width || ldk % 8 != 0 || ldv % 8 != 0) return MIXLLM_E_SHAPE;
   if (!k || !v || !slots) return MIXLLM_E_NULL;
@@ -254,16 +335,23 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
   return MIXLLM_OK;
 }
 
+template <int D, int ROWS>
+void launch_append(const Kv8Args &a, int32_t dtype, hipStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.T + ROWS - 1) / ROWS * a.heads)), block(16 * (ROWS + kKv8Run));  // heads of the same rows together
+  if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, false>), grid, block, 0, s, a);
+}
+
 template <bool APPEND, int D>
 void launch_tokens(const Kv8Args &a, int32_t dtype, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16 * a.heads));  // heads of the same rows together
   if (APPEND) {
-    if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_append_kernel<D, true>), grid, dim3(kAppendThreads), 0, s, a);
-    else hipLaunchKernelGGL((kv8_append_kernel<D, false>), grid, dim3(kAppendThreads), 0, s, a);
-  } else {
-    if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_read_kernel<D, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((kv8_read_kernel<D, false>), grid, dim3(256), 0, s, a);
+    if ((int64_t)a.T * a.heads <= kFewRows) launch_append<D, 4>(a, dtype, s);
+    else launch_append<D, 16>(a, dtype, s);
+    return;
   }
+  const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16 * a.heads));
+  if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_read_kernel<D, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv8_read_kernel<D, false>), grid, dim3(256), 0, s, a);
 }
 
 template <bool APPEND>
