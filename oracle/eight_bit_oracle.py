@@ -8,6 +8,8 @@ the float32 values they stand for.
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 
 RUN = 16
@@ -39,6 +41,12 @@ def head_norm_rotate(x, pos, inv_freq, norm=None, eps=1e-6, neighbours=False):
 
 def block_bytes(page, dim):
     return 2 * page * dim + -(-(page // 2) // 128) * 128
+
+
+@functools.lru_cache(maxsize=None)
+def run_bytes(part, dim):
+    """Places of a run's codes, [16, dim]."""
+    return np.array([[code_byte(part, t, ch) for ch in range(dim)] for t in range(RUN)])
 
 
 def code_byte(part, t, ch):
@@ -80,7 +88,7 @@ def kv8_write(cache, slots, k, v, page):
                 old = held if 0 not in places and np.isfinite(held) and held > 0 else np.float32(0)
                 new = max(old, np.abs(x).max() / np.float32(127))
                 ratio = old / new if new > 0 else np.float32(0)
-                at = np.array([[code_byte(part, t, ch) for ch in range(dim)] for t in range(RUN)])
+                at = run_bytes(part, dim)
                 c = codes[at].astype(np.float32) - np.float32(128)
                 if 0 in places:
                     c = np.zeros_like(c)

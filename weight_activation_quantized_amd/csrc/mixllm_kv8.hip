@@ -101,7 +101,10 @@ __device__ __forceinline__ void codes_of(const uint32_t (&raw)[C / 2], bool with
                                  __builtin_amdgcn_perm(c[4 * j + 1], c[4 * j], 0x0C0C0400u), 0x05040100u);
 }
 
-constexpr int64_t kFewRows = 4096;  // rows times heads
+// Rows times heads up to which a workgroup takes 4 rows, and not 16 by half as many lanes (us, 8 heads of
+// 128): 64 rows of as many requests 6.5 (9.0 with 16), 700 15.5 (23.6); 1500 of one prompt 15.7 (7.7),
+// 6961 of four 52 (18.8).
+constexpr int64_t kFewRows = 8192;
 
 // A row begins a piece of a run if the row before it is of another run (or of none, or not
 // before it in the run).  A workgroup takes the pieces that begin in its ROWS rows and looks at 16
@@ -109,26 +112,30 @@ constexpr int64_t kFewRows = 4096;  // rows times heads
 // each writes the 1024-byte units of the runs: what was held, rounded again where the scale
 // grew, with the new codes in their places.  Values go to LDS in the order of channels 16 j + n
 // -> 4 n + j, so that a unit's lane has its four channels of a token in one dword.
-template <int D, int ROWS, bool BF16>
-__global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Args a) {
+template <int D, int ROWS, int EACH, bool BF16>
+__global__ __launch_bounds__(16 * (ROWS + kKv8Run) / EACH) void kv8_append_kernel(Kv8Args a) {
   constexpr int C = D / 16, U = D / 64;  // channels of a lane; units of a run's keys or values
-  constexpr int kWindow = ROWS + kKv8Run, kWaves = kWindow / 4, kBatch = 4;
-  static_assert(kWindow % 4 == 0 && kWindow <= 64, "a lane for each row");
+  constexpr int kWindow = ROWS + kKv8Run, kQuarters = kWindow / EACH, kWaves = kQuarters / 4, kBatch = 4;
+  static_assert(kQuarters * EACH == kWindow && kWaves * 4 == kQuarters && kWindow <= 64, "a lane for each row");
   __shared__ __attribute__((aligned(16))) uint8_t codes[2][kWindow][D];
   __shared__ float tops[2][kWindow], scales[2][kWindow][2];            // of a piece's first row: held, new
   __shared__ __attribute__((aligned(16))) int8_t rows[kWindow][kKv8Run];  // and the rows of the run's places
   const int lane = threadIdx.x & 63, i = threadIdx.x & 15, quarter = threadIdx.x >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t group = blockIdx.x / a.heads, head = blockIdx.x - group * a.heads;
-  const int32_t row0 = group * ROWS, row = row0 + quarter;
+  const int32_t row0 = group * ROWS;
   const uint32_t tokens = (uint32_t)a.pages * (uint32_t)a.page;
+  auto row_of = [&](int y) { return quarter + y * kQuarters; };  // this quarter's rows of the window
 
-  alignas(16) uint32_t raw[2][C / 2];
-  auto load = [&]() __attribute__((always_inline)) {
-    copy16<C>(reinterpret_cast<uint16_t *>(raw[0]), a.k + (int64_t)row * a.ldk + (int64_t)head * D + i * C);
-    copy16<C>(reinterpret_cast<uint16_t *>(raw[1]), a.v + (int64_t)row * a.ldv + (int64_t)head * D + i * C);
+  alignas(16) uint32_t raw[EACH][2][C / 2];
+  auto load = [&](int y) __attribute__((always_inline)) {
+    const int64_t row = row0 + row_of(y);
+    copy16<C>(reinterpret_cast<uint16_t *>(raw[y][0]), a.k + row * a.ldk + (int64_t)head * D + i * C);
+    copy16<C>(reinterpret_cast<uint16_t *>(raw[y][1]), a.v + row * a.ldv + (int64_t)head * D + i * C);
   };
-  if (quarter < ROWS && row < a.T) load();  // beside the slots, not after them
+#pragma unroll
+  for (int y = 0; y < EACH; ++y)
+    if (row_of(y) < ROWS && row0 + row_of(y) < a.T) load(y);  // beside the slots, not after them
 
   // The window's rows, a lane each: bit r of `live`: row r has a slot; of `begins`: it begins a piece.
   const int32_t mine = row0 + lane;
@@ -137,7 +144,6 @@ __global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Ar
   const bool has = (uint32_t)slot < tokens, had = (uint32_t)prev < tokens;
   const uint64_t live = __ballot(has);
   const uint64_t begins = __ballot(has && !(had && prev / kKv8Run == slot / kKv8Run && prev < slot));
-  rows[quarter][i] = -1;
   // the row that begins the piece of row r, or -1: before this window
   auto head_of = [&](int r) {
     const uint64_t before = begins & (~0ull >> (63 - r));
@@ -147,9 +153,16 @@ __global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Ar
     const uint64_t after = (begins | ~live) & (~1ull << first);
     return after ? __builtin_ctzll(after) : 64;
   };
-  const int lead = live >> quarter & 1 ? head_of(quarter) : -1;
-  const bool take = lead >= 0 && lead < ROWS;
-  const int32_t slot0 = __shfl(slot, take ? lead : 0), own = __shfl(slot, quarter);  // every lane takes part
+  int lead[EACH];
+  bool take[EACH];
+  int32_t slot0[EACH], own[EACH];
+#pragma unroll
+  for (int y = 0; y < EACH; ++y) {
+    rows[row_of(y)][i] = -1;
+    lead[y] = live >> row_of(y) & 1 ? head_of(row_of(y)) : -1;
+    take[y] = lead[y] >= 0 && lead[y] < ROWS;
+    slot0[y] = __shfl(slot, take[y] ? lead[y] : 0), own[y] = __shfl(slot, row_of(y));  // every lane takes part
+  }
 
   auto block_of = [&](int32_t s) {
     return a.cache + ((int64_t)(s >> a.page_log2) * a.heads + head) * mixllm::kv8_block_bytes(a.page, D);
@@ -157,7 +170,13 @@ __global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Ar
   auto scales_of = [&](int32_t s) {
     return reinterpret_cast<float *>(block_of(s) + mixllm::kv8_scale_offset(a.page, D)) + (s & (a.page - 1)) / kKv8Run * 2;
   };
-  if (quarter >= ROWS && take) load();
+  float held[EACH][2];
+#pragma unroll
+  for (int y = 0; y < EACH; ++y) {
+    if (row_of(y) >= ROWS && take[y]) load(y);
+    held[y][0] = held[y][1] = 0.0f;
+    if (take[y] && slot0[y] % kKv8Run) held[y][0] = scales_of(slot0[y])[0], held[y][1] = scales_of(slot0[y])[1];
+  }
   // A wave's jobs: units job = (piece, keys or values, unit), every kWaves-th, kBatch of them at a
   // time.  The first batch's held units are on their way before anything is computed.
   const uint64_t pieces = begins & ((1ull << ROWS) - 1);
@@ -183,47 +202,50 @@ __global__ __launch_bounds__(16 * (ROWS + kKv8Run)) void kv8_append_kernel(Kv8Ar
       if (__builtin_amdgcn_readlane(slot, first) % kKv8Run) old[e] = *unit_of(first, job % (2 * U));
     }
   };
-
   fetch(wave);
-  float held[2] = {0.0f, 0.0f};
-  if (take && slot0 % kKv8Run) held[0] = scales_of(slot0)[0], held[1] = scales_of(slot0)[1];
-  bool within[2] = {true, true};
-  if (take) {
+
+  bool within[EACH][2];
+#pragma unroll
+  for (int y = 0; y < EACH; ++y) {
+    within[y][0] = within[y][1] = true;
+    if (!take[y]) continue;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const uint32_t bits = largest<C>(raw[z]);
-      within[z] = bits <= kLargest<BF16>;
+      const uint32_t bits = largest<C>(raw[y][z]);
+      within[y][z] = bits <= kLargest<BF16>;
       float top = up<BF16>(bits);
-      if (!within[z]) {
+      if (!within[y][z]) {
         top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; ++j) top = fmaxf(top, fabsf(finite(up<BF16>(raw[z][j / 2] >> (16 * (j % 2)) & 0xFFFFu))));
+        for (int j = 0; j < C; ++j) top = fmaxf(top, fabsf(finite(up<BF16>(raw[y][z][j / 2] >> (16 * (j % 2)) & 0xFFFFu))));
       }
       top = quarter_max(top);
-      if (i == 0) tops[z][quarter] = top;
+      if (i == 0) tops[z][row_of(y)] = top;
     }
   }
   __syncthreads();
-  if (take) {
-    const int end = end_of(lead);
-    if (i == 0) rows[lead][own % kKv8Run] = (int8_t)quarter;
+#pragma unroll
+  for (int y = 0; y < EACH; ++y) {
+    if (!take[y]) continue;
+    const int row = row_of(y), end = end_of(lead[y]);
+    if (i == 0) rows[lead[y]][own[y] % kKv8Run] = (int8_t)row;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const float top = quarter_max(lead + i < end ? tops[z][lead + i] : 0.0f);  // 16 rows at most, a lane each
-      const float was = held[z] > 0.0f && held[z] < INFINITY ? held[z] : 0.0f, s = fmaxf(was, top / 127.0f);
-      if (i == 0 && quarter == lead) scales[z][lead][0] = was, scales[z][lead][1] = s;
+      const float top = quarter_max(lead[y] + i < end ? tops[z][lead[y] + i] : 0.0f);  // 16 rows at most, a lane each
+      const float was = held[y][z] > 0.0f && held[y][z] < INFINITY ? held[y][z] : 0.0f, s = fmaxf(was, top / 127.0f);
+      if (i == 0 && row == lead[y]) scales[z][row][0] = was, scales[z][row][1] = s;
       const float r = s >= 0x1p-100f ? __builtin_amdgcn_rcpf(s) : NAN;
       uint32_t w[C / 4];
-      codes_of<C, BF16>(raw[z], within[z], s, r, w);
+      codes_of<C, BF16>(raw[y][z], within[y][z], s, r, w);
 #pragma unroll
       for (int j = 0; j < C / 4; ++j) {
         if (z == 0) {
-          reinterpret_cast<uint32_t *>(&codes[0][quarter][i * C])[j] = w[j];
+          reinterpret_cast<uint32_t *>(&codes[0][row][i * C])[j] = w[j];
         } else {
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int ch = i * C + 4 * j + b;
-            codes[1][quarter][ch / 64 * 64 + ch % 16 * 4 + ch / 16 % 4] = (uint8_t)(w[j] >> (8 * b));
+            codes[1][row][ch / 64 * 64 + ch % 16 * 4 + ch / 16 % 4] = (uint8_t)(w[j] >> (8 * b));
           }
         }
       }
@@ -335,18 +357,18 @@ int check_tokens(const void *k, const void *v, int64_t ldk, int64_t ldv, int32_t
   return MIXLLM_OK;
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int EACH>
 void launch_append(const Kv8Args &a, int32_t dtype, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.T + ROWS - 1) / ROWS * a.heads)), block(16 * (ROWS + kKv8Run));  // heads of the same rows together
-  if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, false>), grid, block, 0, s, a);
+  const dim3 grid((unsigned)(((int64_t)a.T + ROWS - 1) / ROWS * a.heads)), block(16 * (ROWS + kKv8Run) / EACH);  // heads of the same rows together
+  if (dtype == MIXLLM_BF16) hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, EACH, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((kv8_append_kernel<D, ROWS, EACH, false>), grid, block, 0, s, a);
 }
 
 template <bool APPEND, int D>
 void launch_tokens(const Kv8Args &a, int32_t dtype, hipStream_t s) {
   if (APPEND) {
-    if ((int64_t)a.T * a.heads <= kFewRows) launch_append<D, 4>(a, dtype, s);
-    else launch_append<D, 16>(a, dtype, s);
+    if ((int64_t)a.T * a.heads <= kFewRows) launch_append<D, 4, 1>(a, dtype, s);
+    else launch_append<D, 16, 2>(a, dtype, s);
     return;
   }
   const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16 * a.heads));

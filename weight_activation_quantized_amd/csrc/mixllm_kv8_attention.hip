@@ -341,21 +341,309 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kern
   }
 }
 
+// Many rows (prompts): a wave takes 32 rows over all tokens of the workgroup's chunk, and the
+// workgroup's waves share the codes, made fp16 once and kept in LDS, 64 or 32 tokens at a time in
+// two stages.  32 x 32 x 16 instructions: S^T leaves in lane (n, c), c = 0 or 1, row n's scores of the
+// tokens 8 (i / 4) + 4 c + i % 4 of 32, so the eight of a run are the operand of one step of the
+// second product, if the values lie in LDS in that order.  Rows of both stages' arrays are turned
+// by 16-byte units so that 16 lanes read 16 different banks' worth.
+template <int D>
+struct Many {
+  static constexpr int kWaves = D == 256 ? 4 : 8, kThreads = 64 * kWaves, kRows = 32 * kWaves;
+  static constexpr int kStep = D == 256 ? 32 : 64, kRuns = kStep / kRun, kBatch = 64 / kRuns;
+  static constexpr int U = D / 64, kBlocks = 2 * kRuns * U / kWaves;  // 1024-byte units of a step for each wave
+  static constexpr int kKeys = kStep * D * 2, kStage = 2 * kKeys;     // bytes
+  static constexpr int kKeyUnits = D / 8;                             // 16-byte units of a token's keys
+  static __device__ __forceinline__ int key_turn(int token) { return D == 64 ? (token >> 1) & 7 : token & 15; }
+  static constexpr int kValueUnits = 2 * kRuns;                       // of a channel's values
+  static __device__ __forceinline__ int value_turn(int ch) { return kRuns == 4 ? (ch >> 1) & 7 : (ch >> 2) & 3; }
+};
+
+__device__ __forceinline__ float halves_max(float v) {
+  const uint2v a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a.x), __uint_as_float(a.y));
+}
+
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_many_kernel(Args a) {
+  using M = Many<D>;
+  constexpr int U = M::U, E = D / 16, J = D / 32, R = M::kRuns;
+  constexpr int kParts = BF16 ? 1 : 2;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * M::kStage];
+
+  const int lane = threadIdx.x & 63, n = lane & 31, c = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, b = blockIdx.z;
+  const int32_t rt = a.tiles - 1 - (int32_t)blockIdx.y;
+  const Tile t = tile_of(a, b, h, rt);
+  if (t.rows <= 0) return;
+  const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
+  if (split >= nchunks && !(split == 0 && a.splits == 1)) return;
+  const int32_t begin = base_of(t) + split * chunk;
+  const int32_t from = begin > t.lo ? begin : t.lo;
+  const int32_t to = t.hi - begin > chunk ? begin + chunk : t.hi;
+  const int32_t start = from & ~(kRun - 1), steps = to > start ? (to - start + M::kStep - 1) / M::kStep : 0;
+
+  const int32_t P = 1 << a.page_log2, block = mixllm::kv8_block_bytes(P, D);
+  const int32_t *table = a.table + b * a.ldt;
+
+  // Pages and scales of kBatch steps at a time, a run a lane.
+  struct Batch {
+    int32_t pages;
+    float ks, vs;
+    uint64_t there;
+  } now = {-1, 0.0f, 0.0f, 0}, next = now;
+  auto fetch = [&](int32_t j) {
+    const int32_t tok = start + j * M::kStep + lane * kRun;
+    next.pages = tok < to ? table[tok >> a.page_log2] : -1;
+    next.pages = (uint32_t)next.pages < (uint32_t)a.pages ? next.pages : -1;
+    next.there = __ballot(next.pages >= 0);
+    next.ks = next.vs = 0.0f;
+    if (next.pages >= 0) {
+      const float2v s = *reinterpret_cast<const float2v *>(a.cache + ((int64_t)next.pages * a.hkv + h) * block +
+                                                           mixllm::kv8_scale_offset(P, D) + (tok & (P - 1)) / kRun * 8);
+      next.ks = s.x, next.vs = s.y;
+    }
+  };
+  // This wave's units of step j: blocks wave, wave + kWaves, .. of the step's keys, then values.
+  uint4v raw[M::kBlocks];
+  auto load = [&](int32_t j) __attribute__((always_inline)) {
+    if (j % M::kBatch == 0) fetch(j);
+#pragma unroll
+    for (int i = 0; i < M::kBlocks; ++i) {
+      const int ub = wave + i * M::kWaves, part = ub / (R * U), r = ub % (R * U) / U, u = ub % U;
+      const int32_t pg = __builtin_amdgcn_readlane(next.pages, j % M::kBatch * R + r);
+      const int32_t in = (start + j * M::kStep + kRun * r) & (P - 1);
+      // an absent run reads any memory of the cache; its scores are masked
+      raw[i] = *reinterpret_cast<const uint4v *>(a.cache + ((int64_t)(pg < 0 ? 0 : pg) * a.hkv + h) * block +
+                                                 (int64_t)part * P * D + (int64_t)in * D + u * 1024 + lane * 16);
+    }
+  };
+  auto store = [&](int32_t j) __attribute__((always_inline)) {
+    uint8_t *keys = smem + (j & 1) * M::kStage, *values = keys + M::kKeys;
+    const int m = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < M::kBlocks; ++i) {
+      const int ub = wave + i * M::kWaves, part = ub / (R * U), r = ub % (R * U) / U, u = ub % U;
+      const half8 lo = codes8(raw[i].x, raw[i].y), hi = codes8(raw[i].z, raw[i].w);
+      if (part == 0) {  // 16 channels of token m
+        const int token = kRun * r + m, unit = 8 * u + 2 * q, turn = M::key_turn(token);
+        *reinterpret_cast<half8 *>(keys + (token * M::kKeyUnits + (unit ^ turn)) * 16) = lo;
+        *reinterpret_cast<half8 *>(keys + (token * M::kKeyUnits + ((unit + 1) ^ turn)) * 16) = hi;
+      } else {  // tokens 4q .. 4q+3 of the channels 16 j + m
+        const uint4v l4 = __builtin_bit_cast(uint4v, lo), h4 = __builtin_bit_cast(uint4v, hi);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int ch = 64 * u + 16 * jj + m;
+          const uint2v w = jj == 0 ? uint2v{l4.x, l4.y} : jj == 1 ? uint2v{l4.z, l4.w} : jj == 2 ? uint2v{h4.x, h4.y} : uint2v{h4.z, h4.w};
+          *reinterpret_cast<uint2v *>(values + (ch * M::kValueUnits + ((2 * r + (q & 1)) ^ M::value_turn(ch))) * 16 + (q >> 1) * 8) = w;
+        }
+      }
+    }
+  };
+  if (steps > 0) load(0);
+
+  // The wave's query rows, as operands: step e has the channels 16 e + 8 c on.
+  const int32_t first = wave * 32, live = t.rows - first;  // rows of this wave, if positive
+  half8 q[E];
+  float row_scale;
+  int32_t row_hi, row_lo;
+  {
+    const int32_t r = t.row0 + (first + n < t.rows ? first + n : t.rows - 1);
+    const int32_t i = r / a.group, head = h * a.group + r % a.group;
+    const uint16_t *qp = a.q + (int64_t)(t.q0 + i) * a.ldq + (int64_t)head * D + 8 * c;
+    uint4v w[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = *reinterpret_cast<const uint4v *>(qp + 16 * e);
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        top = fmaxf(top, fmaxf(fabsf(up<BF16>(w[e][d] & 0xFFFFu)), fabsf(up<BF16>(w[e][d] >> 16))));
+    top = halves_max(top);
+    int p = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
+    p = p < -100 ? -100 : p;
+    const float mul = ldexpf(1.0f, 14 - p);
+    row_scale = ldexpf(a.scale * kLog2e, p - 14);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        q[e][2 * d] = (_Float16)(up<BF16>(w[e][d] & 0xFFFFu) * mul);
+        q[e][2 * d + 1] = (_Float16)(up<BF16>(w[e][d] >> 16) * mul);
+      }
+    const int32_t pos = t.pos0 + i;
+    row_hi = pos + 1;
+    row_lo = a.window ? pos - a.window + 1 : 0;
+  }
+  // tokens that some row, and that every row of this wave sees
+  const int32_t pos_first = t.pos0 + (t.row0 + first) / a.group;
+  const int32_t pos_last = t.pos0 + (t.row0 + (live < 32 ? t.rows : first + 32) - 1) / a.group;
+  const int32_t any_lo = a.window ? pos_first - a.window + 1 : 0, any_hi = pos_last + 1;
+  const int32_t all_lo = a.window ? pos_last - a.window + 1 : 0, all_hi = pos_first + 1;
+
+  float16v o[J];
+  float ref = kLow, l = 0.0f, limit = kLow, peak = -1000.0f;
+  int32_t shift = -200;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+
+  auto compute = [&](int32_t j) __attribute__((always_inline)) {
+    const int32_t t0 = start + j * M::kStep;
+    if (live <= 0 || t0 >= any_hi || t0 + M::kStep <= any_lo) return;
+    const uint8_t *keys = smem + (j & 1) * M::kStage, *values = keys + M::kKeys;
+    const uint32_t here = (uint32_t)(now.there >> (j % M::kBatch * R)) & ((1u << R) - 1);
+    float16v s[R / 2];
+#pragma unroll
+    for (int x = 0; x < R / 2; ++x) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[x][i] = 0.0f;
+      const int token = 32 * x + n, turn = M::key_turn(token);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const half8 w = *reinterpret_cast<const half8 *>(keys + (token * M::kKeyUnits + ((2 * e + c) ^ turn)) * 16);
+        s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, q[e], s[x], 0, 0, 0);
+      }
+    }
+    float vs[R];
+    int32_t ve[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float f = row_scale * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), j % M::kBatch * R + r));
+      vs[r] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.vs), j % M::kBatch * R + r));
+      ve[r] = vs[r] > 0.0f ? __builtin_amdgcn_frexp_expf(vs[r]) : -1000;  // v < 2^ve
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[r / 2][8 * (r % 2) + i] *= f;
+    }
+    if (!(t0 >= all_lo && t0 >= from && t0 + M::kStep <= all_hi && t0 + M::kStep <= to && here == (1u << R) - 1)) {
+      const int32_t lo = row_lo > from ? row_lo : from, hi = row_hi < to ? row_hi : to;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t tok = t0 + kRun * r + i / 4 * 8 + 4 * c + i % 4;
+          if (!(tok >= lo && tok < hi && (here >> r & 1))) s[r / 2][8 * (r % 2) + i] = -INFINITY;
+        }
+    }
+    float m[R], top = -INFINITY, big = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = s[r / 2][8 * (r % 2)];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m[r] = fmaxf(m[r], s[r / 2][8 * (r % 2) + i]);
+      top = fmaxf(top, m[r]);
+      big = fmaxf(big, m[r] - ref + (float)ve[r]);
+    }
+    if (__any(top > limit || big > (float)shift + kTop)) {
+      const float high = halves_max(top), up_to = high > limit ? high : ref;
+      const float back = ref - up_to;  // kLow stands for no score so far
+      big = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < R; ++r) big = fmaxf(big, m[r] - up_to + (float)ve[r]);
+      peak = fmaxf(peak + back, halves_max(big));
+      const int32_t to_shift = (int32_t)fminf(fmaxf(ceilf(peak), -180.0f), 180.0f) - (int32_t)(kTop - kRoom);
+      const float fl = __builtin_amdgcn_exp2f(back), fo = __builtin_amdgcn_exp2f(back + (float)(shift - to_shift));
+      ref = up_to;
+      limit = up_to + kLazy;
+      shift = to_shift;
+      l *= fl;
+#pragma unroll
+      for (int jj = 0; jj < J; ++jj) o[jj] *= fo;
+    }
+    half8 p[kParts][R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float g = fminf(ldexpf(vs[r], -shift), 0x1p120f);  // where it ends, weights are 0
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __builtin_amdgcn_exp2f(s[r / 2][8 * (r % 2) + i] - ref);
+        l += w;
+        const float x = w * g;
+        p[0][r][i] = (_Float16)x;
+        if (kParts == 2) p[kParts - 1][r][i] = (_Float16)(x - (float)p[0][r][i]);
+      }
+    }
+#pragma unroll
+    for (int jj = 0; jj < J; ++jj) {
+      const int ch = 32 * jj + n, turn = M::value_turn(ch);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const half8 w = *reinterpret_cast<const half8 *>(values + (ch * M::kValueUnits + ((2 * r + c) ^ turn)) * 16);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) o[jj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, p[k][r], o[jj], 0, 0, 0);
+      }
+    }
+  };
+
+  if (steps > 0) store(0);
+  __syncthreads();
+  for (int32_t j = 0; j < steps; ++j) {
+    if (j % M::kBatch == 0) now = next;
+    if (j + 1 < steps) load(j + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(j);
+    if (j + 1 < steps) store(j + 1);
+    __syncthreads();
+  }
+
+  if (n >= live) return;
+  const float sum = [&] {
+    const uint2v v = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    return __uint_as_float(v.x) + __uint_as_float(v.y);
+  }();
+  const int32_t rr = first + n;
+  if (a.splits > 1) {
+    const int64_t place = ((int64_t)(b * a.tiles + rt) * a.hkv + h) * a.splits + split;
+    float *dst = a.ws_o + (place * a.tile_rows + rr) * D;
+#pragma unroll
+    for (int jj = 0; jj < J; ++jj)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float4v v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ldexpf(o[jj][4 * g + i], shift);
+        *reinterpret_cast<float4v *>(dst + 32 * jj + 8 * g + 4 * c) = v;
+      }
+    if (c == 0) *reinterpret_cast<float2v *>(a.ws_ml + (place * a.tile_rows + rr) * 2) = float2v{ref, sum};
+    return;
+  }
+  const int32_t rg = t.row0 + rr, ii = t.q0 + rg / a.group, hh = h * a.group + rg % a.group;
+  const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays NaN
+  uint16_t *dst = a.out + (int64_t)ii * a.ldo + (int64_t)hh * D;
+#pragma unroll
+  for (int jj = 0; jj < J; ++jj)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = down<BF16>(ldexpf(o[jj][4 * g + i], shift) * inv);
+      *reinterpret_cast<uint2v *>(dst + 32 * jj + 8 * g + 4 * c) = uint2v{v[0] | v[1] << 16, v[2] | v[3] << 16};
+    }
+  if (c == 0 && a.lse) a.lse[(int64_t)ii * a.hq + hh] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+}
+
 // How the work of a call is cut.  Rows: tiles of 16 or 32 (row, head) pairs of one key/value
-// head.  Tokens: so many equal chunks of each tile that about kTarget workgroups run at the
-// longest length; 256 CUs hold 2 of them each.
-constexpr int64_t kTarget = 512;
+// head, or of 256 (128 with 256 channels) where there are kMany or more.  Tokens: so many equal
+// chunks of each tile that about kTarget workgroups run at the longest length; 256 CUs hold 2 of
+// them each, or one of the large ones.
+constexpr int64_t kTarget = 512, kMany = 128;
 
 Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
   Cut k;
   const int64_t rows = (int64_t)max_rows * (hq / hkv);
-  k.tile_rows = rows <= 16 || dim == 256 ? 16 : 32;
+  k.tile_rows = rows >= kMany ? (dim == 256 ? 128 : 256) : rows <= 16 || dim == 256 ? 16 : 32;
   k.tiles = (int32_t)((rows + k.tile_rows - 1) / k.tile_rows);
   int64_t span = max_len;
   // a tile's rows are at most tile_rows positions, its first chunk starts at a whole run
   if (window && (int64_t)window + k.tile_rows + kRun < span) span = (int64_t)window + k.tile_rows + kRun;
   const int64_t groups = (int64_t)B * hkv * k.tiles;
-  const int64_t most = (span + kMinChunk - 1) / kMinChunk, want = (kTarget + groups - 1) / groups;
+  const int64_t most = (span + kMinChunk - 1) / kMinChunk;
+  const int64_t want = ((rows >= kMany ? kTarget / 2 : kTarget) + groups - 1) / groups;
   k.splits = (int32_t)(most < 1 || want <= 1 ? 1 : want < most ? want : most);
   return k;
 }
@@ -363,7 +651,9 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
 template <int D, bool BF16>
 void launch(const Args &a, hipStream_t s) {
   const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
-  if (D < 256 && a.tile_rows == 32)
+  if (a.tile_rows > 32)
+    hipLaunchKernelGGL((kv8_many_kernel<D, BF16>), grid, dim3(Many<D>::kThreads), 0, s, a);
+  else if (D < 256 && a.tile_rows == 32)
     hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, BF16>), grid, threads, 0, s, a);
   else hipLaunchKernelGGL((kv8_attention_kernel<D, 1, BF16>), grid, threads, 0, s, a);
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
