@@ -342,8 +342,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kern
 }
 
 // Many rows (prompts): a wave takes 32 rows over all tokens of the workgroup's chunk, and the
-// workgroup's waves share the codes, made fp16 once and kept in LDS, 64 or 32 tokens at a time in
-// two stages.  32 x 32 x 16 instructions: S^T leaves in lane (n, c), c = 0 or 1, row n's scores of the
+// workgroup's waves share the codes, made fp16 once and kept in LDS, 64 or 32 tokens at a time,
+// keys in two stages, values, which are needed later, in three.  32 x 32 x 16 instructions: S^T leaves in lane (n, c), c = 0 or 1, row n's scores of the
 // tokens 8 (i / 4) + 4 c + i % 4 of 32, so the eight of a run are the operand of one step of the
 // second product, if the values lie in LDS in that order.  Rows of both stages' arrays are turned
 // by 16-byte units so that 16 lanes read 16 different banks' worth.
@@ -352,7 +352,8 @@ struct Many {
   static constexpr int kWaves = D == 256 ? 4 : 8, kThreads = 64 * kWaves, kRows = 32 * kWaves;
   static constexpr int kStep = D == 256 ? 32 : 64, kRuns = kStep / kRun, kBatch = 64 / kRuns;
   static constexpr int U = D / 64, kBlocks = 2 * kRuns * U / kWaves;  // 1024-byte units of a step for each wave
-  static constexpr int kKeys = kStep * D * 2, kStage = 2 * kKeys;     // bytes
+  static constexpr int kStage = kStep * D * 2;                        // bytes of a step's keys, or values
+  static constexpr bool kTurns = kWaves == 8;                         // two waves a SIMD, which take turns
   static constexpr int kKeyUnits = D / 8;                             // 16-byte units of a token's keys
   static __device__ __forceinline__ int key_turn(int token) { return D == 64 ? (token >> 1) & 7 : token & 15; }
   static constexpr int kValueUnits = 2 * kRuns;                       // of a channel's values
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
   using M = Many<D>;
   constexpr int U = M::U, E = D / 16, J = D / 32, R = M::kRuns;
   constexpr int kParts = BF16 ? 1 : 2;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * M::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t all_keys[2 * M::kStage], all_values[3 * M::kStage];
 
   const int lane = threadIdx.x & 63, n = lane & 31, c = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
     }
   };
   auto store = [&](int32_t j) __attribute__((always_inline)) {
-    uint8_t *keys = smem + (j & 1) * M::kStage, *values = keys + M::kKeys;
+    uint8_t *keys = all_keys + (j & 1) * M::kStage, *values = all_values + j % 3 * M::kStage;
     const int m = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < M::kBlocks; ++i) {
@@ -443,6 +444,8 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
       }
     }
   };
+  // Group 1 of the waves is half a step behind group 0 (see below) and stores a step further ahead.
+  const int late = M::kTurns && wave >= M::kWaves / 2 ? 1 : 0;
   if (steps > 0) load(0);
 
   // The wave's query rows, as operands: step e has the channels 16 e + 8 c on.
@@ -466,8 +469,8 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
     top = halves_max(top);
     int p = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;
     p = p < -100 ? -100 : p;
-    const float mul = ldexpf(1.0f, 14 - p);
-    row_scale = ldexpf(a.scale * kLog2e, p - 14);
+    const float mul = ldexpf(a.scale < 0.0f ? -1.0f : 1.0f, 14 - p);  // a score's factor is not negative
+    row_scale = ldexpf(fabsf(a.scale) * kLog2e, p - 14);
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
@@ -493,49 +496,74 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
 
-  auto compute = [&](int32_t j) __attribute__((always_inline)) {
+  float16v s[R / 2];
+  half8 p[kParts][R];
+  auto seen = [&](int32_t j) {  // by a row of this wave
     const int32_t t0 = start + j * M::kStep;
-    if (live <= 0 || t0 >= any_hi || t0 + M::kStep <= any_lo) return;
-    const uint8_t *keys = smem + (j & 1) * M::kStage, *values = keys + M::kKeys;
-    const uint32_t here = (uint32_t)(now.there >> (j % M::kBatch * R)) & ((1u << R) - 1);
-    float16v s[R / 2];
+    return live > 0 && t0 < any_hi && t0 + M::kStep > any_lo;
+  };
+  auto multiply = [&](int32_t j) __attribute__((always_inline)) {  // the last step's values, this one's keys
+    if (j > 0 && seen(j - 1)) {
+      const uint8_t *values = all_values + (j - 1) % 3 * M::kStage;
 #pragma unroll
-    for (int x = 0; x < R / 2; ++x) {
+      for (int jj = 0; jj < J; ++jj) {
+        const int ch = 32 * jj + n, turn = M::value_turn(ch);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[x][i] = 0.0f;
-      const int token = 32 * x + n, turn = M::key_turn(token);
+        for (int r = 0; r < R; ++r) {
+          const half8 w = *reinterpret_cast<const half8 *>(values + (ch * M::kValueUnits + ((2 * r + c) ^ turn)) * 16);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const half8 w = *reinterpret_cast<const half8 *>(keys + (token * M::kKeyUnits + ((2 * e + c) ^ turn)) * 16);
-        s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, q[e], s[x], 0, 0, 0);
+          for (int k = 0; k < kParts; ++k) o[jj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, p[k][r], o[jj], 0, 0, 0);
+        }
       }
     }
-    float vs[R];
+    if (j < steps && seen(j)) {
+      const uint8_t *keys = all_keys + (j & 1) * M::kStage;
+#pragma unroll
+      for (int x = 0; x < R / 2; ++x) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[x][i] = 0.0f;
+        const int token = 32 * x + n, turn = M::key_turn(token);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const half8 w = *reinterpret_cast<const half8 *>(keys + (token * M::kKeyUnits + ((2 * e + c) ^ turn)) * 16);
+          s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, q[e], s[x], 0, 0, 0);
+        }
+      }
+    }
+  };
+  auto weigh = [&](int32_t j) __attribute__((always_inline)) {
+    if (!seen(j)) return;
+    const int32_t t0 = start + j * M::kStep;
+    const uint32_t here = (uint32_t)(now.there >> (j % M::kBatch * R)) & ((1u << R) - 1);
+    float f[R], vs[R];
     int32_t ve[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float f = row_scale * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), j % M::kBatch * R + r));
+      f[r] = row_scale * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), j % M::kBatch * R + r));
       vs[r] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.vs), j % M::kBatch * R + r));
       ve[r] = vs[r] > 0.0f ? __builtin_amdgcn_frexp_expf(vs[r]) : -1000;  // v < 2^ve
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[r / 2][8 * (r % 2) + i] *= f;
     }
     if (!(t0 >= all_lo && t0 >= from && t0 + M::kStep <= all_hi && t0 + M::kStep <= to && here == (1u << R) - 1)) {
       const int32_t lo = row_lo > from ? row_lo : from, hi = row_hi < to ? row_hi : to;
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t0 + kRun * r + i / 4 * 8 + 4 * c + i % 4;
-          if (!(tok >= lo && tok < hi && (here >> r & 1))) s[r / 2][8 * (r % 2) + i] = -INFINITY;
+          // the factor is applied here, so that none of 0 meets the infinity
+          const float x = s[r / 2][8 * (r % 2) + i] * f[r];
+          s[r / 2][8 * (r % 2) + i] = tok >= lo && tok < hi && (here >> r & 1) ? x : -INFINITY;
         }
+        f[r] = 1.0f;
+      }
     }
-    float m[R], top = -INFINITY, big = -INFINITY;
+    float m[R], top = -INFINITY, big = -INFINITY;  // of s f: the factors are not negative
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = s[r / 2][8 * (r % 2)];
 #pragma unroll
       for (int i = 1; i < 8; ++i) m[r] = fmaxf(m[r], s[r / 2][8 * (r % 2) + i]);
+      m[r] *= f[r];
       top = fmaxf(top, m[r]);
       big = fmaxf(big, m[r] - ref + (float)ve[r]);
     }
@@ -555,41 +583,52 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
 #pragma unroll
       for (int jj = 0; jj < J; ++jj) o[jj] *= fo;
     }
-    half8 p[kParts][R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float g = fminf(ldexpf(vs[r], -shift), 0x1p120f);  // where it ends, weights are 0
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float w = __builtin_amdgcn_exp2f(s[r / 2][8 * (r % 2) + i] - ref);
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[r / 2][8 * (r % 2) + i], f[r], -ref));
         l += w;
         const float x = w * g;
         p[0][r][i] = (_Float16)x;
         if (kParts == 2) p[kParts - 1][r][i] = (_Float16)(x - (float)p[0][r][i]);
       }
     }
-#pragma unroll
-    for (int jj = 0; jj < J; ++jj) {
-      const int ch = 32 * jj + n, turn = M::value_turn(ch);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const half8 w = *reinterpret_cast<const half8 *>(values + (ch * M::kValueUnits + ((2 * r + c) ^ turn)) * 16);
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) o[jj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, p[k][r], o[jj], 0, 0, 0);
-      }
-    }
+  };
+  // Until the workgroup's waves are here; what they wrote to LDS before is seen after.
+  auto meet = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0); loads from memory stay in flight
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
 
+  // A step is two phases: the products, then the weights with the next codes' way to LDS.  Two waves
+  // share a SIMD, and left alone both multiply and then both weigh: so one of them (`late`) is a
+  // phase behind the other, and one multiplies while the other weighs.  In phase 2 j group 0
+  // multiplies step j and group 1 weighs step j - 1, in phase 2 j + 1 the other way about; step j's
+  // codes are stored in phases 2 j - 1 (group 0) and 2 j - 2 (group 1), its keys are read in 2 j and
+  // 2 j + 1, its values in 2 j + 2 and 2 j + 3, so two and three stages do.
   if (steps > 0) store(0);
-  __syncthreads();
+  if (steps > 1) load(1);
+  meet();
+  if (late) {
+    if (steps > 1) store(1);
+    if (steps > 2) load(2);
+    meet();
+  }
   for (int32_t j = 0; j < steps; ++j) {
     if (j % M::kBatch == 0) now = next;
-    if (j + 1 < steps) load(j + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(j);
-    if (j + 1 < steps) store(j + 1);
-    __syncthreads();
+    multiply(j);
+    if (M::kTurns) meet();
+    weigh(j);
+    if (j + 1 + late < steps) store(j + 1 + late);
+    if (j + 2 + late < steps) load(j + 2 + late);
+    meet();
   }
+  multiply(steps);
+  if (M::kTurns && !late) meet();
 
   if (n >= live) return;
   const float sum = [&] {
