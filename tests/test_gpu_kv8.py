@@ -294,24 +294,25 @@ def test_long_context(L, dim, dtype, window):
     K.compare(out, lse, q, kv, lens, [1, 1], dtype, dim ** -0.5, window)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 64])
 def test_pages_that_are_not_there(L, rows):
     """Negative page numbers and ones past the cache: their tokens count as absent; requests of
     which nothing is left give 0 and -inf."""
     dim, page, dtype, lens = 128, 16, torch.float16, [100, 70, 64]
+    hq = 8 if rows == 64 else 4
     dev, table, kv = build(lens, 2, dim, page, dtype, 17)
     gone = [set(), set(), set()]
     for b, js in ((0, (0, 3, 6)), (1, (4,)), (2, (0, 1, 2, 3))):
         for j in js:
             table[b, j] = [-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1][j % 4]
             gone[b] |= set(range(j * page, (j + 1) * page))
-    q = queries(3 * rows, 4, dim, dtype, 2)
+    q = queries(3 * rows, hq, dim, dtype, 2)
     out, lse = attend(L, q, dev, table, lens, [rows] * 3, page, dtype, 0.1)
     K.compare(out, lse, q, kv, lens, [rows] * 3, dtype, 0.1, absent=gone)
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("rows", [1, 30])
+@pytest.mark.parametrize("rows", [1, 30, 90])
 def test_runs_of_far_apart_sizes(L, dtype, rows):
     """Values whose runs differ by up to 2^30 and keys that make the small ones count: what a weight
     loses goes by the row's own largest product, not by the largest scale that it passes."""
@@ -335,22 +336,44 @@ def test_runs_of_far_apart_sizes(L, dtype, rows):
     assert scale < 1.0 and err.max() <= (torch.finfo(dtype).eps / 2 + 2.0 ** -10) * scale, (err.max(), scale)
 
 
-def test_scores_of_any_size(L):
+@pytest.mark.parametrize("rows", [1, 7, 40])
+def test_scores_of_any_size(L, rows):
     """Large scores (a few tokens take everything), and values of zero."""
     dim, page, dtype, lens = 64, 32, torch.float16, [150, 90]
     dev, table, kv = build(lens, 1, dim, page, dtype, 23)
-    q = queries(2, 4, dim, dtype, 4)
+    q = queries(2 * rows, 4, dim, dtype, 4)
     for scale in (0.0, 3.0, -2.0, 300.0):
-        out, lse = attend(L, q, dev, table, lens, [1, 1], page, dtype, scale)
-        K.compare(out, lse, q, kv, lens, [1, 1], dtype, scale)
+        out, lse = attend(L, q, dev, table, lens, [rows] * 2, page, dtype, scale)
+        K.compare(out, lse, q, kv, lens, [rows] * 2, dtype, scale)
 
     def zero(t, heads, d, dt, seed):
         k, v = key_values(t, heads, d, dt, seed)
         return k, np.where(np.arange(t)[:, None, None] // 16 % 2 == 0, 0, v).astype(np.float32)
 
     dev, table, kv = build(lens, 1, dim, page, dtype, 29, kv=zero)
-    out, lse = attend(L, q, dev, table, lens, [1, 1], page, dtype, 0.1)
-    K.compare(out, lse, q, kv, lens, [1, 1], dtype, 0.1)
+    out, lse = attend(L, q, dev, table, lens, [rows] * 2, page, dtype, 0.1)
+    K.compare(out, lse, q, kv, lens, [rows] * 2, dtype, 0.1)
+
+    def none(t, heads, d, dt, seed):
+        k, v = key_values(t, heads, d, dt, seed)
+        return k, 0 * v
+
+    dev, table, kv = build(lens, 1, dim, page, dtype, 29, kv=none)
+    out, lse = attend(L, q, dev, table, lens, [rows] * 2, page, dtype, 0.1)
+    assert not out.any()
+    K.compare(out, lse, q, kv, lens, [rows] * 2, dtype, 0.1)
+
+
+@pytest.mark.parametrize("hq,hkv,dim,rows,window", [(8, 2, 128, 64, 0), (4, 1, 256, 33, 0), (8, 1, 64, 20, 900), (32, 1, 128, 9, 0)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_rows_over_a_long_context(L, hq, hkv, dim, rows, window, dtype):
+    """Tiles of many rows whose tokens are split among workgroups."""
+    page, lens = 64, [4000, 1531]
+    U.say("attention8 many rows, long", hq, hkv, dim, rows, window, dtype)
+    dev, table, kv = build(lens, hkv, dim, page, dtype, 53)
+    q = queries(2 * rows, hq, dim, dtype, 5)
+    out, lse = attend(L, q, dev, table, lens, [rows] * 2, page, dtype, dim ** -0.5, window)
+    K.compare(out, lse, q, kv, lens, [rows] * 2, dtype, dim ** -0.5, window, picks=lambda n: {0, 7, n - 1})
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])

@@ -36,6 +36,11 @@ __device__ __forceinline__ half8 codes8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(half8, b) - (_Float16)(1024 + mixllm::kKv8Zero);
 }
 
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
 constexpr int kTokens = 2 * kRun;  // of a step: two runs fill an operand of the second product
 constexpr float kTop = 14.0f;      // weights times scales stay below 2^kTop, fp16 ends at 2^16
 constexpr float kRoom = 5.0f;      // and are moved there or kRoom below
@@ -390,31 +395,39 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
   const int32_t P = 1 << a.page_log2, block = mixllm::kv8_block_bytes(P, D);
   const int32_t *table = a.table + b * a.ldt;
 
-  // Pages and scales of kBatch steps at a time, a run a lane.
+  // Pages and scales of kBatch steps at a time, a run a lane.  A value's scale is 2^(ve + lv), its inverse
+  // iv 2^-ve; values of nothing but zeros have ve = kNone and count as with a scale of 1.
+  constexpr int32_t kNone = -1000;
   struct Batch {
-    int32_t pages;
-    float ks, vs;
+    int32_t pages, ve;
+    float ks, lv, iv;
     uint64_t there;
-  } now = {-1, 0.0f, 0.0f, 0}, next = now;
+  } now = {-1, kNone, 0.0f, 0.0f, 1.0f, 0}, next = now;
   auto fetch = [&](int32_t j) {
     const int32_t tok = start + j * M::kStep + lane * kRun;
     next.pages = tok < to ? table[tok >> a.page_log2] : -1;
     next.pages = (uint32_t)next.pages < (uint32_t)a.pages ? next.pages : -1;
     next.there = __ballot(next.pages >= 0);
-    next.ks = next.vs = 0.0f;
-    if (next.pages >= 0) {
-      const float2v s = *reinterpret_cast<const float2v *>(a.cache + ((int64_t)next.pages * a.hkv + h) * block +
-                                                           mixllm::kv8_scale_offset(P, D) + (tok & (P - 1)) / kRun * 8);
-      next.ks = s.x, next.vs = s.y;
-    }
+    float2v sc = {0.0f, 0.0f};
+    if (next.pages >= 0)
+      sc = *reinterpret_cast<const float2v *>(a.cache + ((int64_t)next.pages * a.hkv + h) * block +
+                                              mixllm::kv8_scale_offset(P, D) + (tok & (P - 1)) / kRun * 8);
+    const bool some = sc.y > 0.0f;
+    const float mant = some ? __builtin_amdgcn_frexp_mantf(sc.y) : 1.0f;  // [1/2, 1)
+    next.ks = sc.x;
+    next.ve = some ? __builtin_amdgcn_frexp_expf(sc.y) : kNone;
+    next.lv = log2f(mant), next.iv = 1.0f / mant;
   };
-  // This wave's units of step j: blocks wave, wave + kWaves, .. of the step's keys, then values.
+  // This wave's units of a step: wave, wave + kWaves, .. of its keys, then of its values; with 64
+  // channels one of either.
+  auto part_of = [&](int i) { return M::kBlocks > 1 ? i / (M::kBlocks / 2) : wave / (R * U); };
+  auto unit_of = [&](int i) { return M::kBlocks > 1 ? wave + i % (M::kBlocks / 2) * M::kWaves : wave % (R * U); };
   uint4v raw[M::kBlocks];
   auto load = [&](int32_t j) __attribute__((always_inline)) {
     if (j % M::kBatch == 0) fetch(j);
 #pragma unroll
     for (int i = 0; i < M::kBlocks; ++i) {
-      const int ub = wave + i * M::kWaves, part = ub / (R * U), r = ub % (R * U) / U, u = ub % U;
+      const int part = part_of(i), r = unit_of(i) / U, u = unit_of(i) % U;
       const int32_t pg = __builtin_amdgcn_readlane(next.pages, j % M::kBatch * R + r);
       const int32_t in = (start + j * M::kStep + kRun * r) & (P - 1);
       // an absent run reads any memory of the cache; its scores are masked
@@ -427,7 +440,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
     const int m = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < M::kBlocks; ++i) {
-      const int ub = wave + i * M::kWaves, part = ub / (R * U), r = ub % (R * U) / U, u = ub % U;
+      const int part = part_of(i), r = unit_of(i) / U, u = unit_of(i) % U;
       const half8 lo = codes8(raw[i].x, raw[i].y), hi = codes8(raw[i].z, raw[i].w);
       if (part == 0) {  // 16 channels of token m
         const int token = kRun * r + m, unit = 8 * u + 2 * q, turn = M::key_turn(token);
@@ -502,6 +515,16 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
     const int32_t t0 = start + j * M::kStep;
     return live > 0 && t0 < any_hi && t0 + M::kStep > any_lo;
   };
+  // The order of `reads` operands' reads and `each` products with every one: reads run kAhead ahead.
+  auto reads_ahead = [&](auto reads, auto each) __attribute__((always_inline)) {
+    constexpr int kReads = decltype(reads)::value, kEach = decltype(each)::value, kAhead = 6;
+    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+      if (i + kAhead < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  };
   auto multiply = [&](int32_t j) __attribute__((always_inline)) {  // the last step's values, this one's keys
     if (j > 0 && seen(j - 1)) {
       const uint8_t *values = all_values + (j - 1) % 3 * M::kStage;
@@ -515,33 +538,38 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
           for (int k = 0; k < kParts; ++k) o[jj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, p[k][r], o[jj], 0, 0, 0);
         }
       }
+      reads_ahead(Const<J * R>(), Const<kParts>());
     }
     if (j < steps && seen(j)) {
       const uint8_t *keys = all_keys + (j & 1) * M::kStage;
 #pragma unroll
-      for (int x = 0; x < R / 2; ++x) {
+      for (int x = 0; x < R / 2; ++x)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[x][i] = 0.0f;
-        const int token = 32 * x + n, turn = M::key_turn(token);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int x = 0; x < R / 2; ++x) {
+          const int token = 32 * x + n, turn = M::key_turn(token);
           const half8 w = *reinterpret_cast<const half8 *>(keys + (token * M::kKeyUnits + ((2 * e + c) ^ turn)) * 16);
           s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, q[e], s[x], 0, 0, 0);
         }
-      }
+      reads_ahead(Const<R / 2 * E>(), Const<1>());
     }
   };
   auto weigh = [&](int32_t j) __attribute__((always_inline)) {
     if (!seen(j)) return;
     const int32_t t0 = start + j * M::kStep;
     const uint32_t here = (uint32_t)(now.there >> (j % M::kBatch * R)) & ((1u << R) - 1);
-    float f[R], vs[R];
+    auto of_run = [&](float v, int r) {
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j % M::kBatch * R + r));
+    };
+    float f[R];
     int32_t ve[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      f[r] = row_scale * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), j % M::kBatch * R + r));
-      vs[r] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.vs), j % M::kBatch * R + r));
-      ve[r] = vs[r] > 0.0f ? __builtin_amdgcn_frexp_expf(vs[r]) : -1000;  // v < 2^ve
+      f[r] = row_scale * of_run(now.ks, r);
+      ve[r] = __builtin_amdgcn_readlane(now.ve, j % M::kBatch * R + r);  // v < 2^ve
     }
     if (!(t0 >= all_lo && t0 >= from && t0 + M::kStep <= all_hi && t0 + M::kStep <= to && here == (1u << R) - 1)) {
       const int32_t lo = row_lo > from ? row_lo : from, hi = row_hi < to ? row_hi : to;
@@ -583,17 +611,21 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
 #pragma unroll
       for (int jj = 0; jj < J; ++jj) o[jj] *= fo;
     }
+    // A weight times a value's scale 2^-shift in one exponential; their sum less that factor is the
+    // weights'.
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float g = fminf(ldexpf(vs[r], -shift), 0x1p120f);  // where it ends, weights are 0
+      const int32_t d = ve[r] == kNone ? 0 : ve[r] - shift;
+      const float add = (of_run(now.lv, r) + (float)d) - ref;
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float w = __builtin_amdgcn_exp2f(fmaf(s[r / 2][8 * (r % 2) + i], f[r], -ref));
-        l += w;
-        const float x = w * g;
-        p[0][r][i] = (_Float16)x;
-        if (kParts == 2) p[kParts - 1][r][i] = (_Float16)(x - (float)p[0][r][i]);
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[r / 2][8 * (r % 2) + i], f[r], add));
+        sum += w;
+        p[0][r][i] = (_Float16)w;
+        if (kParts == 2) p[kParts - 1][r][i] = (_Float16)(w - (float)p[0][r][i]);
       }
+      l = fmaf(sum, ldexpf(of_run(now.iv, r), -d), l);
     }
   };
   // Until the workgroup's waves are here; what they wrote to LDS before is seen after.
@@ -620,11 +652,11 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
   }
   for (int32_t j = 0; j < steps; ++j) {
     if (j % M::kBatch == 0) now = next;
+    if (j > 0 && j + 1 + late < steps) load(j + 1 + late);
     multiply(j);
     if (M::kTurns) meet();
     weigh(j);
     if (j + 1 + late < steps) store(j + 1 + late);
-    if (j + 2 + late < steps) load(j + 2 + late);
     meet();
   }
   multiply(steps);
