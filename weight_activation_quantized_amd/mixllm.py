@@ -830,6 +830,42 @@ class PackedLinear:
         return bufs["y"]
 
 
+class RowLinear:
+    """A layer wholly in 8 bits with one scale per output channel, its activations with one per
+    token: ``forward(a)`` runs mixllm_quant_rows then mixllm_gemm_w8a8.  ``w``: [N, K] fp16 (or bf16,
+    as a tensor), quantized once on the GPU; ``dtype``: of the outputs, fp16 or bf16."""
+
+    def __init__(self, w, device="cuda", dtype=None):
+        w = torch.as_tensor(w).to(device)
+        self.n, self.k = w.shape
+        self.w = torch.empty((self.n, self.k), dtype=torch.int8, device=device)
+        self.sw = torch.empty(self.n, dtype=torch.float32, device=device)
+        self.device, self.dtype = device, dtype or torch.float16
+        mixllm_quant_rows(w.contiguous(), self.w, self.sw)
+
+    def buffers(self, m: int):
+        dev = self.device
+        return dict(aq=torch.empty((m, self.k), dtype=torch.int8, device=dev),
+                    sa=torch.empty(m, dtype=torch.float32, device=dev),
+                    y=torch.empty((m, self.n), dtype=self.dtype, device=dev))
+
+    def forward(self, a, bufs=None, stream=None):
+        m = a.shape[0]
+        bufs = bufs or self.buffers(m)
+        _same_rows(bufs, m)
+        if m:
+            mixllm_quant_rows(a, bufs["aq"], bufs["sa"], stream)
+        return self.gemm(bufs, stream, m)
+
+    def gemm(self, bufs, stream=None, rows=None):
+        """The product alone, of activations that are quantized in ``bufs`` already (as many
+        rows as the buffers have, unless ``rows`` is given)."""
+        m = bufs["aq"].shape[0] if rows is None else rows
+        if m:
+            mixllm_gemm_w8a8(bufs["aq"], bufs["sa"], self.w, self.sw, bufs["y"], stream)
+        return bufs["y"]
+
+
 def concat_layers(weights, idx8s):
     """Several layers over the same input as one: their fp16 weights stacked along the output
     channels, each layer's 8-bit channel indices shifted to its rows.  Returns (w, idx8,
@@ -960,24 +996,39 @@ class AttentionBlock:
     the cache, attention, and the quantization and GEMM of the output projection.  Six launches on
     one stream (seven where attention splits the tokens).  ``norm`` is the weight of the norm
     before the projections; ``post_norm``, for layers that norm what a block gives, is the one of
-    the block *before* this one (its output x is normed as it is added).  Argument marshalling
-    only."""
+    the block *before* this one (its output x is normed as it is added).
+
+    ``cache_bits`` 8 keeps the cache in 8 bits.  ``q_norm``, ``k_norm`` ([dim]) norm every head of
+    queries and keys (with ``eps``), ``inv_freq`` (fp32 [rot / 2]) turns their first rot channels by
+    the position, pairs (i, i + rot / 2) or with ``neighbours`` (2i, 2i + 1): one launch more, between
+    the product and the write.  ``idx8_o`` None takes the output projection wholly in 8 bits with a
+    scale per channel and token (RowLinear).  Argument marshalling only."""
 
     def __init__(self, w_q, w_k, w_v, w_o, idx8_q, idx8_k, idx8_v, idx8_o, norm, q_heads: int, kv_heads: int,
-                 pages: int, page: int, post_norm=None, eps: float = 1e-5, window: int = 0, device="cuda"):
+                 pages: int, page: int, post_norm=None, eps: float = 1e-5, window: int = 0, device="cuda",
+                 cache_bits: int = 4, q_norm=None, k_norm=None, inv_freq=None, neighbours: bool = False):
+        if cache_bits not in (4, 8):
+            raise ValueError(f"cache_bits must be 4 or 8, is {cache_bits}")
         self.qkv = QKVProjection(w_q, w_k, w_v, idx8_q, idx8_k, idx8_v, device)
-        self.o = PackedLinear(np.asarray(w_o, np.float16), idx8_o, device)
+        w_o = np.asarray(w_o, np.float16)
+        self.o = RowLinear(w_o, device) if idx8_o is None else PackedLinear(w_o, idx8_o, device)
         self.q_heads, self.kv_heads = q_heads, kv_heads
         self.dim = np.asarray(w_k).shape[0] // kv_heads
         if np.asarray(w_q).shape[0] != q_heads * self.dim or np.asarray(w_k).shape != np.asarray(w_v).shape or (
                 self.o.k != q_heads * self.dim):
             raise ValueError("the projections' shapes do not fit the heads")
-        self.cache = kv4_cache(pages, page, kv_heads, self.dim, device)
+        for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if w is not None and w.numel() != self.dim:
+                raise ValueError(f"{name} must have {self.dim} elements, one per channel of a head, has {w.numel()}")
+        if inv_freq is not None and not 0 < inv_freq.numel() <= self.dim // 2:
+            raise ValueError(f"inv_freq must have 1 to {self.dim // 2} elements, has {inv_freq.numel()}")
+        self.cache = (kv4_cache if cache_bits == 4 else kv8_cache)(pages, page, kv_heads, self.dim, device)
         self.norm, self.post_norm, self.eps, self.window, self.page, self.device = norm, post_norm, eps, window, page, device
+        self.cache_bits, self.q_norm, self.k_norm, self.inv_freq, self.neighbours = cache_bits, q_norm, k_norm, inv_freq, neighbours
 
     def buffers(self, m: int, requests: int, max_rows: int, max_len: int):
-        size = mixllm_kv4_attention_workspace_bytes(m, requests, self.q_heads, self.kv_heads, self.dim, max_rows, max_len,
-                                                    self.window)
+        size_of = mixllm_kv4_attention_workspace_bytes if self.cache_bits == 4 else mixllm_kv8_attention_workspace_bytes
+        size = size_of(m, requests, self.q_heads, self.kv_heads, self.dim, max_rows, max_len, self.window)
         return dict(qkv=self.qkv.buffers(m), o=self.o.buffers(m), max_rows=max_rows, max_len=max_len,
                     attn=torch.zeros((m, self.q_heads, self.dim), dtype=torch.float16, device=self.device),
                     ws=torch.empty(size, dtype=torch.uint8, device=self.device) if size else None)
@@ -987,8 +1038,9 @@ class AttentionBlock:
         x of the layer before (None for the first); M the rows that the plan counts or more (a
         token whose row is missing here is counted and never written); req: RequestPages after
         its plan(); rotate: called with the views q [M, heads, dim], k and the positions before
-        the keys are written, for an embedding of positions (in place, on the stream that is
-        current then, which is ``stream``).  Returns the output projection's [M, hidden]."""
+        the keys are written, for an embedding of positions of the caller's own (in place, on the
+        stream that is current then, which is ``stream``; after the layer's own norms and rotation,
+        if it has them).  Returns the output projection's [M, hidden]."""
         if req.page != self.page or req.pages > self.cache.shape[0]:
             raise ValueError(f"the requests have {req.pages} pages of {req.page} tokens, the cache has "
                              f"{self.cache.shape[0]} pages of {self.page}")
@@ -1000,12 +1052,17 @@ class AttentionBlock:
         q, k, v = self.qkv.split(self.qkv.layer.gemm(b, stream))
         q, k, v = q.unflatten(1, (self.q_heads, self.dim)), k.unflatten(1, (self.kv_heads, self.dim)), v.unflatten(
             1, (self.kv_heads, self.dim))
+        if self.q_norm is not None or self.k_norm is not None or self.inv_freq is not None:
+            mixllm_head_norm_rotate(q, k, req.pos[:m], self.inv_freq, q_norm=self.q_norm, k_norm=self.k_norm, eps=self.eps,
+                                    neighbours=self.neighbours, stream=stream)
         if rotate is not None:
             with _current(stream, q.device):  # between the product and the write, on the same stream
                 rotate(q, k, req.pos[:m])
-        mixllm_kv4_append(k, v, req.slots[:m], self.cache, self.page, stream)
-        mixllm_kv4_attention(q, self.cache, req.table, req.lens, req.cu, bufs["attn"], self.page, bufs["max_rows"],
-                             bufs["max_len"], window=self.window, workspace=bufs["ws"], stream=stream)
+        append, attention = ((mixllm_kv4_append, mixllm_kv4_attention) if self.cache_bits == 4 else
+                             (mixllm_kv8_append, mixllm_kv8_attention))
+        append(k, v, req.slots[:m], self.cache, self.page, stream)
+        attention(q, self.cache, req.table, req.lens, req.cu, bufs["attn"], self.page, bufs["max_rows"],
+                  bufs["max_len"], window=self.window, workspace=bufs["ws"], stream=stream)
         return self.o.forward(bufs["attn"].flatten(1), bo, stream)
 
 
