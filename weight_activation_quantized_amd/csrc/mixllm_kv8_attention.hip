@@ -51,8 +51,11 @@ struct Stage {
   uint4v k[2][D / 64], v[2][D / 64];
 };
 
-// CT: column blocks of 16 rows that share the operands made of codes.
-template <int D, int CT, bool BF16>
+// CT: column blocks of 16 rows that share the operands made of codes.  ONCE: one tile holds all rows of
+// a request and head, so a code is read once and its line need not stay in the caches (us, one
+// tile: 128 requests of up to 8192 tokens 346 -> 312, 32 of up to 4001 50.3 -> 44.3; two tiles that
+// read the same codes 34.6 -> 37.2, so not there).
+template <int D, int CT, bool ONCE, bool BF16>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kernel(Args a) {
   constexpr int U = D / 64, E = D / 32, J = D / 16;
   constexpr int kStride = D + 4;  // floats of a row of partial outputs in LDS
@@ -90,8 +93,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kern
       const uint8_t *src = a.cache + ((int64_t)(pg < 0 ? 0 : pg) * a.hkv + h) * block + (int64_t)in * D;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        st.k[x][u] = *reinterpret_cast<const uint4v *>(src + u * 1024 + lane * 16);
-        st.v[x][u] = *reinterpret_cast<const uint4v *>(src + P * D + u * 1024 + lane * 16);
+        const uint4v *k = reinterpret_cast<const uint4v *>(src + u * 1024 + lane * 16);
+        const uint4v *v = reinterpret_cast<const uint4v *>(src + P * D + u * 1024 + lane * 16);
+        st.k[x][u] = ONCE ? __builtin_nontemporal_load(k) : *k;
+        st.v[x][u] = ONCE ? __builtin_nontemporal_load(v) : *v;
       }
     }
   };
@@ -722,11 +727,18 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
 template <int D, bool BF16>
 void launch(const Args &a, hipStream_t s) {
   const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
-  if (a.tile_rows > 32)
+  if (a.tile_rows > 32) {
     hipLaunchKernelGGL((kv8_many_kernel<D, BF16>), grid, dim3(Many<D>::kThreads), 0, s, a);
-  else if (D < 256 && a.tile_rows == 32)
-    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, BF16>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((kv8_attention_kernel<D, 1, BF16>), grid, threads, 0, s, a);
+  } else if (D == 256) {  // 16-row tiles only
+    if (a.tiles == 1) hipLaunchKernelGGL((kv8_attention_kernel<D, 1, true, BF16>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((kv8_attention_kernel<D, 1, D != 256, BF16>), grid, threads, 0, s, a);
+  } else if (a.tile_rows == 16) {
+    hipLaunchKernelGGL((kv8_attention_kernel<D, 1, true, BF16>), grid, threads, 0, s, a);
+  } else if (a.tiles == 1) {
+    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, true, BF16>), grid, threads, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, false, BF16>), grid, threads, 0, s, a);
+  }
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
   launch_join<D, BF16>(a, s);
 }

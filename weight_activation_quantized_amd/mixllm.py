@@ -674,29 +674,33 @@ def mixllm_head_norm_rotate(q, k, pos, inv_freq, q_out=None, k_out=None, q_norm=
     if lead.dim() != 3:
         raise ValueError(f"q and k must be [T, heads, dim], got {tuple(lead.shape)}")
     t, _, dim = lead.shape
-    side = []
-    for x, out, w, name in ((q, q_out, q_norm, "q"), (k, k_out, k_norm, "k")):
-        if x is None:
-            if out is not None or w is not None:
-                raise ValueError(f"{name}_out and {name}_norm go with {name}, which is None")
-            side.append((None, 0, None, 0, None, 0))
-            continue
-        shape = x.shape
+    pq = pqo = pqn = pk = pko = pkn = pfreq = ppos = None
+    ldq = ldqo = ldk = ldko = hq = hk = rot = 0
+    if q is not None:
+        shape = q.shape
+        hq = shape[1]
+        pq, ldq = q.data_ptr(), _ld(q, "q", t16, dev, shape, hq * dim)
+        pqo, ldqo = (pq, ldq) if q_out is None else (q_out.data_ptr(), _ld(q_out, "q_out", t16, dev, shape, hq * dim))
+        pqn = None if q_norm is None else _channels(q_norm, "q_norm", t16, dev, dim)
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm go with q, which is None")
+    if k is not None:
+        shape = k.shape
         if len(shape) != 3 or shape[0] != t or shape[2] != dim:
-            raise ValueError(f"q and k must be [T, heads, dim] with one T and dim, {name} is {tuple(shape)}")
-        width = shape[1] * dim
-        out = x if out is None else out
-        side.append((x.data_ptr(), _ld(x, name, t16, dev, shape, width), out.data_ptr(),
-                     _ld(out, name + "_out", t16, dev, shape, width),
-                     None if w is None else _channels(w, name + "_norm", t16, dev, dim), shape[1]))
-    (pq, ldq, pqo, ldqo, pqn, hq), (pk, ldk, pko, ldko, pkn, hk) = side
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if rot and pos is None:
-        raise ValueError("pos is required for a rotation")
-    _on(dev, stream, _lib.mixllm_head_norm_rotate, pq, ldq, pk, ldk, pqo, ldqo, pko, ldko,
-        _flat(pos, "pos", _i32t, dev, t) if rot else None,
-        _flat(inv_freq, "inv_freq", torch.float32, dev, 0) if rot else None, pqn, pkn, t, hq, hk, dim, rot,
-        1 if neighbours else 0, dtype, eps)
+            raise ValueError(f"q and k must be [T, heads, dim] with one T and dim, k is {tuple(shape)}")
+        hk = shape[1]
+        pk, ldk = k.data_ptr(), _ld(k, "k", t16, dev, shape, hk * dim)
+        pko, ldko = (pk, ldk) if k_out is None else (k_out.data_ptr(), _ld(k_out, "k_out", t16, dev, shape, hk * dim))
+        pkn = None if k_norm is None else _channels(k_norm, "k_norm", t16, dev, dim)
+    elif k_out is not None or k_norm is not None:
+        raise ValueError("k_out and k_norm go with k, which is None")
+    if inv_freq is not None and inv_freq.numel():
+        if pos is None:
+            raise ValueError("pos is required for a rotation")
+        rot = 2 * inv_freq.numel()
+        pfreq, ppos = _flat(inv_freq, "inv_freq", torch.float32, dev, 0), _flat(pos, "pos", _i32t, dev, t)
+    _on(dev, stream, _lib.mixllm_head_norm_rotate, pq, ldq, pk, ldk, pqo, ldqo, pko, ldko, ppos, pfreq, pqn, pkn, t, hq, hk,
+        dim, rot, 1 if neighbours else 0, dtype, eps)
 
 
 def mixllm_kv8_page_bytes(page: int, heads: int, dim: int) -> int:
