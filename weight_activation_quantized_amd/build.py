@@ -21,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -55,18 +56,20 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
     knobs such as ring depths)."""
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
-    objs = []
-    for src in SOURCES:
-        path = os.path.join(CSRC, src)
-        tag = ("_" + "_".join(d.replace("=", "") for d in defines)) if defines else ""
-        obj = os.path.join(BUILD, src + tag + ".o")
-        dflags = [f"-D{d}" for d in defines]
+    tag = ("_" + "_".join(d.replace("=", "") for d in defines)) if defines else ""
+    dflags = [f"-D{d}" for d in defines]
+
+    def compile_one(src):
+        path, obj = os.path.join(CSRC, src), os.path.join(BUILD, src + tag + ".o")
         if src.endswith(".hip"):
             cmd = [cc, "-x", "hip", *COMMON, *dflags, *DEVICE, "-c", path, "-o", obj]
         else:
             cmd = [cc, "-x", "c++", *COMMON, *dflags, "-c", path, "-o", obj]
         _run(cmd, verbose)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(min(4, os.cpu_count() or 1)) as pool:  # a source each
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = out + ".tmp"
     _run([cc, *DEVICE, "-shared", "-fPIC", "-o", tmp, *objs, "-Wl,-rpath,/opt/rocm/lib"], verbose)
     os.replace(tmp, out)
