@@ -17,8 +17,16 @@
 //
 // Weights 2^(S - ref) times a run's scale v are rounded to fp16 for the product, after a power of
 // two per row that follows the largest such product (`shift`), so that rows whose large
-// values hardly count lose nothing; what the rounding leaves is a second operand.  Statistics,
-// sums and outputs are fp32.
+// values hardly count lose nothing; what the rounding leaves is a second operand (error of fp16
+// outputs 1.0 times that of their own rounding; bf16 prompts, whose rounding is 8 times coarser, go
+// without: 143 us for 2 x 1024 rows, where fp16 takes 182).  Statistics, sums and outputs are fp32.
+//
+// What bounds it, at 128 channels.  Decodes: the cache's bytes, 128 requests of up to 8192 tokens 1.68 GB
+// in 312 us, 5.4 TB/s (a large read reaches 5.9), one of 131071 tokens 269 MB in 45.7 us and 6 for the
+// join; small ones latency (77 tokens 5.8 us).  Prompts (2 x 1024 rows over 4096 tokens: 600 TFLOP/s in
+// fp16, 770 in bf16, where a large library product reaches 1176): the softmax, whose 250 vector
+// operations a step one wave of a SIMD issues at about 7 cycles each while the other multiplies:
+// 1800 - 2350 cycles of the weighing phase to 1000 - 1500 of matrix instructions.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -704,10 +712,15 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
 }
 
 // How the work of a call is cut.  Rows: tiles of 16 or 32 (row, head) pairs of one key/value
-// head, or of 256 (128 with 256 channels) where there are kMany or more.  Tokens: so many equal
-// chunks of each tile that about kTarget workgroups run at the longest length; 256 CUs hold 2 of
-// them each, or one of the large ones.
-constexpr int64_t kTarget = 512, kMany = 128;
+// head, or of 256 (128 with 256 channels) where there are kMany or more: 8 requests over 4001 tokens, 32/8
+// heads of 128, take 34.8 us with 64 pairs each in tiles of 32 and 39.0 in one large, 44.4 with 128
+// in one large and 52.8 in four of 32.  Tokens: equal chunks of each tile.  CUs hold 2 or more
+// small workgroups, so about kTarget of them run at the longest length (32 requests of 4001
+// tokens 50.3 us with 512, 52.2 with 768, 55.0 with 1024); a CU holds one large one, so as many
+// chunks as do not need a second round of kCus (2 x 700 rows of 256 channels 141 us in two
+// chunks for each of 176 tiles, whose second round and join take what the idle CUs would save, 139.5
+// in one).
+constexpr int64_t kTarget = 512, kCus = 256, kMany = 128;
 
 Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len, int32_t window) {
   Cut k;
@@ -719,7 +732,7 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
   if (window && (int64_t)window + k.tile_rows + kRun < span) span = (int64_t)window + k.tile_rows + kRun;
   const int64_t groups = (int64_t)B * hkv * k.tiles;
   const int64_t most = (span + kMinChunk - 1) / kMinChunk;
-  const int64_t want = ((rows >= kMany ? kTarget / 2 : kTarget) + groups - 1) / groups;
+  const int64_t want = rows >= kMany ? kCus / groups : (kTarget + groups - 1) / groups;
   k.splits = (int32_t)(most < 1 || want <= 1 ? 1 : want < most ? want : most);
   return k;
 }

@@ -6,6 +6,11 @@
 // for the pairs i < rot / 2 of a head, channels (i, i + rot / 2) or (2 i, 2 i + 1); channels
 // from rot on are only normed.  All in fp32 from one read, rounded once.  The angle is formed
 // in fp64 and reduced to (-pi, pi] there: in fp32 a position of 10^6 would leave it 0.03 off.
+//
+// Bound by the memory for prompts (8191 tokens x 72 heads of 128: 302 MB in 62 us, 4.9 TB/s, a large
+// copy's rate) and by latency for single tokens (32 tokens x 40 heads: 3.5 us, a launch and little
+// more).  Both needed the angles of a token formed once and not once for every head (153 us with each
+// lane's own), and 16 bytes a load.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
