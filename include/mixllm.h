@@ -508,6 +508,9 @@ int mixllm_kv8_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  *   bf16 values of q 2^-38 below the row's largest count as 0.
  *   Scores have fp32's range, with the bounds of mixllm_kv4_attention; a row that passes them
  *   (or holds no number) spoils no other row.
+ *   Prompts and single tokens may share a call: where max_rows * q_heads / kv_heads is 128 or more,
+ *   B * kv_heads 256 or more and T less than half of B * max_rows, requests of up to 32 rows and
+ *   heads per key/value head (16 with dim 256) are taken by one or two launches of their own.
  */
 size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t dim,
                                             int32_t max_rows, int32_t max_len, int32_t window);

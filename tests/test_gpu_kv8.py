@@ -391,6 +391,70 @@ def test_a_row_without_numbers_spoils_no_other(L, dtype, rows):
     assert out[rows - 1, 2].isnan().all()
 
 
+MIXES = {  # rows of each request: prompts among requests of few rows, some without any
+    "one prompt, 68 of few rows": ([1, 16, 15, 17, 0, 2, 1, 40] * 8 + [0, 300, 1, 16, 1], 2),
+    "two prompts, 130 single rows": ([1] * 60 + [129] + [1] * 69 + [258, 1], 2),
+    "few requests": ([1, 0, 700, 3, 2], 4),
+    "the prompt last": ([1] * 90 + [333], 1),
+}
+
+
+@pytest.mark.parametrize("mix", MIXES)
+@pytest.mark.parametrize("dim,dtype,window", [(64, torch.float16, 0), (128, torch.bfloat16, 0), (128, torch.float16, 90),
+                                              (256, torch.bfloat16, 0)])
+def test_prompts_among_single_rows(L, mix, dim, dtype, window):
+    """One call whose largest request has many rows and most others few: tiles by the rows of the
+    call, and a launch for the requests of few rows where the batch is large; rows that the call
+    does not have stay as they were."""
+    rows, group = MIXES[mix]
+    hkv = 1 if len(rows) < 10 else 3 if len(rows) > 80 else 4
+    lens = [max(0, n - 3) if b % 9 == 5 else n + (b * 67) % 400 for b, n in enumerate(rows)]
+    U.say("attention8 mix", mix, dim, dtype, window)
+    dev, table, kv = build(lens, hkv, dim, 32, dtype, 41)
+    q = queries(sum(rows), hkv * group, dim, dtype, 14)
+    out, lse = attend(L, q, dev, table, lens, rows, 32, dtype, 0.09, window, pad=4)
+    K.compare(out, lse, q, kv, lens, rows, dtype, 0.09, window,
+              picks=lambda n: set(range(n)) if n <= 17 else set(range(0, n, 43)) | {n - 1, n // 2, 15, 16, 63, 64} & set(range(n)))
+
+
+def test_a_replayed_call_of_prompts_among_single_rows(L):
+    """The same graph for another step: which requests have many rows is read on the GPU."""
+    hq, hkv, dim, page, dtype = 8, 4, 64, 16, torch.float16
+    steps = [[1] * 30 + [200] + [1] * 39, [2] * 50 + [150, 0] + [1] * 18, [0] * 69 + [260]]
+    lens = [[(b * 31) % 300 + n for b, n in enumerate(rows)] for rows in steps]
+    dev, table, kv = build([max(x) for x in zip(*lens)], hkv, dim, page, dtype, 43)
+    t, b = 300, 70
+    q, cu, ln = torch.zeros(t, hq, dim, dtype=dtype, device="cuda"), i32([0] * (b + 1)), i32([0] * b)
+    out, tab = torch.empty_like(q), cuda(table)
+    size = L.mixllm_kv8_attention_workspace_bytes(t, b, hq, hkv, dim, 260, 600)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert size
+    call = lambda: L.mixllm_kv8_attention(q, dev, tab, ln, cu, out, page, 260, 600, scale=0.1, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i, (rows, held) in enumerate(zip(steps * 2, lens * 2)):
+        x = queries(t, hq, dim, dtype, 50 + i)
+        q.copy_(cuda(x, dtype))
+        cu.copy_(i32(np.concatenate([[0], np.cumsum(rows)])))
+        ln.copy_(i32(held))
+        out.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        n = sum(rows)
+        got = out[:n].clone()
+        assert torch.all(out[n:] == 9.0)
+        out.fill_(9.0)
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:n], got)
+        alone, lse = attend(L, x[:n], dev, table, held, rows, page, dtype, 0.1, max_rows=260, max_len=600)
+        K.compare(got, lse, x[:n], [tuple(a[:m] for a in one) for one, m in zip(kv, held)], held, rows, dtype, 0.1,
+                  picks=lambda n: set(range(n)) if n <= 17 else set(range(0, n, 43)) | {n - 1})
+
+
 @pytest.mark.parametrize("max_rows,max_len", [(3, 500), (1, 100), (9, 40)])
 def test_promises_that_are_too_small(L, max_rows, max_len):
     """Rows past max_rows are left out, lengths past max_len count as that."""

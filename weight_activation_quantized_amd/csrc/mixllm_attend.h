@@ -109,9 +109,9 @@ __device__ __forceinline__ int32_t chunks_of(const Tile &t, int32_t chunk) {
 // Joins the chunks of a row: out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  WAVES
 // waves share a row and head, wave w takes the chunks w, w + WAVES, ..; a workgroup has 4 waves
 // or as many as share.  Up to 16 chunks a wave does alone (4 us, of which a launch is most);
-// 64 chunks take 5.7 us with 16 waves, 8.0 with 4.
-template <int D, int WAVES, bool BF16>
-__global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void join_kernel(Args a) {
+// 64 chunks take 5.7 us with 16 waves, 8.0 with 4.  A: Args, or what a cache adds to them.
+template <int D, int WAVES, bool BF16, class A>
+__global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void join_kernel(A a) {
   constexpr int C = D / 64;  // channels of a lane
   constexpr int kAll = WAVES > kWaves ? WAVES : kWaves;
   __shared__ float s_m[kAll], s_l[kAll], s_o[kAll][D];
@@ -194,11 +194,11 @@ __global__ __launch_bounds__(64 * (WAVES > kWaves ? WAVES : kWaves)) void join_k
 }
 
 // The second launch of a call whose tokens are split.
-template <int D, bool BF16>
-void launch_join(const Args &a, hipStream_t s) {
+template <int D, bool BF16, class A>
+void launch_join(const A &a, hipStream_t s) {
   const int64_t rows = (int64_t)a.B * a.max_rows * a.hq;
-  if (a.splits > 16) hipLaunchKernelGGL((join_kernel<D, 16, BF16>), dim3((unsigned)rows), dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((join_kernel<D, 1, BF16>), dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a);
+  if (a.splits > 16) hipLaunchKernelGGL((join_kernel<D, 16, BF16, A>), dim3((unsigned)rows), dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((join_kernel<D, 1, BF16, A>), dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a);
 }
 
 struct Cut {

@@ -36,6 +36,45 @@
 
 namespace {
 
+// A launch takes the requests whose (row, head) pairs of a key/value head are `least` to `most`.
+struct Args8 : Args {
+  int32_t least, most;
+  int32_t units;  // tiles of all requests one after another (find_tile); 0: `tiles` for each request
+};
+
+__device__ __forceinline__ Tile tile_of(const Args8 &a, int32_t b, int32_t h, int32_t rt) {
+  Tile t = tile_of(static_cast<const Args &>(a), b, h, rt);
+  const int64_t all = (int64_t)t.n * a.group;
+  if (all < a.least || all > a.most) t.n = t.rows = t.lo = t.hi = 0;
+  return t;
+}
+
+// Tile rt of request b as number `unit` from the last: request b's begin at number cu[b] group / ROWS + b,
+// which leaves each request the numbers that its tiles need.  The wave looks for the last request
+// that begins at or before it, 64 at a time.  False: there is none, or it has no such tile.
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const Args8 &a, int64_t unit, int32_t &b, int32_t &rt) {
+  unit = a.units - 1 - unit;
+  auto begin = [&](int32_t i) {
+    const int32_t row = a.cu[i] < 0 ? 0 : a.cu[i] < a.T ? a.cu[i] : a.T;
+    return (int64_t)((uint64_t)((int64_t)row * a.group) / ROWS) + i;
+  };
+  const int32_t lane = threadIdx.x & 63;
+  b = 0;
+  for (int32_t left = a.B;;) {
+    const int32_t step = (left + 63) / 64, off = lane * step;
+    const int32_t before = __popcll(__ballot(off < left && begin(b + (off < left ? off : 0)) <= unit));
+    if (before == 0) return false;
+    b += (before - 1) * step;
+    if (step == 1) break;
+    left = left - (before - 1) * step < step ? left - (before - 1) * step : step;
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  const int64_t tile = unit - begin(b);
+  rt = (int32_t)tile;
+  return tile >= 0 && tile < a.tiles;
+}
+
 // 8 codes as fp16, exactly.
 __device__ __forceinline__ half8 codes8(uint32_t lo, uint32_t hi) {
   constexpr uint32_t k1024 = 0x64646464u;
@@ -64,7 +103,7 @@ struct Stage {
 // tile: 128 requests of up to 8192 tokens 346 -> 312, 32 of up to 4001 50.3 -> 44.3; two tiles that
 // read the same codes 34.6 -> 37.2, so not there).
 template <int D, int CT, bool ONCE, bool BF16>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kernel(Args a) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kernel(Args8 a) {
   constexpr int U = D / 64, E = D / 32, J = D / 16;
   constexpr int kStride = D + 4;  // floats of a row of partial outputs in LDS
   constexpr int kAll = CT * kCols;
@@ -386,7 +425,7 @@ __device__ __forceinline__ float halves_max(float v) {
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_many_kernel(Args a) {
+__global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_many_kernel(Args8 a) {
   using M = Many<D>;
   constexpr int U = M::U, E = D / 16, J = D / 32, R = M::kRuns;
   constexpr int kParts = BF16 ? 1 : 2;
@@ -394,8 +433,9 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
 
   const int lane = threadIdx.x & 63, n = lane & 31, c = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits, b = blockIdx.z;
-  const int32_t rt = a.tiles - 1 - (int32_t)blockIdx.y;
+  const int32_t h = blockIdx.x / a.splits, split = blockIdx.x - h * a.splits;
+  int32_t b = blockIdx.z, rt = a.tiles - 1 - (int32_t)blockIdx.y;
+  if (a.units && !find_tile<M::kRows>(a, (int64_t)blockIdx.z * gridDim.y + blockIdx.y, b, rt)) return;
   const Tile t = tile_of(a, b, h, rt);
   if (t.rows <= 0) return;
   const int32_t chunk = chunk_of(a, t), nchunks = chunks_of(t, chunk);
@@ -737,10 +777,40 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
   return k;
 }
 
+// A call whose largest request has kMany pairs or more may hold requests with few rows too (prompts
+// and decodes of one step).  Those up to few_pairs are left to a launch of their own with tiles
+// and chunks like a call of decodes, where the batch fills the CUs without them (below it they
+// find idle ones) and is uneven enough to pay for two more launches.  No tiles: there is none.
+int32_t few_pairs(int32_t group, int32_t dim) { return (dim == 256 ? 16 : 32) / group * group; }
+
+Cut few_of(int32_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len,
+           int32_t window) {
+  const int32_t group = hq / hkv, few = few_pairs(group, dim);
+  if ((int64_t)max_rows * group < kMany || !few || (int64_t)B * hkv < kCus || 2 * (int64_t)T >= (int64_t)B * max_rows)
+    return {0, 0, 1};
+  return cut_of(B, hq, hkv, dim, few / group, max_len, window);
+}
+
+int64_t parts_of(const Cut &k, int32_t B, int32_t hkv) { return (int64_t)B * k.tiles * hkv * k.splits; }
+size_t bytes_of(const Cut &k, int32_t B, int32_t hkv, int32_t dim) {
+  return k.splits == 1 ? 0 : (size_t)parts_of(k, B, hkv) * k.tile_rows * (dim + 2) * sizeof(float);
+}
+
 template <int D, bool BF16>
-void launch(const Args &a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
+void launch_cut(Args8 a, const Cut &k, hipStream_t s) {
+  a.tiles = k.tiles, a.tile_rows = k.tile_rows, a.splits = k.splits;
+  a.ws_ml = a.ws_o ? a.ws_o + parts_of(k, a.B, a.hkv) * k.tile_rows * D : nullptr;
+  dim3 grid((unsigned)(a.splits * a.hkv), (unsigned)a.tiles, (unsigned)a.B), threads(kThreads);
   if (a.tile_rows > 32) {
+    // Tiles by the rows of the call where that is fewer (20 requests of 1000 rows among 980 of one row over
+    // 2000 tokens: 1150 us; with tiles for each request and without `few` 8636; one of 2000 rows among
+    // 31: 152 and 572; two prompts of nearly equal rows 185 either way).
+    const int64_t units = (int64_t)a.T * a.group / a.tile_rows + a.B;
+    if (units < (int64_t)a.B * a.tiles) {
+      a.units = (int32_t)units;
+      grid.y = units < 32768 ? (unsigned)units : 32768u;
+      grid.z = (unsigned)((units + grid.y - 1) / grid.y);
+    }
     hipLaunchKernelGGL((kv8_many_kernel<D, BF16>), grid, dim3(Many<D>::kThreads), 0, s, a);
   } else if (D == 256) {  // 16-row tiles only
     if (a.tiles == 1) hipLaunchKernelGGL((kv8_attention_kernel<D, 1, true, BF16>), grid, threads, 0, s, a);
@@ -756,10 +826,20 @@ void launch(const Args &a, hipStream_t s) {
   launch_join<D, BF16>(a, s);
 }
 
+template <int D, bool BF16>
+void launch(Args8 a, const Cut &k, const Cut &few, hipStream_t s) {
+  const int32_t pairs = few.tiles ? few_pairs(a.group, D) : 0;
+  a.least = pairs + 1;
+  launch_cut<D, BF16>(a, k, s);
+  if (!pairs || hipPeekAtLastError() != hipSuccess) return;
+  a.least = 1, a.most = pairs, a.max_rows = pairs / a.group + 1;  // a row more tells the larger requests
+  launch_cut<D, BF16>(a, few, s);
+}
+
 template <int D>
-void launch(const Args &a, int32_t dtype, hipStream_t s) {
-  if (dtype == MIXLLM_BF16) launch<D, true>(a, s);
-  else launch<D, false>(a, s);
+void launch(const Args8 &a, const Cut &k, const Cut &few, int32_t dtype, hipStream_t s) {
+  if (dtype == MIXLLM_BF16) launch<D, true>(a, k, few, s);
+  else launch<D, false>(a, k, few, s);
 }
 
 }  // namespace
@@ -769,8 +849,9 @@ extern "C" size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int
                                                        int32_t window) {
   if (!shape_ok(T, B, q_heads, kv_heads, dim, max_rows, max_len, window) || T == 0 || B == 0 || max_rows == 0) return 0;
   const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
-  if (k.splits == 1) return 0;
-  return (size_t)B * k.tiles * kv_heads * k.splits * k.tile_rows * (dim + 2) * sizeof(float);
+  const Cut few = few_of(T, B, q_heads, kv_heads, dim, max_rows, max_len, window);
+  const size_t large = bytes_of(k, B, kv_heads, dim), small = bytes_of(few, B, kv_heads, dim);  // one after the other
+  return large > small ? large : small;
 }
 
 extern "C" int mixllm_kv8_attention(const void *q, int64_t ldq, int32_t dtype, int32_t T, int32_t q_heads,
@@ -788,21 +869,21 @@ extern "C" int mixllm_kv8_attention(const void *q, int64_t ldq, int32_t dtype, i
   const int bad = check_call(q, ldq, q_heads, dim, table, ldt, width, lens, cu, out, ldo, lse, workspace);
   if (bad != MIXLLM_OK) return bad;
   const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
-  const int64_t parts = (int64_t)B * k.tiles * kv_heads * k.splits;
-  if (parts > 0x7FFFFFFF || B > 65535 || k.tiles > 65535 || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
+  const Cut few = few_of(T, B, q_heads, kv_heads, dim, max_rows, max_len, window);
+  if (parts_of(k, B, kv_heads) > 0x7FFFFFFF || parts_of(few, B, kv_heads) > 0x7FFFFFFF || B > 65535 ||
+      k.tiles > 65535 || (int64_t)B * max_rows * q_heads > 0x7FFFFFFF)
     return MIXLLM_E_SHAPE;
-  float *ws = static_cast<float *>(workspace);
-  if (k.splits > 1) {
-    if (workspace_bytes < (size_t)parts * k.tile_rows * (dim + 2) * sizeof(float)) return MIXLLM_E_SPACE;
-    if (!ws) return MIXLLM_E_NULL;
-  }
-  const Args a = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(cache), table, lens, cu,
-                  static_cast<uint16_t *>(out), lse, ws, ws ? ws + parts * k.tile_rows * dim : nullptr,
-                  ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
-                  mixllm::log2_of(page), width, B, max_rows,
-                  max_len, window, k.tiles, k.tile_rows, k.splits};
-  if (dim == 64) launch<64>(a, dtype, (hipStream_t)stream);
-  else if (dim == 128) launch<128>(a, dtype, (hipStream_t)stream);
-  else launch<256>(a, dtype, (hipStream_t)stream);
+  const size_t large = bytes_of(k, B, kv_heads, dim), small = bytes_of(few, B, kv_heads, dim);
+  if (workspace_bytes < large || workspace_bytes < small) return MIXLLM_E_SPACE;
+  if ((large || small) && !workspace) return MIXLLM_E_NULL;
+  Args8 a;
+  static_cast<Args &>(a) = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(cache), table, lens, cu,
+                            static_cast<uint16_t *>(out), lse, static_cast<float *>(workspace), nullptr,
+                            ldq, ldo, ldt, scale, T, q_heads, kv_heads, q_heads / kv_heads, pages,
+                            mixllm::log2_of(page), width, B, max_rows, max_len, window, 0, 0, 1};
+  a.least = 0, a.most = INT32_MAX, a.units = 0;
+  if (dim == 64) launch<64>(a, k, few, dtype, (hipStream_t)stream);
+  else if (dim == 128) launch<128>(a, k, few, dtype, (hipStream_t)stream);
+  else launch<256>(a, k, few, dtype, (hipStream_t)stream);
   return mixllm::launch_status();
 }
