@@ -102,7 +102,8 @@ def test_sizes():
     assert ws(1, 1, 32, 8, 128, 1, 100000, 64) == ws(1, 1, 32, 8, 128, 1, 1000, 64)
     # 70 requests, one of many rows: room for two chunks of each of the others
     assert ws(400, 70, 8, 4, 64, 300, 600) == 70 * 4 * 2 * 32 * (64 + 2) * 4
-    assert ws(70 * 300, 70, 8, 4, 64, 300, 600) == 0
+    assert ws(70 * 300, 70, 8, 4, 64, 300, 600) == ws(400, 70, 8, 4, 64, 300, 600)  # serves calls of fewer rows
+    assert ws(400, 60, 8, 4, 64, 300, 600) == 0             # fewer requests stay in the one launch
     with pytest.raises(ValueError):
         L.kv8_cache(4, 20, 8, 128, device="cpu")
     assert L.kv8_cache(3, 16, 2, 64, device="cpu").shape == (3, 2, 2 * 16 * 64 + 128)

@@ -426,7 +426,7 @@ def test_a_replayed_call_of_prompts_among_single_rows(L):
     t, b = 300, 70
     q, cu, ln = torch.zeros(t, hq, dim, dtype=dtype, device="cuda"), i32([0] * (b + 1)), i32([0] * b)
     out, tab = torch.empty_like(q), cuda(table)
-    size = L.mixllm_kv8_attention_workspace_bytes(t, b, hq, hkv, dim, 260, 600)
+    size = L.mixllm_kv8_attention_workspace_bytes(b * 260, b, hq, hkv, dim, 260, 600)  # of the largest step
     ws = torch.empty(size, dtype=torch.uint8, device="cuda")
     assert size
     call = lambda: L.mixllm_kv8_attention(q, dev, tab, ln, cu, out, page, 260, 600, scale=0.1, workspace=ws)  # noqa: E731

@@ -849,7 +849,8 @@ extern "C" size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int
                                                        int32_t window) {
   if (!shape_ok(T, B, q_heads, kv_heads, dim, max_rows, max_len, window) || T == 0 || B == 0 || max_rows == 0) return 0;
   const Cut k = cut_of(B, q_heads, kv_heads, dim, max_rows, max_len, window);
-  const Cut few = few_of(T, B, q_heads, kv_heads, dim, max_rows, max_len, window);
+  // enough for calls of fewer rows too, whose batch may be uneven where this one is not
+  const Cut few = few_of(1, B, q_heads, kv_heads, dim, max_rows, max_len, window);
   const size_t large = bytes_of(k, B, kv_heads, dim), small = bytes_of(few, B, kv_heads, dim);  // one after the other
   return large > small ? large : small;
 }
