@@ -837,7 +837,8 @@ class PackedLinear:
 class RowLinear:
     """A layer wholly in 8 bits with one scale per output channel, its activations with one per
     token: ``forward(a)`` runs mixllm_quant_rows then mixllm_gemm_w8a8.  ``w``: [N, K] fp16 (or bf16,
-    as a tensor), quantized once on the GPU; ``dtype``: of the outputs, fp16 or bf16."""
+    as a tensor), quantized once on the GPU, which the constructor waits for; ``dtype``: of the
+    outputs, fp16 or bf16."""
 
     def __init__(self, w, device="cuda", dtype=None):
         w = torch.as_tensor(w).to(device)
@@ -846,6 +847,8 @@ class RowLinear:
         self.sw = torch.empty(self.n, dtype=torch.float32, device=device)
         self.device, self.dtype = device, dtype or torch.float16
         mixllm_quant_rows(w.contiguous(), self.w, self.sw)
+        if self.w.is_cuda:  # forward runs on any stream: the weights are there for all of them
+            torch.cuda.current_stream(self.w.device).synchronize()
 
     def buffers(self, m: int):
         dev = self.device
