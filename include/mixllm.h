@@ -529,7 +529,8 @@ int mixllm_kv8_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t 
  *
  * mixllm_quant_rows: per row m of a (a token's activations, or an output channel's weights)
  *   s[m] = max |a[m]| / 127,  q[m][k] = clamp(rne(a[m][k] / s[m]), -127, 127)
- * in fp32 with IEEE divisions; s = 0 and q = 0 for a row of zeros.
+ * in fp32 with IEEE divisions; s = 0 and q = 0 for a row of zeros, s = NaN (so that its outputs
+ * are NaN) and q = 0 for a row with a NaN or an infinity.
  * a_dev: [M][lda] of dtype (MIXLLM_FP16 or MIXLLM_BF16), lda % 8 == 0; q_dev: int8 [M][ldq],
  * ldq % 16 == 0; s_dev: fp32 [M].  K % 16 == 0, K <= 131072, M below 2^22.
  *

@@ -117,12 +117,15 @@ def kv8_values(cache, slots, page, dim):
 # ----------------------------------------------------------------------- the linear layer
 
 def quant_rows(a):
-    """Codes and scales of the rows of a (float32 values), in fp32 steps."""
+    """Codes and scales of the rows of a (float32 values), in fp32 steps; a row with a NaN or an
+    infinity has a scale of NaN and codes of 0."""
     a = np.asarray(a, np.float32)
+    a = np.where(np.isfinite(a).all(1)[:, None], a, np.float32(np.nan))
     s = np.abs(a).max(1) / np.float32(127)
     with np.errstate(divide="ignore", invalid="ignore"):
         q = np.rint(a / s[:, None])
-    return np.where(s[:, None] > 0, np.clip(q, -127, 127), 0).astype(np.int8), s
+        q = np.where(s[:, None] > 0, np.clip(q, -127, 127), 0)
+    return q.astype(np.int8), s
 
 
 def gemm_w8a8(aq, sa, w, sw):

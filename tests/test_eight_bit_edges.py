@@ -1,8 +1,9 @@
-"""Calls at the edges of what the 8-bit operators allow."""
+"""Calls at the edges of what the 8-bit operators allow: streams, rows that hold no number."""
 import numpy as np
 import pytest
 
 from oracle import eight_bit_oracle as E
+from tests import gpu_util as U
 from tests import test_gpu_gemm8 as G
 from tests.test_gpu_kv4 import cuda, rounded
 
@@ -38,3 +39,39 @@ def test_a_layer_used_on_another_stream_at_once(L, times):
     s.synchronize()
     assert np.array_equal(layer.w.cpu().numpy(), wq) and np.array_equal(layer.sw.cpu().numpy(), sw)
     G.check(y, aq, sa, wq, sw, torch.float16)
+
+
+def test_rows_without_numbers_by_hand():
+    q, s = E.quant_rows([[1, np.nan, -2], [np.inf, 0, 1], [1, -np.inf, np.nan], [-2, 1, 0]])
+    assert np.isnan(s[:3]).all() and not q[:3].any()
+    assert s[3] == np.float32(2) / np.float32(127) and q[3].tolist() == [-127, 64, 0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("m,k", [(9, 16), (9, 1040), (9, 4096), (9, 8208), (9, 16400), (9, 40000), (1030, 2032), (1030, 4096)])
+def test_a_row_that_holds_no_number(L, m, k, dtype):
+    """NaN or an infinity anywhere in a row: its scale is NaN and its codes are 0, so its outputs are
+    NaN, and no other row's."""
+    U.say("quant rows, none", m, k, dtype)
+    rng = np.random.default_rng(k)
+    a = rounded(rng.normal(size=(m, k)).astype(np.float32), dtype)
+    a[1, 0], a[2, k - 1], a[3, k // 2], a[m - 1, 15] = np.nan, np.inf, -np.inf, np.nan
+    a[5], a[6, ::3], a[7] = np.nan, -np.inf, 0.0
+    largest = float(torch.finfo(dtype).max)
+    a[0, 3] = largest                                          # a number, if the largest
+    q = torch.full((m, k), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((m,), 9.0, device="cuda")
+    L.mixllm_quant_rows(cuda(a, dtype), q, s)
+    want_q, want_s = E.quant_rows(a)
+    bad = [1, 2, 3, 5, 6, m - 1]
+    assert np.isnan(want_s[bad]).all() and np.isfinite(np.delete(want_s, bad)).all()
+    assert np.array_equal(s.cpu().numpy(), want_s, equal_nan=True)
+    assert np.array_equal(q.cpu().numpy(), want_q)
+    w, sw = cuda(rng.integers(-127, 128, (33, k)).astype(np.int8)), torch.full((33,), 1e-6, device="cuda")
+    sw[4] = 0.0
+    y = torch.empty((m, 33), dtype=torch.bfloat16, device="cuda")
+    L.mixllm_gemm_w8a8(q, s, w, sw, y)
+    ok = torch.ones(m, dtype=torch.bool)
+    ok[bad] = False
+    assert y[~ok.cuda()].isnan().all() and y[ok.cuda()].isfinite().all()

@@ -24,6 +24,7 @@ using mixllm::up;
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------------- the quantizer
 
@@ -48,16 +49,23 @@ struct Values {
     const uint32_t w = j % 8 / 2 == 0 ? r.x : j % 8 / 2 == 1 ? r.y : j % 8 / 2 == 2 ? r.z : r.w;
     return up<BF16>(w >> (16 * (j % 2)) & 0xFFFFu);
   }
+  // By the magnitudes' bits, among which those of infinities and NaN are above all others; a
+  // maximum of floats would pass over NaN.  Both come out as the infinity.
   template <bool BF16>
   __device__ __forceinline__ float top() const {
-    float t = 0.0f;
+    ushort2v t = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) t = fmaxf(t, fabsf(at<BF16>(j)));
-    return t;
+    for (int j = 0; j < 8; ++j) {
+      const uint4 &r = raw[j / 4];
+      const uint32_t w = j % 4 == 0 ? r.x : j % 4 == 1 ? r.y : j % 4 == 2 ? r.z : r.w;
+      t = __builtin_elementwise_max(t, __builtin_bit_cast(ushort2v, w & 0x7FFF7FFFu));
+    }
+    const uint32_t bits = t.x > t.y ? t.x : t.y;
+    return bits < (BF16 ? 0x7F80u : 0x7C00u) ? up<BF16>(bits) : INFINITY;
   }
   // rne(x / s) by the reciprocal r of s: x r is within 6e-5 of the quotient (|x / s| <= 127), so
   // it rounds to the same number unless it lies within 2^-12 of a half; those divide, and so do
-  // all where s is so small that r may not be a number (r = NaN).
+  // all where s is so small that r may not be a number (r = NaN).  A scale of NaN gives codes of 0.
   template <bool BF16>
   __device__ __forceinline__ uint4 codes(float s, float r) const {
     uint32_t w[4] = {0, 0, 0, 0};
@@ -90,6 +98,9 @@ __device__ __forceinline__ float row_top(float top, float *tops) {
   return top;
 }
 
+// A row that holds no number somewhere has none as its scale, and so in all its outputs.
+__device__ __forceinline__ float scale_of(float top) { return top < INFINITY ? top / 127.0f : NAN; }
+
 __device__ __forceinline__ float inverse(float s) { return s >= 0x1p-100f ? __builtin_amdgcn_rcpf(s) : NAN; }
 
 // A workgroup takes a row, 16 values a thread and chunk, held in registers between the maximum
@@ -111,7 +122,7 @@ __global__ __launch_bounds__(THREADS) void quant_rows_kernel(RowsArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) top = fmaxf(top, v[c].template top<BF16>());
-    const float s = row_top<THREADS>(top, tops) / 127.0f, r = inverse(s);
+    const float s = scale_of(row_top<THREADS>(top, tops)), r = inverse(s);
     if (threadIdx.x == 0) a.s[m] = s;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
@@ -123,7 +134,7 @@ __global__ __launch_bounds__(THREADS) void quant_rows_kernel(RowsArgs a) {
       v.load(src + e);
       top = fmaxf(top, v.template top<BF16>());
     }
-    const float s = row_top<THREADS>(top, tops) / 127.0f, r = inverse(s);
+    const float s = scale_of(row_top<THREADS>(top, tops)), r = inverse(s);
     if (threadIdx.x == 0) a.s[m] = s;
     for (int32_t e = first; e < a.K; e += THREADS * 16) {
       v.load(src + e);

@@ -756,7 +756,7 @@ def mixllm_kv8_attention(q, cache, table, lens, cu, out, page: int, max_rows: in
 
 def mixllm_quant_rows(a, q, s, stream=None):
     """Quantizes the rows of a ([M, K] fp16 or bf16, rows may be strided) to q (int8 [M, K]) with
-    one scale per row in s (fp32 [M])."""
+    one scale per row in s (fp32 [M]; NaN, with codes of 0, for a row with a NaN or an infinity)."""
     if a.dim() != 2:
         raise ValueError(f"a must be [M, K], is {tuple(a.shape)}")
     m, k = shape = a.shape
