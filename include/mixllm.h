@@ -504,7 +504,8 @@ int mixllm_kv8_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  * mixllm_kv4_attention, its workspace mixllm_kv8_attention_workspace_bytes(..).
  *   A weight times a value's scale is held to 2^-22 of itself and to 2^-33 of the row's largest
  *   one (2^-11 for bf16 where max_rows * q_heads / kv_heads is 128 or more).  The scales of values
- *   that a row sees are to lie within a factor of 2^60 of one another, or be 0.
+ *   that a row sees are to lie within a factor of 2^60 of one another, or be 0 (past that an output
+ *   may lose what small weights of large values add to it; lse and what is divided by hold).
  *   bf16 values of q 2^-38 below the row's largest count as 0.
  *   Scores have fp32's range, with the bounds of mixllm_kv4_attention; a row that passes them
  *   (or holds no number) spoils no other row.

@@ -1,10 +1,13 @@
-"""Calls at the edges of what the 8-bit operators allow: streams, rows that hold no number."""
+"""Calls at the edges of what the 8-bit operators allow: streams, rows that hold no number, values whose
+scales are far apart."""
 import numpy as np
 import pytest
 
 from oracle import eight_bit_oracle as E
 from tests import gpu_util as U
 from tests import test_gpu_gemm8 as G
+from tests import test_gpu_kv4 as K
+from tests import test_gpu_kv8 as V
 from tests.test_gpu_kv4 import cuda, rounded
 
 torch = pytest.importorskip("torch")
@@ -75,3 +78,23 @@ def test_a_row_that_holds_no_number(L, m, k, dtype):
     ok = torch.ones(m, dtype=torch.bool)
     ok[bad] = False
     assert y[~ok.cuda()].isnan().all() and y[ok.cuda()].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [-40, -75, -110, -125, -133])
+@pytest.mark.parametrize("rows", [1, 9, 40])
+def test_values_whose_scales_are_far_apart(L, apart, rows):
+    """Every second run's values are 2^apart of the others': they count as next to nothing in the
+    outputs, and in full in what the outputs are divided by."""
+    dim, page, dtype, lens = 128, 16, torch.bfloat16, [300, 200]
+    U.say("attention8 scales apart", apart, rows)
+
+    def kv(t, heads, d, dt, seed):
+        k, v = K.key_values(t, heads, d, dt, seed)
+        v = np.where(np.arange(t)[:, None, None] // 16 % 2, v.astype(np.float64) * 2.0 ** apart, v)
+        return k, rounded(v.astype(np.float32), dt)
+
+    dev, table, vals = V.build(lens, 2, dim, page, dtype, 71, kv=kv)
+    q = V.queries(2 * rows, 8, dim, dtype, 17)
+    out, lse = V.attend(L, q, dev, table, lens, [rows] * 2, page, dtype, 0.09)
+    K.compare(out, lse, q, vals, lens, [rows] * 2, dtype, 0.09)

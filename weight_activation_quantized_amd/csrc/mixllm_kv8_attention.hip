@@ -451,6 +451,9 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
   // Pages and scales of kBatch steps at a time, a run a lane.  A value's scale is 2^(ve + lv), its inverse
   // iv 2^-ve; values of nothing but zeros have ve = kNone and count as with a scale of 1.
   constexpr int32_t kNone = -1000;
+  // Exponents of a scale below the row's are taken as this one: weights (up to 2^kLazy) times scales
+  // are 0 in fp16 from here on anyway, and their sum stays where the factor taken back from it is finite.
+  constexpr int32_t kLeast = -32;
   struct Batch {
     int32_t pages, ve;
     float ks, lv, iv;
@@ -668,7 +671,7 @@ __global__ __launch_bounds__(Many<D>::kThreads, Many<D>::kWaves / 4) void kv8_ma
     // weights'.
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int32_t d = ve[r] == kNone ? 0 : ve[r] - shift;
+      const int32_t below = ve[r] - shift, d = ve[r] == kNone ? 0 : below > kLeast ? below : kLeast;
       const float add = (of_run(now.lv, r) + (float)d) - ref;
       float sum = 0.0f;
 #pragma unroll
