@@ -209,11 +209,6 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-template <int N>
-struct Const {
-  static constexpr int value = N;
-};
-
 // Many tokens: a workgroup takes BM tokens x BN channels.  Stages of BK inputs of both go from
 // memory to LDS, ST - 1 of them in flight; WM x WN waves share the tile, KS such groups the
 // inputs of a stage.  A stage has its rows one after the other, their 16-byte chunks turned by

@@ -815,15 +815,14 @@ void launch_cut(Args8 a, const Cut &k, hipStream_t s) {
       grid.z = (unsigned)((units + grid.y - 1) / grid.y);
     }
     hipLaunchKernelGGL((kv8_many_kernel<D, BF16>), grid, dim3(Many<D>::kThreads), 0, s, a);
-  } else if (D == 256) {  // 16-row tiles only
-    if (a.tiles == 1) hipLaunchKernelGGL((kv8_attention_kernel<D, 1, true, BF16>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((kv8_attention_kernel<D, 1, D != 256, BF16>), grid, threads, 0, s, a);
-  } else if (a.tile_rows == 16) {
+  } else if (a.tile_rows == 16 && a.tiles == 1) {
     hipLaunchKernelGGL((kv8_attention_kernel<D, 1, true, BF16>), grid, threads, 0, s, a);
+  } else if constexpr (D == 256) {  // tiles of 16 rows only
+    hipLaunchKernelGGL((kv8_attention_kernel<D, 1, false, BF16>), grid, threads, 0, s, a);
   } else if (a.tiles == 1) {
-    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, true, BF16>), grid, threads, 0, s, a);
+    hipLaunchKernelGGL((kv8_attention_kernel<D, 2, true, BF16>), grid, threads, 0, s, a);
   } else {
-    hipLaunchKernelGGL((kv8_attention_kernel<D, D < 256 ? 2 : 1, false, BF16>), grid, threads, 0, s, a);
+    hipLaunchKernelGGL((kv8_attention_kernel<D, 2, false, BF16>), grid, threads, 0, s, a);
   }
   if (a.splits == 1 || hipPeekAtLastError() != hipSuccess) return;
   launch_join<D, BF16>(a, s);
