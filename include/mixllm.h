@@ -442,7 +442,7 @@ int mixllm_kv4_attention(const void *q_dev, int64_t ldq, int32_t dtype, int32_t 
  *               of no heads.
  * pos_dev:      int32 [T], inv_freq_dev: fp32 [rot / 2] (both may be NULL for rot 0).
  * q_norm_dev, k_norm_dev: [dim] of dtype, or NULL for no norm.
- * dim, rot even, dim <= 512, 0 <= rot <= dim; T below 2^24 and T * heads below 2^26.
+ * dim, rot even, dim <= 512, 0 <= rot <= dim; T below 2^24 and T * heads at most 2^26 - 4.
  * Any stride and element-aligned pointer; dim % 16 == 0, rot % 16 == 0, strides % 8 == 0 and
  * 16-byte aligned pointers run faster.
  * Errors: E_NULL, E_SHAPE, E_HIP.

@@ -1,5 +1,5 @@
 """Calls at the edges of what the 8-bit operators allow: streams, rows that hold no number, values whose
-scales are far apart."""
+scales are far apart, sizes past a launch."""
 import numpy as np
 import pytest
 
@@ -8,7 +8,9 @@ from tests import gpu_util as U
 from tests import test_gpu_gemm8 as G
 from tests import test_gpu_kv4 as K
 from tests import test_gpu_kv8 as V
+from tests.test_eight_bit_host import ROTATE
 from tests.test_gpu_kv4 import cuda, rounded
+from tests.test_serving_host import SHAPE, call
 
 torch = pytest.importorskip("torch")
 
@@ -98,3 +100,12 @@ def test_values_whose_scales_are_far_apart(L, apart, rows):
     q = V.queries(2 * rows, 8, dim, dtype, 17)
     out, lse = V.attend(L, q, dev, table, lens, [rows] * 2, page, dtype, 0.09)
     K.compare(out, lse, q, vals, lens, [rows] * 2, dtype, 0.09)
+
+
+@pytest.mark.parametrize("t,heads", [(24573, 2731), (1082401, 62), (1 << 20, 64), (671089, 100)])
+def test_more_heads_of_tokens_than_one_launch_has_threads(t, heads):
+    """From 2^26 - 3 on the last workgroup would be the launch's 2^32nd thread."""
+    assert t * heads > (1 << 26) - 4
+    lib = pytest.importorskip("weight_activation_quantized_amd.mixllm").library_handle()
+    wide = heads * 50
+    assert call(lib.mixllm_head_norm_rotate, ROTATE, t=t, hq=heads - 1, hkv=1, dim=50, rot=50, ldq=wide, ldqo=wide) == SHAPE

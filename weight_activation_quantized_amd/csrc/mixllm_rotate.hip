@@ -276,8 +276,8 @@ extern "C" int mixllm_head_norm_rotate(const void *q, int64_t ldq, const void *k
       !(eps >= 0.0f) || q_heads > 65535 || kv_heads > 65535)
     return MIXLLM_E_SHAPE;
   const int32_t heads = q_heads + kv_heads;
-  // a launch has fewer than 2^32 threads: 64 at most for a head of a token
-  if (T >= 1 << 24 || (int64_t)T * heads >= 1 << 26) return MIXLLM_E_SHAPE;
+  // a launch has fewer than 2^32 threads: 64 at most for a head of a token, in whole workgroups of 4
+  if (T >= 1 << 24 || (int64_t)T * heads > (1 << 26) - 4) return MIXLLM_E_SHAPE;
   if (T == 0 || heads == 0) return MIXLLM_OK;
   if ((q_heads && (!q || !q_out)) || (kv_heads && (!k || !k_out)) || (rot && (!pos || !inv_freq)) ||
       (!q_heads && q_norm) || (!kv_heads && k_norm))
