@@ -511,7 +511,8 @@ int mixllm_kv8_read(const void *cache_dev, size_t cache_bytes, int32_t pages, in
  *   (or holds no number) spoils no other row.
  *   Prompts and single tokens may share a call: where max_rows * q_heads / kv_heads is 128 or more,
  *   B * kv_heads 256 or more and T less than half of B * max_rows, requests of up to 32 rows and
- *   heads per key/value head (16 with dim 256) are taken by one or two launches of their own.
+ *   heads per key/value head (16 with dim 256) are taken by one or two launches of their own.  Elsewhere
+ *   single tokens over long contexts are faster in a call of their own.
  *   A workspace for T rows serves calls of fewer rows.
  */
 size_t mixllm_kv8_attention_workspace_bytes(int32_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t dim,

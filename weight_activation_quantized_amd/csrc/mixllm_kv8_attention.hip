@@ -19,12 +19,12 @@
 // two per row that follows the largest such product (`shift`), so that rows whose large
 // values hardly count lose nothing; what the rounding leaves is a second operand (error of fp16
 // outputs 1.0 times that of their own rounding; bf16 prompts, whose rounding is 8 times coarser, go
-// without: 143 us for 2 x 1024 rows, where fp16 takes 182).  Statistics, sums and outputs are fp32.
+// without: 145 us for 2 x 1024 rows, where fp16 takes 183 - 190).  Statistics, sums and outputs are fp32.
 //
 // What bounds it, at 128 channels.  Decodes: the cache's bytes, 128 requests of up to 8192 tokens 1.68 GB
 // in 312 us, 5.4 TB/s (a large read reaches 5.9), one of 131071 tokens 269 MB in 45.7 us and 6 for the
-// join; small ones latency (77 tokens 5.8 us).  Prompts (2 x 1024 rows over 4096 tokens: 600 TFLOP/s in
-// fp16, 770 in bf16, where a large library product reaches 1176): the softmax, whose 250 vector
+// join; small ones latency (77 tokens 5.8 us).  Prompts (2 x 1024 rows over 4096 tokens: 590 TFLOP/s in
+// fp16, 750 in bf16, where a large library product reaches 1176): the softmax, whose 250 vector
 // operations a step one wave of a SIMD issues at about 7 cycles each while the other multiplies:
 // 1800 - 2350 cycles of the weighing phase to 1000 - 1500 of matrix instructions.
 #include <hip/hip_runtime.h>
@@ -101,7 +101,8 @@ struct Stage {
 // CT: column blocks of 16 rows that share the operands made of codes.  ONCE: one tile holds all rows of
 // a request and head, so a code is read once and its line need not stay in the caches (us, one
 // tile: 128 requests of up to 8192 tokens 346 -> 312, 32 of up to 4001 50.3 -> 44.3; two tiles that
-// read the same codes 34.6 -> 37.2, so not there).
+// read the same codes 34.6 -> 37.2, so not there; requests whose tables name the same pages read them
+// past the caches too, 128 over the same 8192 tokens 166.5 -> 167).
 template <int D, int CT, bool ONCE, bool BF16>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv8_attention_kernel(Args8 a) {
   constexpr int U = D / 64, E = D / 32, J = D / 16;
@@ -783,7 +784,9 @@ Cut cut_of(int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, in
 // A call whose largest request has kMany pairs or more may hold requests with few rows too (prompts
 // and decodes of one step).  Those up to few_pairs are left to a launch of their own with tiles
 // and chunks like a call of decodes, where the batch fills the CUs without them (below it they
-// find idle ones) and is uneven enough to pay for two more launches.  No tiles: there is none.
+// find idle ones) and is uneven enough to pay for two more launches.  No tiles: there is none.  In a
+// smaller batch a long decode beside a prompt is walked by one workgroup a head: 15 over 32768 tokens
+// take 183 us, a prompt of 1000 rows 84, both in one call 1016.
 int32_t few_pairs(int32_t group, int32_t dim) { return (dim == 256 ? 16 : 32) / group * group; }
 
 Cut few_of(int32_t T, int32_t B, int32_t hq, int32_t hkv, int32_t dim, int32_t max_rows, int32_t max_len,

@@ -188,7 +188,8 @@ constexpr int32_t kMaxDim = 512;
 constexpr int32_t kEnoughWaves = 4096;
 
 // Any even number of channels and element-aligned rows: a wave takes one head, a lane single
-// pairs of it.
+// pairs of it, whose angles it forms for every head again: 8191 tokens x 72 heads of 128 take 237 us with
+// 40 channels turned, where the kernel above takes 53 with all.  For shapes that no model here has.
 template <bool BF16, bool NEXT>
 __global__ __launch_bounds__(256) void rotate_any_kernel(RotateArgs a) {
   constexpr int kPairs = kMaxDim / 2 / 64;
