@@ -1,5 +1,7 @@
 """Calls at the edges of what the 8-bit operators allow: streams, rows that hold no number, values whose
 scales are far apart, sizes past a launch."""
+import contextlib
+
 import numpy as np
 import pytest
 
@@ -109,3 +111,53 @@ def test_more_heads_of_tokens_than_one_launch_has_threads(t, heads):
     lib = pytest.importorskip("weight_activation_quantized_amd.mixllm").library_handle()
     wide = heads * 50
     assert call(lib.mixllm_head_norm_rotate, ROTATE, t=t, hq=heads - 1, hkv=1, dim=50, rot=50, ldq=wide, ldqo=wide) == SHAPE
+
+
+@pytest.mark.parametrize("kind", ["packed", "rows"])
+def test_buffers_of_a_call_are_the_streams(monkeypatch, kind):
+    """A call without buffers makes them while its stream is the current one, so that what it frees on
+    return is reused behind its work only."""
+    lib = pytest.importorskip("weight_activation_quantized_amd.mixllm")
+    for name in ("mixllm_quant_act", "mixllm_gemm_w4w8a8", "mixllm_quant_rows", "mixllm_gemm_w8a8"):
+        monkeypatch.setattr(lib, name, lambda *a, **k: None)
+    now, made = [None], []
+
+    @contextlib.contextmanager
+    def current(stream, dev):
+        now[0] = stream
+        yield
+        now[0] = None
+
+    monkeypatch.setattr(lib, "_current", current)
+    w = np.zeros((64, 256), np.float16)
+    layer = lib.RowLinear(w, "cpu") if kind == "rows" else lib.PackedLinear(w, [3], "cpu")
+    own = layer.buffers
+    monkeypatch.setattr(layer, "buffers", lambda m: made.append(now[0]) or own(m))
+    a = torch.zeros((5, 256), dtype=torch.float16)
+    layer.forward(a, stream="a stream")
+    layer.forward(a)
+    layer.forward(a, own(5), "another")
+    assert made == ["a stream", None]
+
+
+@pytest.mark.gpu
+def test_memory_of_a_call_is_not_given_away_before_it_ran(L):
+    """Work that the current stream does while a layer waits on its own stream leaves the layer's codes alone."""
+    rng = np.random.default_rng(5)
+    w = rounded(rng.normal(size=(512, 2048)).astype(np.float32), torch.float16)
+    layer, a = L.RowLinear(torch.from_numpy(w).half()), cuda(rng.normal(size=(64, 2048)).astype(np.float32), torch.float16)
+    aq, sa = E.quant_rows(a.float().cpu().numpy())
+    wq, sw = E.quant_rows(w)
+    s, busy = torch.cuda.Stream(), torch.ones((4096, 4096), device="cuda")
+    for _ in range(3):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            work = busy
+            for _ in range(10):
+                work = (work @ busy).clamp_(max=1.0)
+        y = layer.forward(a, stream=s)
+        others = [torch.full((64, 2048), 77, dtype=torch.int8, device="cuda") for _ in range(8)]
+        others += [torch.full((64,), 1e9, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        G.check(y, aq, sa, wq, sw, torch.float16)
+        assert all(bool((x == (77 if x.dtype == torch.int8 else 1e9)).all()) for x in others)

@@ -791,6 +791,13 @@ def _same_rows(bufs, m):
         raise ValueError(f"the buffers are for {bufs['aq'].shape[0]} rows, the input has {m} rows")
 
 
+def _own_buffers(layer, a, stream):
+    """A layer's buffers for one call on ``stream``, from that stream's memory: freed when the call
+    returns they wait for its work, where those of another stream could be given away before."""
+    with _current(stream, a.device):
+        return layer.buffers(a.shape[0])
+
+
 class PackedLinear:
     """A packed layer resident on the GPU plus the buffers one forward pass needs.
 
@@ -820,7 +827,7 @@ class PackedLinear:
 
     def forward(self, a, bufs=None, stream=None):
         m = a.shape[0]
-        bufs = bufs or self.buffers(m)
+        bufs = bufs or _own_buffers(self, a, stream)
         _same_rows(bufs, m)
         mixllm_quant_act(a, bufs["aq"], bufs["sa"], bufs["asum"], bufs["rowop"], stream)
         return self.gemm(bufs, stream, m)
@@ -858,7 +865,7 @@ class RowLinear:
 
     def forward(self, a, bufs=None, stream=None):
         m = a.shape[0]
-        bufs = bufs or self.buffers(m)
+        bufs = bufs or _own_buffers(self, a, stream)
         _same_rows(bufs, m)
         if m:
             mixllm_quant_rows(a, bufs["aq"], bufs["sa"], stream)
